@@ -606,6 +606,136 @@ qr_status_t qr_fp4_twoshot_peer_decode(qr_dtype_t dtype, int R, size_t n, const 
 qr_status_t qr_fp4_allreduce(qr_dtype_t dtype, int R, const void *const *x,
                              size_t n, void *y, int ctas, qr_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving operators: what runs on each tensor-parallel rank before its
+ * message is all-reduced -- attention over a paged key/value cache held in
+ * 8 bits, and matrix-vector products with 4-bit weights.
+ *
+ * The cache.  A block holds block_size consecutive tokens of one request for
+ * every key/value head; keys and values are int8 codes, one fp32 scale for
+ * each (block, head), and value = code * scale.  The arithmetic is the
+ * symmetric codec's at INT8 with the scale kept in fp32:
+ *   A = max|x| over the tokens of the block that one call writes,
+ *   s = max(s_old, A / 128)   (s_old = 0 when the call writes the block's
+ *                              first token; exact), r = fp32_RN(1/s), 0 if s = 0,
+ *   code = round_half_even(clip(fp32_RN(x*r), -128, 127)),
+ *   and when s > s_old the codes already in the block become
+ *   round_half_even(clip(fp32_RN(fp32_RN(code*s_old) * r), -128, 127)).
+ * Inputs must be finite; a non-finite key or value leaves the codes and the
+ * scale of its own (block, head) unspecified and touches nothing else.
+ *
+ * Codes are [blocks][heads][block_size][head_dim] with each head's tokens
+ * contiguous; the strides between blocks and heads are the caller's (so the
+ * two halves may be slices of one buffer).  head_dim is a multiple of 16 up
+ * to 256; block_size 16, 32, 64, 128 or 256; heads and blocks at least 1.
+ * A token's slot is block * block_size + (its position % block_size).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void *k_codes, *v_codes;                 /* int8, 16-byte aligned           */
+    float *k_scales, *v_scales;              /* [blocks][heads], contiguous     */
+    int64_t k_block_stride, k_head_stride;   /* bytes, multiples of 16          */
+    int64_t v_block_stride, v_head_stride;
+    int blocks, heads, block_size, head_dim;
+} qr_kv_cache_t;
+
+/* Block tables and slots of a step, from the requests' lengths (device
+ * int32 arrays).  Request r holds cached_lens[r] tokens and brings
+ * new_lens[r] more (negative counts as 0).  Its table row
+ * block_table[r*table_width ...] already names the blocks of the cached
+ * tokens; the blocks it needs beyond those are taken from free_blocks in
+ * request order (r's first new block is free_blocks[sum over j < r of the
+ * blocks that j takes]) and written into the row; other entries are left
+ * alone.  Writes, all on the device:
+ *   q_offsets[0..requests]  exclusive sums of the new lengths (clipped to
+ *                           max_tokens);
+ *   kv_lens[r]              cached + new;
+ *   slots[0..max_tokens)    the slot of every new token, request after
+ *                           request; -1 past the last, and for a token
+ *                           without a block (free list or row exhausted);
+ *   counts[0..3]            blocks taken, new tokens, blocks that were
+ *                           needed beyond num_free, table entries that were
+ *                           needed beyond table_width.
+ * counts[2] and counts[3] are 0 in a step that fitted.  free_blocks may be
+ * NULL when num_free is 0; slots when max_tokens is 0.  int32 arrays 4-byte,
+ * slots 8-byte aligned.  requests <= 65536. */
+qr_status_t qr_kv_plan(int requests, const int32_t *cached_lens, const int32_t *new_lens,
+                       int block_size, const int32_t *free_blocks, int num_free,
+                       int32_t *block_table, int table_width, int32_t *q_offsets,
+                       int32_t *kv_lens, int64_t *slots, int64_t max_tokens,
+                       int32_t *counts, qr_stream_t stream);
+
+/* Writes the keys and values of `tokens` tokens into the cache at slots[]
+ * (device int64; a slot outside the cache, such as -1, skips its token).
+ * k and v are fp16/bf16 [tokens][heads][head_dim] with token and head
+ * strides in values (multiples of 8; 16-byte aligned pointers).  Tokens of
+ * one block are consecutive in the arrays with consecutive slots, each block
+ * occurring in one such run, as qr_kv_plan lays them out: the run's first
+ * slot says how many tokens the block already holds. */
+qr_status_t qr_kv_append(qr_dtype_t dtype, int64_t tokens, const void *k, const void *v,
+                         int64_t k_token_stride, int64_t k_head_stride,
+                         int64_t v_token_stride, int64_t v_head_stride,
+                         const int64_t *slots, const qr_kv_cache_t *cache,
+                         qr_stream_t stream);
+
+/* Attention of ragged queries over the cache.  Query token t of request r
+ * (q_offsets[r] <= t < q_offsets[r+1], device int32) is the
+ * (t - q_offsets[r])-th of n_r = q_offsets[r+1] - q_offsets[r] and stands at
+ * position p = kv_lens[r] - n_r + (t - q_offsets[r]); query head j reads
+ * key/value head j / (q_heads / heads).  It sees the keys
+ *   0 <= i < kv_lens[r],  i <= p if causal,  i > p - window if window > 0
+ * (window only with causal), whose block-table entry names a block of the
+ * cache (others are masked, and never read):
+ *   S_i = scale * k_scale * sum_d q_d kcode_id,  P = softmax(S),
+ *   out = sum_i P_i v_scale vcode_i,  lse = log(sum_i exp(S_i)).
+ * A query that sees nothing gives out = 0, lse = -inf.  kv_lens above
+ * table_width * block_size count as that.  q and out are fp16/bf16
+ * [tokens][q_heads][head_dim], token and head strides in values (multiples
+ * of 8; 16-byte aligned); lse (may be NULL) is fp32 [tokens][q_heads].
+ * Tokens past q_offsets[requests] are left alone.  max_q is the caller's
+ * bound on the n_r (it picks the kernel; results do not depend on it).
+ * Products are exact in fp32 accumulation: codes as fp16 integers, queries
+ * as fp16 after an exact power-of-two scaling of each row (values more than
+ * 2^-28 below their row's largest lose bits); softmax weights are rounded to
+ * fp16 for the second product; statistics and sums are fp32.
+ * The workspace (qr_kv_attention_workspace_bytes, 16-byte aligned) must be
+ * zeroed once before its first use; every call leaves it ready for the next
+ * one on the same stream. */
+size_t qr_kv_attention_workspace_bytes(int requests, int64_t tokens, int q_heads, int heads,
+                                       int head_dim);      /* 0 if unsupported */
+qr_status_t qr_kv_attention(qr_dtype_t dtype, int requests, int64_t tokens, int q_heads,
+                            const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                            const int32_t *q_offsets, const int32_t *kv_lens,
+                            const int32_t *block_table, int table_width,
+                            const qr_kv_cache_t *cache, float scale, int causal, int window,
+                            int max_q, void *out, int64_t out_token_stride,
+                            int64_t out_head_stride, float *lse, void *workspace,
+                            size_t workspace_bytes, qr_stream_t stream);
+
+/* 4-bit weights [rows][cols]: w = (u - z) * s with a code u of 0..15, an fp16
+ * scale s and a zero point z of 0..15 (8 without zero points) for each group
+ * of 32, 64 or 128 consecutive columns (the last group may be short).
+ * qr_w4_pack lays codes (row-major, two to a byte, the even column in the
+ * low nibble, rows of ceil(cols/2) bytes), scales and zeros (row-major,
+ * [rows][ceil(cols/group)]; zeros NULL for the symmetric form) out in the
+ * matrix instructions' order; qr_w4_quantize does so from fp16/bf16 weights
+ * with the INT4 codec's arithmetic on each group (symmetric; for group 32
+ * the codes and scales of qr_encode(4, ...)).  The packed buffer
+ * (qr_w4_bytes, 16-byte aligned) is read by qr_w4_matvec only. */
+size_t qr_w4_bytes(int rows, int cols, int group, int has_zeros); /* 0 if unsupported */
+qr_status_t qr_w4_pack(int rows, int cols, int group, const uint8_t *codes, const void *scales,
+                       const uint8_t *zeros, void *packed, qr_stream_t stream);
+qr_status_t qr_w4_quantize(qr_dtype_t dtype, int rows, int cols, int group, const void *w,
+                           int64_t w_row_stride, void *packed, qr_stream_t stream);
+
+/* y[m][n] = sum_k x[m][k] w[n][k] for `tokens` rows of x: fp16/bf16 in and
+ * out, row strides in values, accumulated in fp32 (codes and zero points
+ * enter the products as exact integers, scales in fp32) and rounded once.
+ * Made for few tokens; any number is served.  x and y 2-byte aligned, any
+ * stride of at least a row; 16-byte aligned rows of x are read faster. */
+qr_status_t qr_w4_matvec(qr_dtype_t dtype, int64_t tokens, const void *x, int64_t x_row_stride,
+                         int rows, int cols, int group, int has_zeros, const void *packed,
+                         void *y, int64_t y_row_stride, qr_stream_t stream);
+
 /* A static string naming a status code (never NULL). */
 const char *qr_status_string(qr_status_t status);
 
