@@ -201,6 +201,19 @@ def test_zero_queries_and_wide_ranges_of_a_row():
     c.check(scale=1e-3)
 
 
+@pytest.mark.parametrize("nq", [1, 40])
+def test_non_finite_queries_stay_in_their_row(nq):
+    c = Case([64, 100, 700], [nq, nq, nq], 2, 4, seed=27)
+    clean, clean_lse = c.run()
+    c.q_dev = c.q_dev.clone()
+    c.q_dev[0, 1, 5], c.q_dev[nq, 6, 0] = float("nan"), float("inf")
+    out, lse = c.run()
+    bad = torch.zeros_like(lse, dtype=torch.bool)
+    bad[0, 1] = bad[nq, 6] = True
+    assert torch.isnan(out[bad].float()).all() and torch.isnan(lse[bad]).all()
+    assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], clean_lse[~bad])
+
+
 def test_one_long_context():
     Case([20000], [1], 1, 8, bs=64, seed=17).check()
     Case([9001], [4], 2, 5, bs=16, seed=18).check()
