@@ -31,6 +31,15 @@ inline KvView kv_view(const qr_kv_cache_t &c) {
 // from which 1152 is subtracted (exact: every |code| <= 128).
 constexpr uint32_t kFlip = 0x80808080u, kHigh = 0x64646464u;
 
+// The scale of a block's values is split into a power of two and a rest of at
+// most 1: 2^e with e in [kLeastExp, 129], scale <= 2^e.
+constexpr int kLeastExp = -100;
+__device__ __forceinline__ int scale_exp(float s) {
+    return max(static_cast<int>((__float_as_uint(s) >> 23) & 255) - 126, kLeastExp);
+}
+// 2^n for -126 <= n <= 127
+__device__ __forceinline__ float pow2i(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
+
 __device__ __forceinline__ uint32_t minus_1152(uint32_t h2) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&h2), __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t *>(&r);
@@ -52,12 +61,15 @@ __device__ __forceinline__ void codes_f16_pairs(uint32_t a, uint32_t b, uint32_t
     out[3] = minus_1152(__byte_perm(hi, kHigh, 0x4342));
 }
 
-// D += A B on fp16 operands with fp32 accumulators.
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// D = A B + C on fp16 operands with fp32 accumulators.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                        float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_f16_acc(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    mma_f16(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

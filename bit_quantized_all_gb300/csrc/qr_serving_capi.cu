@@ -136,7 +136,7 @@ QR_EXPORT qr_status_t qr_kv_append(qr_dtype_t dtype, int64_t tokens, const void 
 namespace {
 
 size_t attention_workspace(int requests, int64_t tokens, int q_heads, int heads, int head_dim) {
-    if (requests < 1 || requests > 65536 || tokens < 1 || tokens > INT_MAX || heads < 1 || heads > 65535 ||
+    if (requests < 1 || requests > 65536 || tokens < 1 || tokens > (1 << 30) || heads < 1 || heads > 65535 ||
         q_heads < heads || q_heads % heads || q_heads > 65535 || !head_dim_ok(head_dim))
         return 0;
     return qrk::kv_attention_workspace(requests, tokens, q_heads, heads, head_dim);
@@ -162,7 +162,9 @@ QR_EXPORT qr_status_t qr_kv_attention(qr_dtype_t dtype, int requests, int64_t to
     const qr_status_t st = check_cache(cache);
     if (st != QR_OK) return st;
     if (requests > 65536 || q_heads % cache->heads || q_heads > 65535) return QR_ERR_UNSUPPORTED;
-    if (int64_t(table_width) * cache->block_size > INT_MAX - 512 || tokens > INT_MAX) return QR_ERR_SIZE;
+    // positions minus a window stay within an int
+    constexpr int kFar = 1 << 30;
+    if (int64_t(table_width) * cache->block_size > INT_MAX - 512 || tokens > kFar) return QR_ERR_SIZE;
     const size_t need = attention_workspace(requests, tokens, q_heads, cache->heads, cache->head_dim);
     const size_t nq = extent(tokens, q_heads, cache->head_dim, q_token_stride, q_head_stride);
     const size_t no = extent(tokens, q_heads, cache->head_dim, out_token_stride, out_head_stride);
@@ -189,7 +191,7 @@ QR_EXPORT qr_status_t qr_kv_attention(qr_dtype_t dtype, int requests, int64_t to
     }
     return from_cuda(qrk::launch_kv_attention(
         dtype, {q, out, lse, q_offsets, kv_lens, block_table, q_token_stride, q_head_stride, out_token_stride,
-                out_head_stride, tokens, requests, q_heads, table_width, causal != 0, window, max_q, scale, workspace},
+                out_head_stride, tokens, requests, q_heads, table_width, causal != 0, window < kFar ? window : kFar, max_q, scale, workspace},
         *cache, reinterpret_cast<cudaStream_t>(stream)));
 }
 
