@@ -250,8 +250,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
             for (int i = 0; i < MT * kSteps; ++i)
                 *reinterpret_cast<uint4 *>(qf[i]) = reinterpret_cast<const uint4 *>(q_frag)[i * 32 + lane];
         }
-        // keys that every row sees: [seen_begin, seen_end)
-        const int seen_end = rows_here < kRows ? 0 : a.causal ? min(x.kv, pos_first + 1) : x.kv;
+        // keys that every row sees: [seen_begin, seen_end); rows past the
+        // item's are zero queries, whose sums are finite and not written
+        const int seen_end = a.causal ? min(x.kv, pos_first + 1) : x.kv;
         const int seen_begin = a.window > 0 ? pos_last - a.window + 1 : 0;
 
         float o[MT][kOut][4], m[MT][2], l[MT][2];
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int rr = q * 16 + g + 8 * k, pos = p0 + (row0 + rr) / group;
-                        const int row_end = rr >= rows_here ? 0 : a.causal ? min(x.kv, pos + 1) : x.kv;
+                        const int row_end = a.causal ? min(x.kv, pos + 1) : x.kv;
                         const int row_begin = a.window > 0 ? pos - a.window + 1 : 0;
                         e[k] = kLeastExp;
 #pragma unroll
