@@ -8,19 +8,25 @@ size_t kv_attention_workspace(int, long long, int, int, int head_dim) {
     return kWorkspaceCounters + size_t(2 * kMostCtas) * (dp <= 128 ? 32 : 16) * (dp + 2) * 4;
 }
 
-template <int DP, int MT>
+template <int DP, int NT>
 static cudaError_t run_split(int dtype, const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {
-    return c.dim == DP ? run_kv_split<DP, MT, true>(dtype, a, c, group, s)
-                       : run_kv_split<DP, MT, false>(dtype, a, c, group, s);
+    return c.dim == DP ? run_kv_split<DP, NT, true>(dtype, a, c, group, s)
+                       : run_kv_split<DP, NT, false>(dtype, a, c, group, s);
 }
 
 cudaError_t launch_kv_attention(int dtype, const KvAttentionArgs &a, const qr_kv_cache_t &cache, cudaStream_t s) {
     const KvView c = kv_view(cache);
     const int group = a.q_heads / c.heads;
-    const bool one = static_cast<long long>(a.max_q) * group <= 16;
-    if (c.dim <= 64) return one ? run_split<64, 1>(dtype, a, c, group, s) : run_split<64, 2>(dtype, a, c, group, s);
-    if (c.dim <= 128) return one ? run_split<128, 1>(dtype, a, c, group, s) : run_split<128, 2>(dtype, a, c, group, s);
-    return run_split<256, 1>(dtype, a, c, group, s);
+    const long long rows = static_cast<long long>(a.max_q) * group;
+    if (c.dim <= 64)
+        return rows <= 8    ? run_split<64, 1>(dtype, a, c, group, s)
+               : rows <= 16 ? run_split<64, 2>(dtype, a, c, group, s)
+                            : run_split<64, 4>(dtype, a, c, group, s);
+    if (c.dim <= 128)
+        return rows <= 8    ? run_split<128, 1>(dtype, a, c, group, s)
+               : rows <= 16 ? run_split<128, 2>(dtype, a, c, group, s)
+                            : run_split<128, 4>(dtype, a, c, group, s);
+    return rows <= 8 ? run_split<256, 1>(dtype, a, c, group, s) : run_split<256, 2>(dtype, a, c, group, s);
 }
 
 }  // namespace qrk

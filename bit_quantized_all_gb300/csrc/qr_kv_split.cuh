@@ -1,6 +1,6 @@
 // qr_kv_split.cuh -- attention over the 8-bit paged cache, split over the keys.
 //
-// An item is 16 * MT query rows (a row is a query token and one of the group's
+// An item is 8 * NT query rows (a row is a query token and one of the group's
 // heads) of one request and key/value head; its keys are counted in steps of
 // kStep tokens.  All items' steps in a row are cut into equal shares, one per
 // CTA, so the load is even whatever the lengths, and every CTA finds its
@@ -11,16 +11,21 @@
 // the parts in order, so the result does not depend on who comes last.
 //
 // Within a CTA each of four warps takes every fourth tile of 32 keys: copied
-// by 16-byte asynchronous copies into the warp's own ring, converted in
-// registers to fp16 (exact for codes) and multiplied on m16n8k16.  The order
-// of the head's dimensions within a product is free, so a lane's sixteen
+// by 16-byte asynchronous copies into the warp's own buffers, converted in
+// registers to fp16 (exact for codes) and multiplied on m16n8k16 with the keys
+// (then the values' dimensions) as M and the rows as N: a group of up to eight
+// heads fills one instruction, and nothing is converted twice.  The order of
+// the head's dimensions within a product is free, so a lane's sixteen
 // consecutive code bytes of a key are the operands of four instructions, and
-// its sixteen bytes of two value rows those of sixteen.  Scores are scaled by
+// its sixteen bytes of two value rows those of eight.  The weights reach the
+// second product's operand order by an 8 x 8 transpose between registers.  Scores are scaled by
 // the block's scale in fp32.  The values' scale goes into the softmax weight
 // before its rounding to fp16, relative to a power of two kept per row (the
 // largest among the blocks that the row sees), so that the accumulators are
 // the matrix instruction's own.
 #pragma once
+
+#include <type_traits>
 
 #include "qr_kv_device.cuh"
 #include "qr_launch.h"
@@ -29,10 +34,9 @@ namespace qrk {
 
 constexpr int kAttnThreads = 128, kAttnWarps = 4;
 constexpr int kTile = 32;                      // keys per warp and step of its loop
-constexpr int kStages = 2;
 constexpr int kStep = kTile * kAttnWarps;
 constexpr int kWeightExp = 12;                 // weights are at most 2^12: fp16 keeps 26 binades below them exact
-constexpr int kWorkspaceCounters = 4096;       // bytes: one counter per slot, two slots per CTA
+constexpr int kWorkspaceCounters = 8192;       // bytes: one counter per slot, two slots per CTA
 constexpr int kMostCtas = kWorkspaceCounters / 8;
 
 // A request as the sums see it: keys [kv - len, kv) are visible to some query.
@@ -74,17 +78,19 @@ __device__ __forceinline__ uint32_t v_offset(int row, int chunk) {
     return DP == 64 ? (row >> 1) * 128 + ((((row & 1) << 2 | chunk) ^ s) << 4) : row * DP + ((chunk ^ s) << 4);
 }
 
-template <int DP, int MT>
+template <int DP, int NT>
 struct AttnSmem {
-    static constexpr int kStage = 2 * kTile * DP;  // keys, values
-    static constexpr int kRing = kAttnWarps * kStages * kStage;
-    static constexpr int kQ = 16 * MT * DP * 2;    // fp16 fragments
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kHalf = kTile * DP;       // a tile's keys, or its values
+    static constexpr int kRing = kAttnWarps * 2 * kHalf;
+    static constexpr int kQ = kRows * DP * 2;      // fp16 fragments
     static constexpr int kOutStride = DP + 4;
-    static constexpr int kMerge = kAttnWarps * 16 * MT * (kOutStride + 2) * 4;
+    static constexpr int kMerge = kAttnWarps * kRows * (kOutStride + 2) * 4;
     static constexpr int kFirst = kRing > kMerge ? kRing : kMerge;
-    static constexpr int kBytes = kFirst + kQ + 16 * MT * 4;
-    static constexpr int kCtas = DP <= 128 && MT == 1 ? 3 : 2;  // per SM, by registers and shared memory
-    static constexpr int kSlot = 16 * MT * (DP + 2);          // floats of a part: accumulators, then (max, sum) pairs
+    static constexpr int kBytes = kFirst + kQ + kRows * 4;
+    // CTAs per SM, by registers (accumulators: DP / 4 * NT / 2 a thread)
+    static constexpr int kCtas = DP * NT <= 128 ? 4 : DP * NT <= 256 && NT <= 2 ? 3 : 2;
+    static constexpr int kSlot = kRows * (DP + 2);  // floats of a part: accumulators, then (max, sum) pairs
 };
 
 // One row's 4 values from dimension d on, and with d = 0 its lse.
@@ -110,13 +116,15 @@ __device__ __forceinline__ void attn_write(const KvAttentionArgs &a, bool bf16, 
 }
 
 // DP: the head's dimensions padded to 64, 128 or 256; FULL: they are exactly DP.
-template <int DP, int MT, bool FULL>
-__global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
+template <int DP, int NT, bool FULL>
+__global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
     kv_attention_split_kernel(KvAttentionArgs a, KvView c, bool bf16, int group) {
     chain_entry();
-    using S = AttnSmem<DP, MT>;
-    constexpr int kRows = 16 * MT, kSteps = DP / 16, kOut = DP / 8;
-    constexpr bool kQRegs = MT * DP <= 128;
+    using S = AttnSmem<DP, NT>;
+    constexpr int kRows = S::kRows, kSteps = DP / 16;
+    constexpr int kDimTiles = DP / 16;                     // output tiles of 16 dimensions
+    constexpr int kDims = DP == 64 ? 8 : 16;               // a lane's dimensions in a piece of a value row
+    constexpr bool kQRegs = NT * DP <= 128;
     const int dim = FULL ? DP : c.dim;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long warp_sums[kAttnWarps];
@@ -159,7 +167,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
     float *const partial = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kWorkspaceCounters);
     uint32_t *const q_frag = reinterpret_cast<uint32_t *>(smem + S::kFirst);
     float *const row_scale = reinterpret_cast<float *>(smem + S::kFirst + S::kQ);
-    const uint32_t ring_addr = smem_addr(smem + warp * (kStages * S::kStage));
+    const uint32_t kaddr = smem_addr(smem + warp * (2 * S::kHalf)), vaddr = kaddr + S::kHalf;
 
     long long at = 0;  // first step of request r
     int r = -1;
@@ -235,37 +243,35 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
 #pragma unroll
             for (int i = 0; i < DP / 32; ++i) {
                 // dimension d = 64 c + 16 t + 4 j + w is element w of lane
-                // (row, t) in step 4 c + j: fragment register (row >= 8) + 2 (w / 2)
+                // (row % 8, t) in step 4 c + j
                 const int d = lane + 32 * i;
                 const int ks = (d >> 6) * 4 + ((d >> 2) & 3), ft = (d >> 4) & 3, w = d & 3;
-                const int tile = rr >> 4, fr = rr & 15;
-                frag[(((tile * kSteps + ks) * 32 + (fr & 7) * 4 + ft) * 4 + (fr >> 3) + 2 * (w >> 1)) * 2 + (w & 1)] =
-                    __float2half_rn(f[i] * down1 * down2);
+                frag[(((rr >> 3) * kSteps + ks) * 32 + (rr & 7) * 4 + ft) * 4 + w] = __float2half_rn(f[i] * down1 * down2);
             }
         }
         __syncthreads();
-        uint32_t qf[kQRegs ? MT * kSteps : 1][4];
+        uint32_t qf[kQRegs ? NT * kSteps : 1][2];
         if constexpr (kQRegs) {
 #pragma unroll
-            for (int i = 0; i < MT * kSteps; ++i)
-                *reinterpret_cast<uint4 *>(qf[i]) = reinterpret_cast<const uint4 *>(q_frag)[i * 32 + lane];
+            for (int i = 0; i < NT * kSteps; ++i)
+                *reinterpret_cast<uint2 *>(qf[i]) = reinterpret_cast<const uint2 *>(q_frag)[i * 32 + lane];
         }
         // keys that every row sees: [seen_begin, seen_end); rows past the
         // item's are zero queries, whose sums are finite and not written
         const int seen_end = a.causal ? min(x.kv, pos_first + 1) : x.kv;
         const int seen_begin = a.window > 0 ? pos_last - a.window + 1 : 0;
 
-        float o[MT][kOut][4], m[MT][2], l[MT][2];
-        int ve[MT][2];  // the row's power of two of the values' scales
+        float o[NT][kDimTiles][4], m[NT][2], l[NT][2];
+        int ve[NT][2];  // the row's power of two of the values' scales
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+        for (int q = 0; q < NT; ++q) {
 #pragma unroll
-            for (int j = 0; j < kOut; ++j)
+            for (int j = 0; j < kDimTiles; ++j)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[i][j][k] = 0.0f;
-            m[i][0] = m[i][1] = -INFINITY;
-            l[i][0] = l[i][1] = 0.0f;
-            ve[i][0] = ve[i][1] = kLeastExp;
+                for (int k = 0; k < 4; ++k) o[q][j][k] = 0.0f;
+            m[q][0] = m[q][1] = -INFINITY;
+            l[q][0] = l[q][1] = 0.0f;
+            ve[q][0] = ve[q][1] = kLeastExp;
         }
 
         const int tiles = end > begin ? (end - begin + kTile - 1) / kTile : 0;
@@ -291,31 +297,41 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
             }
         };
         const int in_block = (1 << c.shift) - 1;
-        auto issue = [&](int i) {
-            const uint32_t dst = ring_addr + (i % kStages) * S::kStage;
-            const int key = begin + (i * kAttnWarps + warp) * kTile;
+        // Copies the keys (or the values) of the warp's i-th tile.
+        auto issue = [&](int i, auto values) {
+            constexpr bool kValues = decltype(values)::value;
             constexpr int kPer = DP / 16;  // 16-byte pieces of a padded row
-            const int row_l = lane / kPer, q_l = lane % kPer;  // this lane's piece, for DP <= 512
+            const int row_l = lane / kPer, q_l = lane % kPer;
+            if (i < mine) {
+                const int key = begin + (i * kAttnWarps + warp) * kTile;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int b = __shfl_sync(~0u, id, 2 * (i & 15) + k);
-                if (b >= 0 && (FULL || q_l * 16 < dim)) {
-                    const long long off = ((key + 16 * k) & in_block) * dim + row_l * dim + q_l * 16;
-                    const int8_t *kp = c.k + (b * c.k_block + h * c.k_head + off);
-                    const int8_t *vp = c.v + (b * c.v_block + h * c.v_head + off);
+                for (int k = 0; k < 2; ++k) {
+                    const int b = __shfl_sync(~0u, id, 2 * (i & 15) + k);
+                    if (b >= 0 && (FULL || q_l * 16 < dim)) {
+                        const int8_t *src = (kValues ? c.v + (b * c.v_block + h * c.v_head)
+                                                     : c.k + (b * c.k_block + h * c.k_head)) +
+                                            (((key + 16 * k) & in_block) + row_l) * dim + q_l * 16;
 #pragma unroll
-                    for (int j = 0; j < 16 * kPer / 32; ++j) {
-                        const int row = j * (32 / kPer);
-                        copy16_async(dst + k_offset<DP>(16 * k + row + row_l, q_l), kp + row * dim);
-                        copy16_async(dst + kTile * DP + v_offset<DP>(16 * k + row + row_l, q_l), vp + row * dim);
+                        for (int j = 0; j < 16 * kPer / 32; ++j) {
+                            const int row = j * (32 / kPer);
+                            copy16_async(kValues ? vaddr + v_offset<DP>(16 * k + row + row_l, q_l)
+                                                 : kaddr + k_offset<DP>(16 * k + row + row_l, q_l),
+                                         src + row * dim);
+                        }
                     }
                 }
             }
             copy_commit();
         };
+        constexpr std::false_type kKeysTag{};
+        constexpr std::true_type kValuesTag{};
 
+        // one buffer each for keys and values: a tile's keys are copied while
+        // the one before is weighted and summed, its values while the next
+        // tile's scores are taken
         look_up(0);
-        if (mine > 0) issue(0);
+        issue(0, kKeysTag);
+        issue(0, kValuesTag);
         for (int i = 0; i < mine; ++i) {
             float ks_cur[2], vs_cur[2];
             bool valid[2];
@@ -325,104 +341,100 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
                 vs_cur[k] = __shfl_sync(~0u, vs, 2 * (i & 15) + k);
                 valid[k] = __shfl_sync(~0u, id, 2 * (i & 15) + k) >= 0;
             }
-            if (i + 1 < mine) {
-                if (((i + 1) & 15) == 0) look_up(i + 1);
-                issue(i + 1);
-                copy_wait<1>();
-            } else {
-                copy_wait<0>();
-            }
-            __syncwarp();
-            const uint32_t kaddr = ring_addr + (i % kStages) * S::kStage, vaddr = kaddr + kTile * DP;
             const int key0 = begin + (i * kAttnWarps + warp) * kTile;
+            copy_wait<1>();
+            __syncwarp();
 
-            // scores of 32 keys
-            float s[MT][4][4];
+            // scores of 32 keys, as [key][row]
+            float s[NT][2][4];
 #pragma unroll
             for (int cc = 0; cc < DP / 64; ++cc) {
-                uint32_t qv[kQRegs ? 1 : MT][4][4];
+                uint32_t qv[kQRegs ? 1 : NT][4][2];
                 if constexpr (!kQRegs) {
 #pragma unroll
-                    for (int q = 0; q < MT; ++q)
+                    for (int q = 0; q < NT; ++q)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4 *>(qv[q][j]) =
-                                reinterpret_cast<const uint4 *>(q_frag)[(q * kSteps + cc * 4 + j) * 32 + lane];
+                            *reinterpret_cast<uint2 *>(qv[q][j]) =
+                                reinterpret_cast<const uint2 *>(q_frag)[(q * kSteps + cc * 4 + j) * 32 + lane];
                 }
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const uint4 kv4 = lds128(kaddr + k_offset<DP>(nt * 8 + g, cc * 4 + t));
-                    const uint32_t kw[4] = {kv4.x, kv4.y, kv4.z, kv4.w};
+                for (int kt = 0; kt < 2; ++kt) {
+                    const uint4 lo = lds128(kaddr + k_offset<DP>(kt * 16 + g, cc * 4 + t));
+                    const uint4 hi = lds128(kaddr + k_offset<DP>(kt * 16 + 8 + g, cc * 4 + t));
+                    const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        uint32_t b0, b1;
-                        codes_f16(kw[j], b0, b1);
+                        uint32_t ka[4];
+                        codes_f16(lw[j], ka[0], ka[2]);
+                        codes_f16(hw[j], ka[1], ka[3]);
 #pragma unroll
-                        for (int q = 0; q < MT; ++q) {
-                            const uint32_t(&f)[4] = kQRegs ? qf[q * kSteps + cc * 4 + j] : qv[kQRegs ? 0 : q][j];
+                        for (int q = 0; q < NT; ++q) {
+                            const uint32_t(&f)[2] = kQRegs ? qf[q * kSteps + cc * 4 + j] : qv[kQRegs ? 0 : q][j];
                             if (cc == 0 && j == 0)
-                                mma_f16(s[q][nt], f, b0, b1, 0.0f, 0.0f, 0.0f, 0.0f);
+                                mma_f16(s[q][kt], ka, f[0], f[1], 0.0f, 0.0f, 0.0f, 0.0f);
                             else
-                                mma_f16_acc(s[q][nt], f, b0, b1);
+                                mma_f16_acc(s[q][kt], ka, f[0], f[1]);
                         }
                     }
                 }
             }
+            __syncwarp();
+            if (((i + 1) & 15) == 0) look_up(i + 1);
+            issue(i + 1, kKeysTag);
 
             // running maximum and sum in powers of two; a tile that some row
-            // does not see whole is scaled and masked first
+            // does not see whole is masked first
             const bool mask = !valid[0] || !valid[1] || key0 + kTile > seen_end || key0 < seen_begin;
-            const int e0 = scale_exp(vs_cur[0]), e1 = scale_exp(vs_cur[1]);
-            uint32_t p[MT][2][4];  // A fragments of the two 16-key groups
+            const int vexp[2] = {scale_exp(vs_cur[0]), scale_exp(vs_cur[1])};
+            uint32_t p[NT][2][2];  // B fragments of the two 16-key groups
 #pragma unroll
-            for (int q = 0; q < MT; ++q) {
-                float f[2][2];
+            for (int q = 0; q < NT; ++q) {
+                // (a score is rounded before the maximum is taken from it: of
+                // scores of 2^30 a fused product would leave a remainder of 64)
+                const float2 row = *reinterpret_cast<const float2 *>(row_scale + q * 8 + 2 * t);
                 int e[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float row = row_scale[q * 16 + g + 8 * k];
-                    f[k][0] = row * ks_cur[0];
-                    f[k][1] = row * ks_cur[1];
-                    e[k] = max(e0, e1);
+#pragma unroll
+                    for (int kt = 0; kt < 2; ++kt) {
+                        const float f = (k ? row.y : row.x) * ks_cur[kt];
+                        s[q][kt][k] *= f;
+                        s[q][kt][2 + k] *= f;
+                    }
+                    e[k] = max(vexp[0], vexp[1]);
                 }
                 if (mask) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int rr = q * 16 + g + 8 * k, pos = p0 + (row0 + rr) / group;
+                        const int pos = p0 + (row0 + q * 8 + 2 * t + k) / group;
                         const int row_end = a.causal ? min(x.kv, pos + 1) : x.kv;
                         const int row_begin = a.window > 0 ? pos - a.window + 1 : 0;
                         e[k] = kLeastExp;
 #pragma unroll
-                        for (int gr = 0; gr < 2; ++gr) {
-                            const int key = key0 + 16 * gr;
-                            if (valid[gr] && key < row_end && key + 16 > row_begin) e[k] = max(e[k], gr ? e1 : e0);
+                        for (int kt = 0; kt < 2; ++kt) {
+                            const int key = key0 + 16 * kt;
+                            if (valid[kt] && key < row_end && key + 16 > row_begin) e[k] = max(e[k], vexp[kt]);
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const int col = key + 8 * (u >> 1) + 2 * t + (u & 1);
-                                float &v = s[q][2 * gr + (u >> 1)][2 * k + (u & 1)];
-                                v = valid[gr] && col < row_end && col >= row_begin ? v * f[k][gr] : -INFINITY;
+                            for (int u = 0; u < 2; ++u) {
+                                const int at_key = key + 8 * u + g;
+                                if (!valid[kt] || at_key >= row_end || at_key < row_begin) s[q][kt][2 * u + k] = -INFINITY;
                             }
                         }
-                        f[k][0] = f[k][1] = 1.0f;
                     }
                 }
-                float w0[2], w1[2], base[2];
+                float mx[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float a0 = max_nan(max_nan(s[q][0][2 * k], s[q][0][2 * k + 1]),
-                                             max_nan(s[q][1][2 * k], s[q][1][2 * k + 1]));
-                    const float a1 = max_nan(max_nan(s[q][2][2 * k], s[q][2][2 * k + 1]),
-                                             max_nan(s[q][3][2 * k], s[q][3][2 * k + 1]));
-                    float mx = max_nan(a0 * f[k][0], a1 * f[k][1]);
-                    mx = max_nan(mx, __shfl_xor_sync(~0u, mx, 1));
-                    mx = max_nan(mx, __shfl_xor_sync(~0u, mx, 2));
-                    base[k] = mx;
+                    mx[k] = max_nan(max_nan(s[q][0][k], s[q][0][2 + k]), max_nan(s[q][1][k], s[q][1][2 + k]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx[k] = max_nan(mx[k], __shfl_xor_sync(~0u, mx[k], d));
                 }
-                const bool grew = !(base[0] <= m[q][0]) || !(base[1] <= m[q][1]) || e[0] > ve[q][0] || e[1] > ve[q][1];
+                const bool grew = !(mx[0] <= m[q][0]) || !(mx[1] <= m[q][1]) || e[0] > ve[q][0] || e[1] > ve[q][1];
                 if (__any_sync(~0u, grew)) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float top = max_nan(m[q][k], base[k]);
+                        const float top = max_nan(m[q][k], mx[k]);
                         const float was = top == -INFINITY ? 0.0f : m[q][k] - top;
                         const int e_new = max(e[k], ve[q][k]);
                         l[q][k] *= exp2_fast(was);
@@ -430,45 +442,48 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
                         m[q][k] = top;
                         ve[q][k] = e_new;
 #pragma unroll
-                        for (int j = 0; j < kOut; ++j) {
-                            o[q][j][2 * k] *= fo;
-                            o[q][j][2 * k + 1] *= fo;
+                        for (int j = 0; j < kDimTiles; ++j) {
+                            o[q][j][k] *= fo;
+                            o[q][j][2 + k] *= fo;
                         }
                     }
                 }
+                float w[2][2], base[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    base[k] = m[q][k] == -INFINITY ? 0.0f : -m[q][k];
+                    base[k] = m[q][k] == -INFINITY ? 0.0f : m[q][k];
                     const float up = pow2i(kWeightExp - ve[q][k]);
-                    w0[k] = vs_cur[0] * up;
-                    w1[k] = vs_cur[1] * up;
-                    if (mask && e0 > ve[q][k]) w0[k] = 0.0f;  // a group that the row does not see
-                    if (mask && e1 > ve[q][k]) w1[k] = 0.0f;
+#pragma unroll
+                    for (int kt = 0; kt < 2; ++kt)
+                        // (a group whose scale is above the row's power is not seen by it)
+                        w[k][kt] = mask && vexp[kt] > ve[q][k] ? 0.0f : vs_cur[kt] * up;
                 }
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
+                for (int kt = 0; kt < 2; ++kt) {
                     float y[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        y[k] = exp2_fast(__fmaf_rn(s[q][nt][k], f[k >> 1][nt >> 1], base[k >> 1]));
-                        l[q][k >> 1] += y[k];
-                        y[k] *= nt < 2 ? w0[k >> 1] : w1[k >> 1];
+                        y[k] = exp2_fast(s[q][kt][k] - base[k & 1]);
+                        l[q][k & 1] += y[k];
+                        y[k] *= w[k & 1][kt];
                     }
-                    p[q][nt >> 1][2 * (nt & 1)] = pack_f16(y[0], y[1]);
-                    p[q][nt >> 1][2 * (nt & 1) + 1] = pack_f16(y[2], y[3]);
+                    p[q][kt][0] = transpose8(pack_f16(y[0], y[1]));
+                    p[q][kt][1] = transpose8(pack_f16(y[2], y[3]));
                 }
             }
 
-            constexpr int kPieces = DP == 64 ? 1 : DP / 128;  // 16- or 8-byte pieces of a value row per lane
-            constexpr int kWords = DP == 64 ? 2 : 4;
+            // values, as [dimension][row]
+            copy_wait<1>();
+            __syncwarp();
+            constexpr int kPieces = DP == 64 ? 1 : DP / 128;
 #pragma unroll
             for (int pc = 0; pc < kPieces; ++pc)
 #pragma unroll
-                for (int gr = 0; gr < 2; ++gr) {
-                    uint32_t vw[4][4];  // rows 2t, 2t + 1, 2t + 8, 2t + 9
+                for (int kt = 0; kt < 2; ++kt) {
+                    uint32_t vw[4][kDims / 4];  // rows 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
                     for (int rr = 0; rr < 4; ++rr) {
-                        const int row = 16 * gr + 2 * t + (rr & 1) + 8 * (rr >> 1);
+                        const int row = 16 * kt + 2 * t + (rr & 1) + 8 * (rr >> 1);
                         if constexpr (DP == 64) {
                             const uint2 v2 = lds64(vaddr + v_offset<DP>(row, g >> 1) + (g & 1) * 8);
                             vw[rr][0] = v2.x, vw[rr][1] = v2.y;
@@ -478,18 +493,24 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
                         }
                     }
 #pragma unroll
-                    for (int wd = 0; wd < kWords; ++wd) {
-                        uint32_t b0[4], b1[4];
-                        codes_f16_pairs(vw[0][wd], vw[1][wd], b0);
-                        codes_f16_pairs(vw[2][wd], vw[3][wd], b1);
+                    for (int wd = 0; wd < kDims / 4; ++wd) {
+                        uint32_t lo[4], hi[4];
+                        codes_f16_pairs(vw[0][wd], vw[1][wd], lo);
+                        codes_f16_pairs(vw[2][wd], vw[3][wd], hi);
 #pragma unroll
-                        for (int q = 0; q < MT; ++q)
+                        for (int u = 0; u < 2; ++u) {
+                            // dimensions 2u and 2u + 1 of the word: the tile's rows g and g + 8
+                            const uint32_t va[4] = {lo[2 * u], lo[2 * u + 1], hi[2 * u], hi[2 * u + 1]};
 #pragma unroll
-                            for (int d = 0; d < 4; ++d) mma_f16_acc(o[q][pc * 16 + wd * 4 + d], p[q][gr], b0[d], b1[d]);
+                            for (int q = 0; q < NT; ++q)
+                                mma_f16_acc(o[q][pc * 8 + wd * 2 + u], va, p[q][kt][0], p[q][kt][1]);
+                        }
                     }
                 }
             __syncwarp();
+            issue(i + 1, kValuesTag);
         }
+        copy_wait<0>();
 
         // join the four warps
         float *const merge_o = reinterpret_cast<float *>(smem);
@@ -497,30 +518,26 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
         float *const merge_l = merge_m + kAttnWarps * kRows;
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < MT; ++q)
+        for (int q = 0; q < NT; ++q)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float sum = l[q][k];
-                sum += __shfl_xor_sync(~0u, sum, 1);
-                sum += __shfl_xor_sync(~0u, sum, 2);
-                const int rr = warp * kRows + q * 16 + g + 8 * k;
-                if (t == 0) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+                const int rr = warp * kRows + q * 8 + 2 * t + k;
+                if (g == 0) {
                     merge_m[rr] = m[q][k];
                     merge_l[rr] = sum;
                 }
                 float *dst = merge_o + rr * S::kOutStride;
-                const float back = pow2i(min(ve[q][k] - kWeightExp, 127));
+                const float back = pow2i(ve[q][k] - kWeightExp);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    // column 2t + half of output tile j is dimension j % kDims
-                    // of piece 2t + half
-                    constexpr int kDims = DP == 64 ? 8 : 16;
-#pragma unroll
-                    for (int j = 0; j < kOut; j += 4) {
-                        const int d = (j / kDims) * 128 + (2 * t + half) * kDims + j % kDims, u = 2 * k + half;
-                        *reinterpret_cast<float4 *>(dst + d) =
-                            make_float4(o[q][j][u] * back, o[q][j + 1][u] * back, o[q][j + 2][u] * back, o[q][j + 3][u] * back);
-                    }
+                for (int j = 0; j < kDimTiles; j += 2) {
+                    // output tile j holds dimensions 2 (j % 8) and the next of
+                    // the lane's piece
+                    const int d = DP == 64 ? g * 8 + 2 * j : (j / 8) * 128 + g * 16 + 2 * (j % 8);
+                    *reinterpret_cast<float4 *>(dst + d) = make_float4(o[q][j][k] * back, o[q][j][2 + k] * back,
+                                                                       o[q][j + 1][k] * back, o[q][j + 1][2 + k] * back);
                 }
             }
         __syncthreads();
@@ -588,16 +605,16 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, MT>::kCtas)
     }
 }
 
-template <int DP, int MT, bool FULL>
+template <int DP, int NT, bool FULL>
 cudaError_t run_kv_split(int dtype, const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {
-    using S = AttnSmem<DP, MT>;
-    auto kern = kv_attention_split_kernel<DP, MT, FULL>;
+    using S = AttnSmem<DP, NT>;
+    auto kern = kv_attention_split_kernel<DP, NT, FULL>;
     cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(kern), S::kBytes);
     if (err != cudaSuccess) return err;
     const int sms = sm_count(&err);
     if (sms <= 0) return err;
     // no more CTAs than there can be steps
-    const long long items = (a.tokens * group / (16 * MT) + a.requests) * c.heads;
+    const long long items = (a.tokens * group / (8 * NT) + a.requests) * c.heads;
     const long long most = items * (((static_cast<long long>(a.width) << c.shift) + kStep - 1) / kStep);
     long long grid = static_cast<long long>(sms) * S::kCtas;
     grid = grid > kMostCtas ? kMostCtas : grid;
