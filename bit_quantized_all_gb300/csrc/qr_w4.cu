@@ -1,5 +1,5 @@
-// qr_w4.cu -- 4-bit weights with group scales: packing, quantizing and the
-// matrix-vector product (qr_w4_pack, qr_w4_quantize, qr_w4_matvec).
+// qr_w4.cu -- 4-bit weights with group scales: packing and quantizing
+// (qr_w4_pack, qr_w4_quantize); the product is in qr_w4_matvec.cu.
 //
 // Packed order.  y^T = W x^T runs on m16n8k16 matrix instructions with 16
 // weight rows as M and 8 tokens as N.  A tile of 16 rows x 64 columns is 512
@@ -121,49 +121,6 @@ __global__ void __launch_bounds__(kW4Threads) w4_quantize_kernel(int rows, int c
     }
 }
 
-// One warp per (token, row tile): lane l holds the sums of rows g and g + 8
-// over its own columns.
-template <int DT>
-__global__ void __launch_bounds__(kW4Threads) w4_matvec_simple_kernel(long long tokens, const uint16_t *x,
-                                                                      long long x_stride, int rows, int cols,
-                                                                      int group, bool has_zeros, W4Layout l,
-                                                                      const uint8_t *packed, uint16_t *y,
-                                                                      long long y_stride) {
-    chain_entry();
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const long long item = static_cast<long long>(blockIdx.x) * (kW4Threads / 32) + (threadIdx.x >> 5);
-    const long long m = item / l.row_tiles;
-    const int rt = static_cast<int>(item % l.row_tiles);
-    if (m >= tokens) return;
-    float acc[2] = {0.0f, 0.0f};
-    for (int c = 0; c < l.chunks; ++c) {
-        const uint4 w4 = reinterpret_cast<const uint4 *>(packed)[(static_cast<long long>(rt) * l.chunks + c) * 32 + lane];
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-        for (int j = 0; j < 4; ++j) {
-            const int gi = (c * 64 + 32 * (j >> 1)) / group;
-            const long long at = (static_cast<long long>(rt) * l.groups + gi) * 16 + 2 * g;
-            for (int nib = 0; nib < 8; ++nib) {
-                const int k = nib & 1, col = c * 64 + w4_column(t, j, nib);
-                const float s = __half2float(reinterpret_cast<const __half *>(packed + l.scales_at)[at + k]);
-                const float z = has_zeros ? static_cast<float>((packed + l.zeros_at)[at + k]) : 8.0f;
-                if (col < cols) {
-                    const uint16_t u = x[m * x_stride + col];
-                    const float xf = DT ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u));
-                    acc[k] = __fmaf_rn(xf, (static_cast<float>((w[j] >> (4 * nib)) & 15) - z) * s, acc[k]);
-                }
-            }
-        }
-    }
-    for (int k = 0; k < 2; ++k) {
-        acc[k] += __shfl_xor_sync(~0u, acc[k], 1);
-        acc[k] += __shfl_xor_sync(~0u, acc[k], 2);
-        const long long row = static_cast<long long>(rt) * 16 + g + 8 * k;
-        if (t == 0 && row < rows)
-            y[m * y_stride + row] = DT ? __bfloat16_as_ushort(__float2bfloat16_rn(acc[k]))
-                                       : __half_as_ushort(__float2half_rn(acc[k]));
-    }
-}
-
 cudaError_t launch_w4_pack(int rows, int cols, int group, const uint8_t *codes, const void *scales,
                            const uint8_t *zeros, void *packed, cudaStream_t s) {
     const W4Layout l = w4_layout(rows, cols, group, zeros != nullptr);
@@ -185,17 +142,6 @@ cudaError_t launch_w4_quantize(int dtype, int rows, int cols, int group, const v
     if (grid <= 0) return err;
     return launch_chained(kern, grid, kW4Threads, 0, s, rows, cols, group, l, static_cast<const uint16_t *>(w), w_stride,
                           static_cast<uint8_t *>(packed));
-}
-
-cudaError_t launch_w4_matvec(int dtype, long long tokens, const void *x, long long x_stride, int rows, int cols,
-                             int group, bool has_zeros, const void *packed, void *y, long long y_stride,
-                             cudaStream_t s) {
-    const W4Layout l = w4_layout(rows, cols, group, has_zeros);
-    const long long warps = tokens * l.row_tiles;
-    return launch_chained(dtype ? w4_matvec_simple_kernel<1> : w4_matvec_simple_kernel<0>,
-                          static_cast<unsigned>((warps + 7) / 8), kW4Threads, 0, s, tokens,
-                          static_cast<const uint16_t *>(x), x_stride, rows, cols, group, has_zeros, l,
-                          static_cast<const uint8_t *>(packed), static_cast<uint16_t *>(y), y_stride);
 }
 
 }  // namespace qrk
