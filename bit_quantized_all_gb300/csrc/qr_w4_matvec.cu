@@ -62,6 +62,35 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t zero) {
     }
 }
 
+// The first `have` (at most 8; none if below 1) 16-bit values from a 2-byte
+// aligned address, zeros after them: from the one or two aligned 16-byte words
+// that hold them.
+__device__ __forceinline__ uint4 load8_any(const uint16_t *p, int have) {
+    if (have <= 0) return make_uint4(0, 0, 0, 0);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint32_t off = static_cast<uint32_t>(at & 15);
+    const uint4 *src = reinterpret_cast<const uint4 *>(at - off);
+    const uint4 a = __ldg(src);
+    uint4 b = make_uint4(0, 0, 0, 0);
+    if (off + 2 * have > 16) b = __ldg(src + 1);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (off & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t bits = (off & 2) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+        if (2 * i + 1 >= have) w[i] = 2 * i >= have ? 0u : w[i] & 0xffffu;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <int NT>
 struct MatvecSmem {
     static constexpr int kPanel = NT <= 2 ? 16 : 32 / NT;  // chunks of x held at a time
@@ -95,12 +124,11 @@ __global__ void __launch_bounds__(kMvThreads, RT *NT <= 8 ? 2 : 1) w4_matvec_ker
             const int m = i / pieces, q = i % pieces, col = col0 + q * 8;
             const uint16_t *src = a.x + (token0 + m) * a.x_stride + col;
             uint8_t *const to = dst + m * S::kPitch + q * 16;
-            if (vector && col + 8 <= a.cols) {
+            const int have = min(8, a.cols - col);
+            if (vector && have == 8)
                 copy16_async(smem_addr(to), src);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) reinterpret_cast<uint16_t *>(to)[e] = col + e < a.cols ? src[e] : uint16_t(0);
-            }
+            else
+                *reinterpret_cast<uint4 *>(to) = load8_any(src, have);
         }
         copy_commit();
     };
