@@ -21,25 +21,29 @@ namespace qrk {
 constexpr int kPlanThreads = 256;
 constexpr int kEach = 8;                         // requests per thread and chunk
 constexpr int kChunk = kPlanThreads * kEach;
+constexpr long long kMostTokens = INT_MAX;       // tokens past it are counted, and get neither block nor slot
+constexpr int kWide = 4;                         // tokens per thread and step
 
 // The two sums a request adds: its new tokens and the blocks it takes.
 struct PlanSum {
     long long tokens, blocks;
 };
 
-__device__ __forceinline__ long long blocks_of(long long tokens, int shift) {
-    return (tokens + (1LL << shift) - 1) >> shift;
+// Blocks of a length below 2^32.
+__device__ __forceinline__ uint32_t blocks_of(uint32_t tokens, int shift) {
+    return tokens ? ((tokens - 1) >> shift) + 1 : 0;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(KvPlanArgs a, int shift, long long range) {
+__global__ void __launch_bounds__(kPlanThreads, 3) kv_plan_kernel(KvPlanArgs a, int shift, long long range) {
     chain_entry();
     __shared__ PlanSum warp_sums[kPlanThreads / 32];
-    __shared__ long long s_token[kChunk], s_block[kChunk];
-    __shared__ int s_cached[kChunk];
+    // request 8 j + k of a chunk at [k][j]: the threads' stores meet no bank
+    // twice, and the search goes over the j first
+    __shared__ int s_token[kEach][kPlanThreads], s_block[kEach][kPlanThreads], s_cached[kEach][kPlanThreads];
     __shared__ unsigned long long s_beyond;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // the last CTA also sees to tokens past max_tokens, which have blocks but no slots
-    const long long lo = range * blockIdx.x, hi = blockIdx.x + 1 == gridDim.x ? LLONG_MAX : lo + range;
+    const long long lo = range * blockIdx.x, hi = blockIdx.x + 1 == gridDim.x ? kMostTokens : lo + range;
     if (tid == 0) s_beyond = 0;
     PlanSum all = {0, 0};
     for (int c0 = 0; c0 < a.requests; c0 += kChunk) {
@@ -47,17 +51,17 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(KvPlanArgs a, int
         int cached[kEach], fresh[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            cached[k] = r0 + k < a.requests ? max(__ldg(a.cached + r0 + k), 0) : 0;
-            fresh[k] = r0 + k < a.requests ? max(__ldg(a.fresh + r0 + k), 0) : 0;
+            cached[k] = r0 + k < a.requests ? max(a.cached[r0 + k], 0) : 0;
+            fresh[k] = r0 + k < a.requests ? max(a.fresh[r0 + k], 0) : 0;
         }
         PlanSum mine = {0, 0};
         unsigned long long beyond = 0;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const long long need = blocks_of(static_cast<long long>(cached[k]) + fresh[k], shift);
+            const uint32_t c = cached[k], need = blocks_of(c + fresh[k], shift);
             mine.tokens += fresh[k];
-            mine.blocks += need - blocks_of(cached[k], shift);
-            beyond += need > a.width ? need - a.width : 0;
+            mine.blocks += need - blocks_of(c, shift);
+            beyond += need > static_cast<uint32_t>(a.width) ? need - a.width : 0;
         }
         PlanSum incl = mine;
 #pragma unroll
@@ -72,6 +76,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(KvPlanArgs a, int
         if (lane == 31) warp_sums[warp] = incl;
         if (blockIdx.x == 0 && beyond) atomicAdd(&s_beyond, beyond);
         __syncthreads();
+        const long long chunk_lo = all.tokens;
         PlanSum at = all;
 #pragma unroll
         for (int w = 0; w < kPlanThreads / 32; ++w) {
@@ -84,50 +89,63 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(KvPlanArgs a, int
         }
         at.tokens += incl.tokens - mine.tokens;
         at.blocks += incl.blocks - mine.blocks;
-        const long long chunk_lo = all.tokens - (warp_sums[0].tokens + warp_sums[1].tokens + warp_sums[2].tokens +
-                                                 warp_sums[3].tokens + warp_sums[4].tokens + warp_sums[5].tokens +
-                                                 warp_sums[6].tokens + warp_sums[7].tokens);
         // this CTA's share of the per-request outputs, and the chunk's sums
         const bool writes = (c0 / kEach + tid) % gridDim.x == blockIdx.x;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int i = tid * kEach + k;
-            s_token[i] = at.tokens;
-            s_block[i] = at.blocks;
-            s_cached[i] = cached[k];
+            s_token[k][tid] = static_cast<int>(min(at.tokens, kMostTokens));
+            s_block[k][tid] = static_cast<int>(min(at.blocks, kMostTokens));
+            s_cached[k][tid] = cached[k];
             if (writes && r0 + k < a.requests) {
                 a.q_offsets[r0 + k] = static_cast<int>(min(at.tokens, a.max_tokens));
                 a.kv_lens[r0 + k] =
-                    static_cast<int>(min(static_cast<long long>(cached[k]) + fresh[k], static_cast<long long>(INT_MAX)));
+                    static_cast<int>(min(static_cast<uint32_t>(cached[k]) + fresh[k], static_cast<uint32_t>(INT_MAX)));
             }
             at.tokens += fresh[k];
-            at.blocks += blocks_of(static_cast<long long>(cached[k]) + fresh[k], shift) - blocks_of(cached[k], shift);
+            at.blocks += blocks_of(static_cast<uint32_t>(cached[k]) + fresh[k], shift) - blocks_of(cached[k], shift);
         }
         __syncthreads();
-        const long long from = max(lo, chunk_lo), to = min(hi, all.tokens);
-        for (long long t = from + tid; t < to; t += kPlanThreads) {
-            // the last request whose first token is not after t (those past the
-            // last request, and those without new tokens, are passed over)
-            int i = 0;
+        const int from = static_cast<int>(min(max(lo, chunk_lo), kMostTokens)), to = static_cast<int>(min(hi, all.tokens));
+        for (long long t0 = from + kWide * tid; t0 < to; t0 += kWide * kPlanThreads) {
+            // kWide tokens in a row: the first one's request is the last whose
+            // first token is not after it (those past the last request, and
+            // those without new tokens, are passed over), the others' follow
+            int j = 0, k = 0;
 #pragma unroll
-            for (int step = kChunk / 2; step; step >>= 1)
-                if (s_token[i + step] <= t) i += step;
-            const int r = c0 + i;
-            const long long c = s_cached[i];
-            const long long pos = c + (t - s_token[i]), b = pos >> shift, have = blocks_of(c, shift);
-            const long long in_block = pos & ((1LL << shift) - 1);
-            int id = -1;
-            if (b < have) {
-                if (b < a.width) id = a.table[static_cast<long long>(r) * a.width + b];
-            } else {
-                const long long f = s_block[i] + (b - have);
-                if (f < a.num_free) id = __ldg(a.free_blocks + f);
-                if (b >= a.width)
-                    id = -1;
-                else if (in_block == 0)
-                    a.table[static_cast<long long>(r) * a.width + b] = id;
+            for (int step = kPlanThreads / 2; step; step >>= 1)
+                if (s_token[0][j + step] <= t0) j += step;
+#pragma unroll
+            for (int step = kEach / 2; step; step >>= 1)
+                if (s_token[k + step][j] <= t0) k += step;
+            int i = j * kEach + k, id[kWide];
+            uint32_t pos[kWide];
+            int request[kWide];
+#pragma unroll
+            for (int u = 0; u < kWide; ++u) {
+                if (u)
+                    while (i + 1 < kChunk && s_token[(i + 1) % kEach][(i + 1) / kEach] <= t0 + u) ++i;
+                k = i % kEach, j = i / kEach;
+                request[u] = c0 + i;
+                const uint32_t c = s_cached[k][j], have = blocks_of(c, shift);
+                pos[u] = c + (static_cast<int>(t0) + u - s_token[k][j]);
+                const uint32_t b = pos[u] >> shift, f = s_block[k][j] + (b - have);
+                const bool held = b < have;
+                id[u] = -1;
+                if (t0 + u < to && (held ? b < static_cast<uint32_t>(a.width) : f < static_cast<uint32_t>(a.num_free)))
+                    id[u] = held ? a.table[static_cast<long long>(request[u]) * a.width + b] : a.free_blocks[f];
             }
-            if (t < a.max_tokens) a.slots[t] = id >= 0 ? (static_cast<long long>(id) << shift) + in_block : -1;
+#pragma unroll
+            for (int u = 0; u < kWide; ++u) {
+                const long long t = t0 + u;
+                const uint32_t b = pos[u] >> shift, in_block = pos[u] & ((1u << shift) - 1);
+                if (t >= to) break;
+                if (b >= static_cast<uint32_t>(a.width))
+                    id[u] = -1;
+                else if (in_block == 0)
+                    a.table[static_cast<long long>(request[u]) * a.width + b] = id[u];
+                if (t < a.max_tokens)
+                    a.slots[t] = id[u] >= 0 ? (static_cast<long long>(id[u]) << shift) + in_block : -1;
+            }
         }
     }
     for (long long t = max(lo, all.tokens) + tid; t < min(hi, a.max_tokens); t += kPlanThreads) a.slots[t] = -1;
@@ -148,7 +166,7 @@ cudaError_t launch_kv_plan(const KvPlanArgs &a, cudaStream_t s) {
     const int sms = sm_count(&err);
     if (sms <= 0) return err;
     long long grid = (a.max_tokens + kPlanThreads - 1) / kPlanThreads;
-    grid = grid < 1 ? 1 : grid > 2 * sms ? 2 * sms : grid;
+    grid = grid < 1 ? 1 : grid > 3 * sms ? 3 * sms : grid;
     const long long range = (a.max_tokens + grid - 1) / grid;
     return launch_chained(kv_plan_kernel, static_cast<unsigned>(grid), kPlanThreads, 0, s, a, shift, range);
 }

@@ -70,9 +70,9 @@ __device__ __forceinline__ uint4 load8_any(const uint16_t *p, int have) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
     const uint32_t off = static_cast<uint32_t>(at & 15);
     const uint4 *src = reinterpret_cast<const uint4 *>(at - off);
-    const uint4 a = __ldg(src);
+    const uint4 a = *src;
     uint4 b = make_uint4(0, 0, 0, 0);
-    if (off + 2 * have > 16) b = __ldg(src + 1);
+    if (off + 2 * have > 16) b = src[1];
     uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (off & 8) {
 #pragma unroll
@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(kMvThreads, RT *NT <= 8 ? 2 : 1) w4_matvec_ker
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const int gi = NG == 2 ? (first + i) * 2 + n : (first + i) >> (a.group_shift - 1);
-                s[d][r][n] = __ldg(sp[r] + gi * 8);
-                if constexpr (ZEROS) z[d][r][n] = __ldg(zp[r] + gi * 8);
+                s[d][r][n] = sp[r][gi * 8];
+                if constexpr (ZEROS) z[d][r][n] = zp[r][gi * 8];
             }
         }
     };

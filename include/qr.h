@@ -655,7 +655,8 @@ typedef struct {
  *   counts[0..3]            blocks taken, new tokens, blocks that were
  *                           needed beyond num_free, table entries that were
  *                           needed beyond table_width.
- * counts[2] and counts[3] are 0 in a step that fitted.  free_blocks may be
+ * counts[2] and counts[3] are 0 in a step that fitted; tokens past the
+ * 2^31 - 1st are counted (to that number) and get neither block nor slot.  free_blocks may be
  * NULL when num_free is 0; slots when max_tokens is 0.  int32 arrays 4-byte,
  * slots 8-byte aligned.  requests <= 65536. */
 qr_status_t qr_kv_plan(int requests, const int32_t *cached_lens, const int32_t *new_lens,
