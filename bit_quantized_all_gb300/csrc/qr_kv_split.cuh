@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long warp_sums[kAttnWarps];
     __shared__ long long run_steps[kAttnThreads];
+    __shared__ AttnRequest run_request[kAttnThreads];  // each run's first request
     __shared__ unsigned s_ticket;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
 
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
         long long steps = 0;
         for (int r = r0; r < r1; ++r) {
             const AttnRequest x = attn_request(a, c, kRows, group, r);
+            if (r == r0) run_request[tid] = x;
             steps += static_cast<long long>(x.items) * attn_steps(x.len);
         }
         long long incl = steps;
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
             }
             at = run_steps[lo];
             r = lo * per;
-            x = attn_request(a, c, kRows, group, r);
+            x = run_request[lo];
             n_steps = attn_steps(x.len);
         }
         while (step >= at + static_cast<long long>(x.items) * n_steps) {
@@ -213,10 +215,69 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
         if (a.window > 0 && pos_first - a.window + 1 > begin)
             begin += (pos_first - a.window + 1 - begin) / kTile * kTile;
 
+        const int tiles = end > begin ? (end - begin + kTile - 1) / kTile : 0;
+        const int mine = tiles > warp ? (tiles - warp + kAttnWarps - 1) / kAttnWarps : 0;
+        // A lane holds one 16-key group's block and scales at a time: lane
+        // 2 i + k the k-th group of the warp's tile 16 * batch + i.
+        int id = -1;
+        float ks = 0.0f, vs = 0.0f;
+        auto look_up = [&](int first_tile) {
+            const int i = first_tile + (lane >> 1);
+            const int key = begin + (i * kAttnWarps + warp) * kTile + (lane & 1) * 16;
+            id = -1;
+            ks = vs = 0.0f;
+            if (i < mine && key < end) {
+                id = a.table[static_cast<long long>(r) * a.width + (key >> c.shift)];
+                if (id < 0 || id >= c.blocks) {
+                    id = -1;
+                } else {
+                    const long long s = static_cast<long long>(id) * c.heads + h;
+                    ks = c.ks[s];
+                    vs = c.vs[s];
+                }
+            }
+        };
+        const int in_block = (1 << c.shift) - 1;
+        // Copies the keys (or the values) of the warp's i-th tile.
+        auto issue = [&](int i, auto values) {
+            constexpr bool kValues = decltype(values)::value;
+            constexpr int kPer = DP / 16;  // 16-byte pieces of a padded row
+            const int row_l = lane / kPer, q_l = lane % kPer;
+            if (i < mine) {
+                const int key = begin + (i * kAttnWarps + warp) * kTile;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int b = __shfl_sync(~0u, id, 2 * (i & 15) + k);
+                    if (b >= 0 && (FULL || q_l * 16 < dim)) {
+                        const int8_t *src = (kValues ? c.v + (b * c.v_block + h * c.v_head)
+                                                     : c.k + (b * c.k_block + h * c.k_head)) +
+                                            (((key + 16 * k) & in_block) + row_l) * dim + q_l * 16;
+#pragma unroll
+                        for (int j = 0; j < 16 * kPer / 32; ++j) {
+                            const int row = j * (32 / kPer);
+                            copy16_async(kValues ? vaddr + v_offset<DP>(16 * k + row + row_l, q_l)
+                                                 : kaddr + k_offset<DP>(16 * k + row + row_l, q_l),
+                                         src + row * dim);
+                        }
+                    }
+                }
+            }
+            copy_commit();
+        };
+        constexpr std::false_type kKeysTag{};
+        constexpr std::true_type kValuesTag{};
+
+        // one buffer each for keys and values: a tile's keys are copied while
+        // the one before is weighted and summed, its values while the next
+        // tile's scores are taken; the first tile's while the queries are laid out
+        __syncthreads();
+        look_up(0);
+        issue(0, kKeysTag);
+        issue(0, kValuesTag);
+
         // the queries as fp16 fragments, each row scaled by a power of two to
         // a largest magnitude in [2^12, 2^13): exact for fp16 and bf16 inputs
         // down to 2^-26 of it, and the inverse goes into the score's factor
-        __syncthreads();
         for (int rr = warp; rr < kRows; rr += kAttnWarps) {
             const int row = row0 + rr;
             const uint16_t *q = static_cast<const uint16_t *>(a.q) + (x.q0 + row / group) * a.q_token +
@@ -274,64 +335,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
             ve[q][0] = ve[q][1] = kLeastExp;
         }
 
-        const int tiles = end > begin ? (end - begin + kTile - 1) / kTile : 0;
-        const int mine = tiles > warp ? (tiles - warp + kAttnWarps - 1) / kAttnWarps : 0;
-        // A lane holds one 16-key group's block and scales at a time: lane
-        // 2 i + k the k-th group of the warp's tile 16 * batch + i.
-        int id = -1;
-        float ks = 0.0f, vs = 0.0f;
-        auto look_up = [&](int first_tile) {
-            const int i = first_tile + (lane >> 1);
-            const int key = begin + (i * kAttnWarps + warp) * kTile + (lane & 1) * 16;
-            id = -1;
-            ks = vs = 0.0f;
-            if (i < mine && key < end) {
-                id = a.table[static_cast<long long>(r) * a.width + (key >> c.shift)];
-                if (id < 0 || id >= c.blocks) {
-                    id = -1;
-                } else {
-                    const long long s = static_cast<long long>(id) * c.heads + h;
-                    ks = c.ks[s];
-                    vs = c.vs[s];
-                }
-            }
-        };
-        const int in_block = (1 << c.shift) - 1;
-        // Copies the keys (or the values) of the warp's i-th tile.
-        auto issue = [&](int i, auto values) {
-            constexpr bool kValues = decltype(values)::value;
-            constexpr int kPer = DP / 16;  // 16-byte pieces of a padded row
-            const int row_l = lane / kPer, q_l = lane % kPer;
-            if (i < mine) {
-                const int key = begin + (i * kAttnWarps + warp) * kTile;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int b = __shfl_sync(~0u, id, 2 * (i & 15) + k);
-                    if (b >= 0 && (FULL || q_l * 16 < dim)) {
-                        const int8_t *src = (kValues ? c.v + (b * c.v_block + h * c.v_head)
-                                                     : c.k + (b * c.k_block + h * c.k_head)) +
-                                            (((key + 16 * k) & in_block) + row_l) * dim + q_l * 16;
-#pragma unroll
-                        for (int j = 0; j < 16 * kPer / 32; ++j) {
-                            const int row = j * (32 / kPer);
-                            copy16_async(kValues ? vaddr + v_offset<DP>(16 * k + row + row_l, q_l)
-                                                 : kaddr + k_offset<DP>(16 * k + row + row_l, q_l),
-                                         src + row * dim);
-                        }
-                    }
-                }
-            }
-            copy_commit();
-        };
-        constexpr std::false_type kKeysTag{};
-        constexpr std::true_type kValuesTag{};
-
-        // one buffer each for keys and values: a tile's keys are copied while
-        // the one before is weighted and summed, its values while the next
-        // tile's scores are taken
-        look_up(0);
-        issue(0, kKeysTag);
-        issue(0, kValuesTag);
         for (int i = 0; i < mine; ++i) {
             float ks_cur[2], vs_cur[2];
             bool valid[2];

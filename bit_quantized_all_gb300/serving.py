@@ -15,7 +15,6 @@ missing, and there is no CPU path.
 from __future__ import annotations
 
 import ctypes
-import math
 from typing import NamedTuple
 
 import torch
@@ -36,16 +35,20 @@ class KVCacheStruct(ctypes.Structure):
                 ("block_size", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
+_L = None  # the library, its serving signatures set
+
+
 def _lib():
-    L = lib()
-    if not getattr(L, "_serving_sigs", False):
+    global _L
+    if _L is None:
+        L = lib()
         vp, sz, i32, i64, f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64, ctypes.c_float
-        cache = ctypes.POINTER(KVCacheStruct)
+        # qr_kv_cache_t by address (KVCache keeps the structure alive)
         sigs = {
             "qr_kv_plan": (i32, [i32, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, i64, vp, vp]),
-            "qr_kv_append": (i32, [i32, i64, vp, vp, i64, i64, i64, i64, vp, cache, vp]),
+            "qr_kv_append": (i32, [i32, i64, vp, vp, i64, i64, i64, i64, vp, vp, vp]),
             "qr_kv_attention_workspace_bytes": (sz, [i32, i64, i32, i32, i32]),
-            "qr_kv_attention": (i32, [i32, i32, i64, i32, vp, i64, i64, vp, vp, vp, i32, cache, f32, i32, i32, i32,
+            "qr_kv_attention": (i32, [i32, i32, i64, i32, vp, i64, i64, vp, vp, vp, i32, vp, f32, i32, i32, i32,
                                       vp, i64, i64, vp, vp, sz, vp]),
             "qr_w4_bytes": (sz, [i32, i32, i32, i32]),
             "qr_w4_pack": (i32, [i32, i32, i32, vp, vp, vp, vp, vp]),
@@ -56,16 +59,35 @@ def _lib():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
-        L._serving_sigs = True
-    return L
+        _L = L
+    return _L
+
+
+# The handle of a device's current stream without building a Stream object
+# around it: these calls are made thousands of times a second.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current(device: torch.device, stream) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream(device, stream)
 
 
 def _int_tensor(t, what: str, dtype, shape=None) -> None:
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     _cuda_contig(t, what)
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _on(device: torch.device, what: str, *tensors) -> None:
+    for t in tensors:
+        if t.device != device:
+            raise ValueError(f"{what}: every tensor must be on {device}")
 
 
 # ---------------------------------------------------------------------------
@@ -100,7 +122,7 @@ class KVCache:
         self._struct = KVCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                      k_codes.stride(0), k_codes.stride(1), v_codes.stride(0), v_codes.stride(1),
                                      blocks, heads, block_size, head_dim)
-        self._ref = ctypes.byref(self._struct)
+        self._ref = ctypes.addressof(self._struct)
 
     @classmethod
     def empty(cls, blocks: int, heads: int, block_size: int, head_dim: int, device="cuda") -> "KVCache":
@@ -137,29 +159,37 @@ def qr_kv_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     _int_tensor(free_blocks, "free_blocks", torch.int32)
     if block_table.dim() != 2 or block_table.shape[0] != requests:
         raise ValueError(f"block_table must be [{requests}, width]")
-    dev = _same_device([cached_lens, new_lens, block_table, free_blocks], "qr_kv_plan")
+    dev = cached_lens.device
+    _on(dev, "qr_kv_plan", new_lens, block_table, free_blocks)
     if plan is None:
-        plan = KVPlan(block_table, torch.empty(requests + 1, dtype=torch.int32, device=dev),
-                      torch.empty(requests, dtype=torch.int32, device=dev),
-                      torch.empty(max_tokens, dtype=torch.int64, device=dev),
-                      torch.empty(4, dtype=torch.int32, device=dev))
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        q_offsets = torch.empty(requests + 1, dtype=torch.int32, device=dev)
+        kv_lens = torch.empty_like(cached_lens)
+        counts = torch.empty(4, dtype=torch.int32, device=dev)
+        plan = KVPlan(block_table, q_offsets, kv_lens, slots, counts)
     else:
-        _int_tensor(plan.q_offsets, "plan.q_offsets", torch.int32, (requests + 1,))
-        _int_tensor(plan.kv_lens, "plan.kv_lens", torch.int32, (requests,))
-        _int_tensor(plan.slots, "plan.slots", torch.int64, (max_tokens,))
-        _int_tensor(plan.counts, "plan.counts", torch.int32, (4,))
-        _same_device([block_table, plan.q_offsets, plan.kv_lens, plan.slots, plan.counts], "qr_kv_plan")
+        _, q_offsets, kv_lens, slots, counts = plan
+        _int_tensor(q_offsets, "plan.q_offsets", torch.int32, (requests + 1,))
+        _int_tensor(kv_lens, "plan.kv_lens", torch.int32, (requests,))
+        _int_tensor(slots, "plan.slots", torch.int64, (max_tokens,))
+        _int_tensor(counts, "plan.counts", torch.int32, (4,))
+        _on(dev, "qr_kv_plan", q_offsets, kv_lens, slots, counts)
         plan = plan._replace(block_table=block_table)
-    _check(_lib().qr_kv_plan(requests, cached_lens.data_ptr(), new_lens.data_ptr(), block_size,
-                             free_blocks.data_ptr(), free_blocks.numel(), block_table.data_ptr(),
-                             block_table.shape[1], plan.q_offsets.data_ptr(), plan.kv_lens.data_ptr(),
-                             plan.slots.data_ptr(), max_tokens, plan.counts.data_ptr(), _stream(dev, stream)),
-           "qr_kv_plan")
+    status = (_L or _lib()).qr_kv_plan(
+        requests, cached_lens.data_ptr(), new_lens.data_ptr(), block_size, free_blocks.data_ptr(), free_blocks.numel(),
+        block_table.data_ptr(), block_table.shape[1], q_offsets.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(),
+        max_tokens, counts.data_ptr(), _current(dev, stream))
+    if status:
+        _check(status, "qr_kv_plan")
     return plan
 
 
 def _rows(t: torch.Tensor, what: str, heads: int | None, dim: int) -> None:
     """A [tokens, heads, head_dim] operand, its last dimension contiguous."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3:
+        n = t.shape
+        if n[2] == dim and (heads is None or n[1] == heads) and t.stride(2) == 1:
+            return
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{what} must be a tensor [tokens, heads, head_dim]")
     if not t.is_cuda:
@@ -180,12 +210,15 @@ def qr_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.
         raise ValueError("k and v must have the same shape and dtype")
     dt = _dtype_code(k, "k")
     _int_tensor(slots, "slots", torch.int64, (tokens,))
-    if not (k.device == v.device == slots.device == cache.device):
-        raise ValueError(f"qr_kv_append: every tensor must be on {cache.device}")
+    dev = cache.device
+    _on(dev, "qr_kv_append", k, v, slots)
     if tokens:
-        _check(_lib().qr_kv_append(dt, tokens, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0),
-                                   v.stride(1), slots.data_ptr(), cache._ref, _stream(cache.device, stream)),
-               "qr_kv_append")
+        kt, kh, _ = k.stride()
+        vt, vh, _ = v.stride()
+        status = (_L or _lib()).qr_kv_append(dt, tokens, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(),
+                                             cache._ref, _current(dev, stream))
+        if status:
+            _check(status, "qr_kv_append")
     return cache
 
 
@@ -226,7 +259,7 @@ def qr_kv_attention(q: torch.Tensor, cache: KVCache, q_offsets: torch.Tensor, kv
     if block_table.dim() != 2 or block_table.shape[0] != requests:
         raise ValueError(f"block_table must be [{requests}, width]")
     if out is None:
-        out = torch.empty((tokens, q_heads, cache.head_dim), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _rows(out, "out", q_heads, cache.head_dim)
         if out.dtype != q.dtype or out.shape != q.shape:
@@ -239,17 +272,17 @@ def qr_kv_attention(q: torch.Tensor, cache: KVCache, q_offsets: torch.Tensor, kv
             _cuda_contig(workspace, "workspace")
             if workspace.dtype != torch.uint8:
                 raise TypeError(f"workspace must be torch.uint8, got {workspace.dtype}")
-        if not (q.device == kv_lens.device == q_offsets.device == block_table.device == out.device
-                == workspace.device == cache.device):
-            raise ValueError(f"qr_kv_attention: every tensor must be on {cache.device}")
-        _check(_lib().qr_kv_attention(dt, requests, tokens, q_heads, q.data_ptr(), q.stride(0), q.stride(1),
-                                      q_offsets.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
-                                      block_table.shape[1], cache._ref,
-                                      1.0 / math.sqrt(cache.head_dim) if scale is None else scale, 1 if causal else 0,
-                                      window, max(tokens, 1) if max_q is None else max_q, out.data_ptr(),
-                                      out.stride(0), out.stride(1), lse.data_ptr() if return_lse else None,
-                                      workspace.data_ptr(), workspace.numel(), _stream(cache.device, stream)),
-               "qr_kv_attention")
+        dev = cache.device
+        _on(dev, "qr_kv_attention", q, kv_lens, q_offsets, block_table, out, workspace)
+        qt, qh, _ = q.stride()
+        ot, oh, _ = out.stride()
+        status = (_L or _lib()).qr_kv_attention(
+            dt, requests, tokens, q_heads, q.data_ptr(), qt, qh, q_offsets.data_ptr(), kv_lens.data_ptr(),
+            block_table.data_ptr(), block_table.shape[1], cache._ref, cache.head_dim ** -0.5 if scale is None else scale,
+            1 if causal else 0, window, tokens if max_q is None else max_q, out.data_ptr(), ot, oh,
+            lse.data_ptr() if return_lse else None, workspace.data_ptr(), workspace.numel(), _current(dev, stream))
+        if status:
+            _check(status, "qr_kv_attention")
     return (out, lse) if return_lse else out
 
 
@@ -303,6 +336,10 @@ def qr_w4_pack(codes: torch.Tensor, scales: torch.Tensor, cols: int, group: int,
 
 
 def _matrix(t: torch.Tensor, what: str, cols: int | None = None) -> None:
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2:
+        n = t.shape[1]
+        if (cols is None or n == cols) and (n < 2 or t.stride(1) == 1):
+            return
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{what} must be a matrix")
     if not t.is_cuda:
@@ -335,12 +372,14 @@ def qr_w4_matvec(x: torch.Tensor, weight: W4Weight, y: torch.Tensor | None = Non
         _matrix(y, "y", weight.rows)
         if y.dtype != x.dtype or y.shape[0] != tokens:
             raise ValueError("y must be [tokens, rows] of x's dtype")
-    if not (x.device == y.device == weight.packed.device):
-        raise ValueError(f"qr_w4_matvec: every tensor must be on {x.device}")
+    dev = weight.packed.device
+    _on(dev, "qr_w4_matvec", x, y)
     if tokens:
-        _check(_lib().qr_w4_matvec(dt, tokens, x.data_ptr(), x.stride(0), weight.rows, weight.cols, weight.group,
-                                   1 if weight.has_zeros else 0, weight.packed.data_ptr(), y.data_ptr(), y.stride(0),
-                                   _stream(x.device, stream)), "qr_w4_matvec")
+        status = (_L or _lib()).qr_w4_matvec(dt, tokens, x.data_ptr(), x.stride(0), weight.rows, weight.cols,
+                                             weight.group, weight.has_zeros, weight.packed.data_ptr(), y.data_ptr(),
+                                             y.stride(0), _current(dev, stream))
+        if status:
+            _check(status, "qr_w4_matvec")
     return y
 
 

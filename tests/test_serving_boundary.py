@@ -57,7 +57,7 @@ def test_append_refusals():
 
     def call(**kw):
         v = {**ok, **kw}
-        v["cache"] = ctypes.byref(v["cache"]) if v["cache"] is not None else None
+        v["cache"] = ctypes.addressof(v["cache"]) if v["cache"] is not None else None
         return serving._lib().qr_kv_append(*v.values())
 
     for kw in (dict(tokens=0), dict(k=None), dict(v=None), dict(slots=None), dict(cache=None),
@@ -83,7 +83,7 @@ def test_attention_refusals():
 
     def call(**kw):
         v = {**ok, **kw}
-        v["cache"] = ctypes.byref(v["cache"]) if v["cache"] is not None else None
+        v["cache"] = ctypes.addressof(v["cache"]) if v["cache"] is not None else None
         return serving._lib().qr_kv_attention(*v.values())
 
     for kw in (dict(requests=0), dict(tokens=0), dict(q_heads=0), dict(q=None), dict(off=None), dict(kv=None),
