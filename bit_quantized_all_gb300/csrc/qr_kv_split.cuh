@@ -36,8 +36,10 @@ constexpr int kAttnThreads = 128, kAttnWarps = 4;
 constexpr int kTile = 32;                      // keys per warp and step of its loop
 constexpr int kStep = kTile * kAttnWarps;
 constexpr int kWeightExp = 12;                 // weights are at most 2^12: fp16 keeps 26 binades below them exact
-constexpr int kWorkspaceCounters = 8192;       // bytes: one counter per slot, two slots per CTA
-constexpr int kMostCtas = kWorkspaceCounters / 8;
+constexpr int kMostCtas = 640;
+constexpr int kWorkspaceCounters = 16 * kMostCtas;  // bytes: two slots per CTA, two counters per slot
+constexpr int kGroup = 16;                     // parts of an item joined at a time
+constexpr int kMostParts = kMostCtas / kGroup > kGroup ? kMostCtas / kGroup : kGroup;
 
 // A request as the sums see it: keys [kv - len, kv) are visible to some query.
 struct AttnRequest {
@@ -519,6 +521,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
         float *const merge_o = reinterpret_cast<float *>(smem);
         float *const merge_m = merge_o + kAttnWarps * kRows * S::kOutStride;
         float *const merge_l = merge_m + kAttnWarps * kRows;
+        float *const merge_sum = merge_o + kRows * (kMostParts + 2);  // (when parts are joined)
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < NT; ++q)
@@ -575,34 +578,71 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
             }
         }
         if (parts > 1) {
-            __syncthreads();
-            if (tid == 0) {
+            // In groups of kGroup parts, then the groups: whichever CTA brings the
+            // last one joins them.  A counter wraps to 0 with its last arrival,
+            // ready for the next call.
+            const int groups = (parts + kGroup - 1) / kGroup;
+            const int my_group = static_cast<int>(blockIdx.x - first_cta) / kGroup;
+            long long at_cta = first_cta + my_group * kGroup;
+            int count = min(kGroup, parts - my_group * kGroup), stride = 1;
+            unsigned *counter = counters + slot_of(at_cta);
+            for (int level = 0;; ++level) {
+                __syncthreads();
+                if (tid == 0) {
+                    __threadfence();
+                    s_ticket = atomicInc(counter, static_cast<unsigned>(count - 1));
+                }
+                __syncthreads();
+                if (s_ticket != static_cast<unsigned>(count - 1)) break;
                 __threadfence();
-                // wraps to 0 with the item's last part: ready for the next call
-                s_ticket = atomicInc(counters + slot_of(first_cta), static_cast<unsigned>(parts - 1));
-            }
-            __syncthreads();
-            if (s_ticket == static_cast<unsigned>(parts - 1)) {
-                __threadfence();
+                // every row's maximum, sum and the parts' weights
+                float *const weight = reinterpret_cast<float *>(smem);  // [row][part]
+                float2 *const total = reinterpret_cast<float2 *>(weight + kRows * kMostParts);
+                for (int i = tid; i < rows_here * count; i += kAttnThreads) {
+                    const int rr = i / count, k = i % count;
+                    const float *src = partial + slot_of(at_cta + k * stride) * S::kSlot + kRows * DP + 2 * rr;
+                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src));
+                    weight[rr * kMostParts + k] = ml.x;
+                    merge_sum[rr * kMostParts + k] = ml.y;
+                }
+                __syncthreads();
+                if (tid < rows_here) {
+                    float top = -INFINITY, sum = 0.0f;
+                    for (int k = 0; k < count; ++k) top = max_nan(top, weight[tid * kMostParts + k]);
+                    for (int k = 0; k < count; ++k) {
+                        const float f = top == -INFINITY ? 0.0f : exp2_fast(weight[tid * kMostParts + k] - top);
+                        sum = __fmaf_rn(merge_sum[tid * kMostParts + k], f, sum);
+                        weight[tid * kMostParts + k] = f;
+                    }
+                    total[tid] = make_float2(top, sum);
+                }
+                __syncthreads();
+                const bool last = level == 1 || groups == 1;
+                float *const to = partial + slot_of(at_cta) * S::kSlot;
                 for (int i = tid; i < rows_here * kQuads; i += kAttnThreads) {
                     const int rr = i / kQuads, d = i % kQuads * 4, row = row0 + rr;
-                    float top = -INFINITY, sum = 0.0f;
                     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-                    for (int k = 0; k < parts; ++k) {
-                        const float *src = partial + slot_of(first_cta + k) * S::kSlot;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + kRows * DP + 2 * rr));
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + rr * DP + d));
-                        const float next = max_nan(top, ml.x);
-                        const float base = next == -INFINITY ? 0.0f : next;
-                        const float f0 = exp2_fast(top - base), f1 = exp2_fast(ml.x - base);
-                        top = next;
-                        sum = __fmaf_rn(ml.y, f1, sum * f0);
-                        v.x = __fmaf_rn(y.x, f1, v.x * f0), v.y = __fmaf_rn(y.y, f1, v.y * f0);
-                        v.z = __fmaf_rn(y.z, f1, v.z * f0), v.w = __fmaf_rn(y.w, f1, v.w * f0);
+                    for (int k = 0; k < count; ++k) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(
+                            partial + slot_of(at_cta + k * stride) * S::kSlot + rr * DP + d));
+                        const float f = weight[rr * kMostParts + k];
+                        v.x = __fmaf_rn(y.x, f, v.x), v.y = __fmaf_rn(y.y, f, v.y);
+                        v.z = __fmaf_rn(y.z, f, v.z), v.w = __fmaf_rn(y.w, f, v.w);
                     }
-                    attn_write(a, bf16, dim, x.q0 + row / group, h * group + row % group, d, v, top, sum);
+                    const float2 ts = total[rr];
+                    if (last) {
+                        attn_write(a, bf16, dim, x.q0 + row / group, h * group + row % group, d, v, ts.x, ts.y);
+                    } else {
+                        __stcg(reinterpret_cast<float4 *>(to + rr * DP + d), v);
+                        if (d == 0) __stcg(reinterpret_cast<float2 *>(to + kRows * DP + 2 * rr), ts);
+                    }
                 }
+                if (last) break;
+                counter = counters + 2 * kMostCtas + slot_of(first_cta);
+                at_cta = first_cta;
+                count = groups;
+                stride = kGroup;
             }
         }
     }
@@ -617,7 +657,9 @@ cudaError_t run_kv_split(int dtype, const KvAttentionArgs &a, const KvView &c, i
     const int sms = sm_count(&err);
     if (sms <= 0) return err;
     // no more CTAs than there can be steps
-    const long long items = (a.tokens * group / (8 * NT) + a.requests) * c.heads;
+    const long long by_tokens = a.tokens * group / (8 * NT) + a.requests;
+    const long long by_requests = ((static_cast<long long>(a.max_q) * group + 8 * NT - 1) / (8 * NT)) * a.requests;
+    const long long items = (by_tokens < by_requests ? by_tokens : by_requests) * c.heads;
     const long long most = items * (((static_cast<long long>(a.width) << c.shift) + kStep - 1) / kStep);
     long long grid = static_cast<long long>(sms) * S::kCtas;
     grid = grid > kMostCtas ? kMostCtas : grid;
