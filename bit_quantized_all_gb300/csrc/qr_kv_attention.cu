@@ -3,7 +3,11 @@
 
 namespace qrk {
 
+// The tcgen05 kernel (qr_kv_tc.cu), for head_dim up to 128.
+cudaError_t launch_kv_tc(int dtype, const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s);
+
 size_t kv_attention_workspace(int, long long, int, int, int head_dim) {
+    // two slots per CTA: 640 CTAs of up to 32 rows, or 160 of 128
     const size_t dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
     return kWorkspaceCounters + size_t(2 * kMostCtas) * (dp <= 128 ? 32 : 16) * (dp + 2) * 4;
 }
@@ -18,6 +22,7 @@ cudaError_t launch_kv_attention(int dtype, const KvAttentionArgs &a, const qr_kv
     const KvView c = kv_view(cache);
     const int group = a.q_heads / c.heads;
     const long long rows = static_cast<long long>(a.max_q) * group;
+    if (c.dim <= 128 && rows > 16) return launch_kv_tc(dtype, a, c, group, s);
     if (c.dim <= 64)
         return rows <= 8    ? run_split<64, 1>(dtype, a, c, group, s)
                : rows <= 16 ? run_split<64, 2>(dtype, a, c, group, s)

@@ -1,0 +1,672 @@
+// qr_kv_tc.cuh -- attention over the 8-bit paged cache for many query rows, on
+// tcgen05.
+//
+// An item is 128 query rows (a row is a query token and one of the group's
+// heads) of one request and key/value head; its keys are taken 128 at a time.
+// As in qr_kv_split.cuh the items' key tiles are cut into equal shares, one
+// per CTA (here counting only tiles that some row sees), and the parts of a
+// divided item are joined by whichever CTA brings the last one.
+//
+// A CTA is nine warps.  Four convert: each tile's codes come through registers
+// and go to shared memory as fp16 (exact), double buffered.  One thread issues
+// the products: S = Q K^T into one of two halves of tensor memory, then
+// O += P V with P read from tensor memory.  Four warps, a thread per row, do
+// the softmax: S is read twice (maximum, then weights, which are written back
+// as fp16), so a thread holds 32 values at a time.  The next tile's S is
+// computed while a tile's weights are.
+//
+// O stays in tensor memory.  It is rescaled only when a row's maximum has
+// grown by more than 2^kSlack, or the power of two under which the values'
+// scales are kept by more than 2^kScaleSlack; weights are then below 2^15, and
+// fp16 keeps them exact to 2^-11 down to 2^-21 of a weight of 1.
+//
+// What bounds it: the tensor cores and, close behind, the softmax (about 800
+// issue slots per scheduler and tile against 1024 cycles of products).
+#pragma once
+
+#include "qr_kv_split.cuh"
+#include "qr_tcgen05.cuh"
+
+namespace qrk {
+
+constexpr int kTcRows = 128, kTcKeys = 128;
+constexpr int kTcThreads = 288;
+constexpr int kTcMostCtas = 160;
+constexpr float kSlack = 6.0f;
+constexpr int kScaleSlack = 2;
+constexpr int kTcWeightExp = 7;  // weight 1 of the largest scale is 2^7
+
+// Tensor memory columns: S twice, O, P twice.
+constexpr uint32_t kColS = 0, kColO = 256, kColP = 384, kColumns = 512;
+
+struct TcMeta {
+    float ks[8], vs[8];
+    uint32_t valid;
+    int vexp;  // the largest scale_exp of the tile's valid groups
+    int pad[2];
+};
+
+template <int DP>
+struct TcSmem {
+    static constexpr int kSlabs = DP / 64, kTile = kSlabs * 16384;  // 128 rows of fp16
+    uint8_t q[kTile];
+    uint8_t k[2][kTile];
+    uint8_t v[2][kTile];
+    TcMeta meta[4];
+    float row_scale[kTcRows], row_sum[kTcRows];
+    long long run_steps[128], warp_sums[4];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done, q_full;
+    uint32_t tmem;
+    unsigned ticket;
+    int fail;
+};
+
+template <int DP>
+constexpr int kTcSlot = kTcRows * (DP + 2);
+
+// The items of a CTA's share, in order; every thread keeps its own copy.
+struct TcWalk {
+    long long step, last, share, at;
+    int r, j, tiles_of_r;
+    AttnRequest x;
+    // the current item
+    long long item_first;
+    int head, row0, rows, begin, end, steps, p0;
+    int part_first_cta, parts;
+
+    // The keys that some row of row tile `jj` sees, [b, e).
+    __device__ __forceinline__ static int range(const KvAttentionArgs &a, const AttnRequest &x, int group, int jj, int *b,
+                                                int *e) {
+        const int p0 = x.kv - x.nq, rows = min(kTcRows, x.nq * group - jj * kTcRows);
+        const int pos_first = p0 + jj * kTcRows / group, pos_last = p0 + (jj * kTcRows + rows - 1) / group;
+        *e = a.causal ? max(0, min(x.kv, pos_last + 1)) : x.kv;
+        *b = a.window > 0 ? max(0, pos_first - a.window + 1) / 16 * 16 : 0;
+        return *e > *b ? (*e - *b + kTcKeys - 1) / kTcKeys : 1;
+    }
+    __device__ __forceinline__ void enter(const KvAttentionArgs &a, const KvView &c, int group, int request) {
+        r = request;
+        j = 0;
+        x = attn_request(a, c, kTcRows, group, r);
+        tiles_of_r = x.items / c.heads;
+    }
+    __device__ __forceinline__ bool next(const KvAttentionArgs &a, const KvView &c, int group, const long long *run_steps) {
+        if (step >= last) return false;
+        if (r < 0) {
+            int lo = 0, hi = 127;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (run_steps[mid] <= step) lo = mid; else hi = mid - 1;
+            }
+            at = run_steps[lo];
+            enter(a, c, group, lo * ((a.requests + 127) / 128));
+        }
+        int b, e;
+        for (;;) {
+            if (j >= tiles_of_r) {
+                enter(a, c, group, r + 1);
+                continue;
+            }
+            steps = range(a, x, group, j, &b, &e);
+            if (step < at + static_cast<long long>(steps) * c.heads) break;
+            at += static_cast<long long>(steps) * c.heads;
+            ++j;
+        }
+        head = static_cast<int>((step - at) / steps);
+        item_first = at + static_cast<long long>(head) * steps;
+        const int s0 = static_cast<int>(step - item_first), s1 = static_cast<int>(min(item_first + steps, last) - item_first);
+        begin = b + s0 * kTcKeys;
+        end = min(b + s1 * kTcKeys, e);
+        row0 = j * kTcRows;
+        rows = min(kTcRows, x.nq * group - row0);
+        p0 = x.kv - x.nq;
+        part_first_cta = static_cast<int>(item_first / share);
+        parts = static_cast<int>((item_first + steps - 1) / share) - part_first_cta + 1;
+        step = item_first + s1;
+        return true;
+    }
+    __device__ __forceinline__ int tiles() const { return end > begin ? (end - begin + kTcKeys - 1) / kTcKeys : 0; }
+};
+
+// Waits for a phase; after a wait that ran out every wait of the CTA fails.
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*static_cast<volatile int *>(fail)) return false;
+    if (mbar_wait(bar, parity)) return true;
+    if (atomicExch(fail, 1) == 0) atomicAdd(timeouts, 1u);
+    return false;
+}
+
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <int DP, bool FULL>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    kv_attention_tc_kernel(KvAttentionArgs a, KvView c, bool bf16, int group, unsigned *timeouts) {
+    chain_entry();
+    using S = TcSmem<DP>;
+    extern __shared__ uint8_t raw[];
+    S &sm = *reinterpret_cast<S *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
+    const int dim = FULL ? DP : c.dim;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // sums of the steps over 128 runs of requests
+    {
+        const int per = (a.requests + 127) / 128;
+        long long steps = 0, incl = 0;
+        if (tid < 128) {
+            const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
+            for (int r = r0; r < r1; ++r) {
+                const AttnRequest x = attn_request(a, c, kTcRows, group, r);
+                int b, e;
+                for (int j = 0; j < x.items / c.heads; ++j)
+                    steps += static_cast<long long>(TcWalk::range(a, x, group, j, &b, &e)) * c.heads;
+            }
+            incl = steps;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long o = __shfl_up_sync(~0u, incl, d);
+                if (lane >= d) incl += o;
+            }
+            if (lane == 31) sm.warp_sums[warp] = incl;
+        }
+        if (tid == 128) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&sm.k_full[i], 128);
+                mbar_init(&sm.v_full[i], 128);
+                mbar_init(&sm.k_empty[i], 1);
+                mbar_init(&sm.v_empty[i], 1);
+                mbar_init(&sm.s_full[i], 1);
+                mbar_init(&sm.p_full[i], 128);
+            }
+            mbar_init(&sm.pv_done, 1);
+            mbar_init(&sm.q_full, 128);
+            mbar_init_fence();
+            sm.fail = 0;
+        }
+        if (warp == 8) tc_alloc(&sm.tmem, kColumns);
+        __syncthreads();
+        if (tid < 128) {
+            long long before = 0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                if (w < warp) before += sm.warp_sums[w];
+            sm.run_steps[tid] = before + incl - steps;
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
+    const uint32_t tmem = sm.tmem;
+    TcWalk walk;
+    {
+        const long long all = sm.warp_sums[0] + sm.warp_sums[1] + sm.warp_sums[2] + sm.warp_sums[3];
+        walk.share = (all + gridDim.x - 1) / gridDim.x;
+        walk.step = walk.share * blockIdx.x;
+        walk.last = min(walk.step + walk.share, all);
+        walk.at = 0;
+        walk.r = -1;
+    }
+    int *const fail = &sm.fail;
+
+    if (warp >= 4 && warp < 8) {
+        // ---- the codes, through registers, to fp16 tiles in shared memory
+        const int ct = tid - 128;
+        constexpr int kPer = DP / 16;           // 16-byte pieces of a padded row; also passes
+        constexpr int kPassRows = 128 / kPer;
+        const int q_l = ct % kPer, row_l = ct / kPer;
+        const bool in_row = FULL || q_l * 16 < dim;
+        const int in_block = (1 << c.shift) - 1;
+        uint32_t it = 0;
+        while (walk.next(a, c, group, sm.run_steps)) {
+            const int tiles = walk.tiles();
+            const int32_t *const table = a.table + static_cast<long long>(walk.r) * a.width;
+            const long long khead = walk.head * c.k_head + q_l * 16, vhead = walk.head * c.v_head + q_l * 16;
+            int id[kPer], mid = -1;
+            float mks = 0.0f, mvs = 0.0f;
+            uint4 kr[kPer], vr[kPer];
+            auto ids = [&](int i) {
+                const int key0 = walk.begin + i * kTcKeys;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int key = (key0 + row_l + j * kPassRows) & ~15;
+                    id[j] = -1;
+                    if (key < walk.end) id[j] = table[key >> c.shift];
+                    if (id[j] >= c.blocks) id[j] = -1;
+                }
+                mid = -1;
+                if (ct < 8 && key0 + ct * 16 < walk.end) mid = table[(key0 + ct * 16) >> c.shift];
+                if (mid >= c.blocks) mid = -1;
+            };
+            auto load = [&](int i, uint4 (&reg)[kPer], const int8_t *base, long long block, long long head_off) {
+                const int key0 = walk.begin + i * kTcKeys;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    reg[j] = make_uint4(0, 0, 0, 0);
+                    if (id[j] >= 0 && in_row)
+                        reg[j] = __ldcs(reinterpret_cast<const uint4 *>(
+                            base + id[j] * block + head_off + ((key0 + row_l + j * kPassRows) & in_block) * dim));
+                }
+            };
+            auto scales = [&]() {
+                mks = mvs = 0.0f;
+                if (ct < 8 && mid >= 0) {
+                    const long long s = static_cast<long long>(mid) * c.heads + walk.head;
+                    mks = c.ks[s];
+                    mvs = c.vs[s];
+                }
+            };
+            auto store = [&](const uint4 (&reg)[kPer], uint8_t *tile) {
+                const uint32_t base = smem_addr(tile) + (q_l >> 2) * 16384;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int row = row_l + j * kPassRows;
+                    const uint32_t w[4] = {reg[j].x, reg[j].y, reg[j].z, reg[j].w};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) codes_f16(w[i], h[2 * i], h[2 * i + 1]);
+                    // two 16-byte pieces; lanes of the second slab store theirs
+                    // in the other order, so that a phase meets no bank twice
+                    const bool swap = (q_l >> 2) & 1;
+                    const int piece = (q_l & 3) * 2;
+                    const uint32_t first = base + swizzled(row, piece + (swap ? 1 : 0));
+                    const uint32_t second = base + swizzled(row, piece + (swap ? 0 : 1));
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(first), "r"(swap ? h[4] : h[0]),
+                                 "r"(swap ? h[5] : h[1]), "r"(swap ? h[6] : h[2]), "r"(swap ? h[7] : h[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(second), "r"(swap ? h[0] : h[4]),
+                                 "r"(swap ? h[1] : h[5]), "r"(swap ? h[2] : h[6]), "r"(swap ? h[3] : h[7])
+                                 : "memory");
+                }
+            };
+            if (tiles > 0) {
+                ids(0);
+                load(0, kr, c.k, c.k_block, khead);
+                load(0, vr, c.v, c.v_block, vhead);
+                scales();
+            }
+            for (int i = 0; i < tiles; ++i, ++it) {
+                const int s = it & 1;
+                const uint32_t parity = ((it >> 1) & 1) ^ 1;
+                const bool bad = mid < 0;
+                const float ks_now = mks, vs_now = mvs;
+                if (i + 1 < tiles) ids(i + 1);
+                if (it >= 2 && !tc_wait(&sm.k_empty[s], parity, fail, timeouts)) goto out;
+                store(kr, sm.k[s]);
+                if (warp == 4) {
+                    // (entry it % 4: tile it - 4's softmax is done before K of
+                    // tile it may be written)
+                    TcMeta &meta = sm.meta[it & 3];
+                    const uint32_t valid = __ballot_sync(~0u, ct < 8 && !bad);
+                    int e = ct < 8 && !bad ? scale_exp(vs_now) : kLeastExp;
+#pragma unroll
+                    for (int d = 1; d < 8; d <<= 1) e = max(e, __shfl_xor_sync(~0u, e, d));
+                    if (ct < 8) {
+                        meta.ks[ct] = ks_now;
+                        meta.vs[ct] = vs_now;
+                    }
+                    if (ct == 0) {
+                        meta.valid = valid;
+                        meta.vexp = e;
+                    }
+                }
+                smem_to_tensor_fence();
+                mbar_arrive(&sm.k_full[s]);
+                if (i + 1 < tiles) {
+                    load(i + 1, kr, c.k, c.k_block, khead);
+                    scales();
+                }
+                if (it >= 2 && !tc_wait(&sm.v_empty[s], parity, fail, timeouts)) goto out;
+                store(vr, sm.v[s]);
+                smem_to_tensor_fence();
+                mbar_arrive(&sm.v_full[s]);
+                if (i + 1 < tiles) load(i + 1, vr, c.v, c.v_block, vhead);
+            }
+        }
+    } else if (warp == 8) {
+        // ---- the products, by one thread
+        if (lane == 0) {
+            constexpr uint32_t kDescS = mma_desc(kTcKeys, false), kDescO = mma_desc(DP, true);
+            const uint32_t q = smem_addr(sm.q);
+            uint32_t it = 0, items = 0;
+            while (walk.next(a, c, group, sm.run_steps)) {
+                const int tiles = walk.tiles();
+                if (tiles == 0) continue;
+                if (!tc_wait(&sm.q_full, items & 1, fail, timeouts)) goto out;
+                ++items;
+                for (int i = 0; i <= tiles; ++i) {
+                    if (i < tiles) {
+                        const uint32_t t = it + i, s = t & 1;
+                        if (!tc_wait(&sm.k_full[s], (t >> 1) & 1, fail, timeouts)) goto out;
+                        tc_fence_after();
+                        const uint32_t k = smem_addr(sm.k[s]);
+#pragma unroll
+                        for (int n = 0; n < DP / 16; ++n) {
+                            const uint32_t at = (n >> 2) * 16384 + (n & 3) * 32;
+                            tc_mma_ss(tmem + kColS + s * 128, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024), kDescS,
+                                      n > 0);
+                        }
+                        tc_commit(&sm.k_empty[s]);
+                        tc_commit(&sm.s_full[s]);
+                    }
+                    if (i > 0) {
+                        const uint32_t t = it + i - 1, s = t & 1;
+                        if (!tc_wait(&sm.v_full[s], (t >> 1) & 1, fail, timeouts)) goto out;
+                        if (!tc_wait(&sm.p_full[s], (t >> 1) & 1, fail, timeouts)) goto out;
+                        tc_fence_after();
+                        const uint32_t v = smem_addr(sm.v[s]);
+#pragma unroll
+                        for (int n = 0; n < kTcKeys / 16; ++n)
+                            tc_mma_ts(tmem + kColO, tmem + kColP + s * 64 + n * 8, smem_desc(v + n * 2048, 16384, 1024),
+                                      kDescO, i > 1 || n > 0);
+                        tc_commit(&sm.v_empty[s]);
+                        tc_commit(&sm.pv_done);
+                    }
+                }
+                it += tiles;
+            }
+        }
+    } else {
+        // ---- the softmax, a thread per row.  After a wait that ran out these
+        // warps go on (every later wait fails at once), so that none of them is
+        // missing at the barriers they share; the results are then void.
+        unsigned *const counters = static_cast<unsigned *>(a.workspace);
+        float *const partial = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kWorkspaceCounters);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        uint32_t it = 0;
+        while (walk.next(a, c, group, sm.run_steps)) {
+            const int tiles = walk.tiles();
+            // the queries: each row scaled by a power of two to a largest
+            // magnitude in [2^12, 2^13), as in qr_kv_split.cuh
+            if (tiles > 0) {
+                constexpr int kRowLanes = DP / 4;
+                const int d = 4 * (lane % kRowLanes);
+#pragma unroll 4
+                for (int i = 0; i < 32; i += 32 / kRowLanes) {
+                    const int rr = warp * 32 + i + lane / kRowLanes, row = walk.row0 + rr;
+                    uint2 raw2 = make_uint2(0, 0);
+                    if (rr < walk.rows && d < dim)
+                        raw2 = *reinterpret_cast<const uint2 *>(
+                            static_cast<const uint16_t *>(a.q) + (walk.x.q0 + row / group) * a.q_token +
+                            (static_cast<long long>(walk.head) * group + row % group) * a.q_head + d);
+                    float f[4] = {widen1(bf16, raw2.x & 0xffff), widen1(bf16, raw2.x >> 16), widen1(bf16, raw2.y & 0xffff),
+                                  widen1(bf16, raw2.y >> 16)};
+                    float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+#pragma unroll
+                    for (int o = kRowLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+                    int e = 0;
+                    if (amax > 0.0f && amax < INFINITY) {
+                        frexpf(amax, &e);
+                        e -= 13;
+                    }
+                    const float down1 = pow2i(-(e / 2)) * (a.scale < 0.0f ? -1.0f : 1.0f), down2 = pow2i(-(e - e / 2));
+                    if (lane % kRowLanes == 0) sm.row_scale[rr] = ldexpf(fabsf(a.scale) * 1.4426950408889634f, e);
+                    *reinterpret_cast<uint2 *>(sm.q + (d >> 6) * 16384 + swizzled(rr, (d & 63) >> 3) + (d & 4) * 2) =
+                        make_uint2(pack_f16(f[0] * down1 * down2, f[1] * down1 * down2),
+                                   pack_f16(f[2] * down1 * down2, f[3] * down1 * down2));
+                }
+                smem_to_tensor_fence();
+                mbar_arrive(&sm.q_full);
+                __syncwarp();
+            }
+            const float row_scale = tiles > 0 ? sm.row_scale[tid] : 0.0f;
+            const bool active = warp * 32 < walk.rows;  // else no row of the warp is the item's
+            const int pos = walk.p0 + (walk.row0 + tid) / group;
+            const int row_end = a.causal ? min(walk.x.kv, pos + 1) : walk.x.kv;
+            const int row_begin = a.window > 0 ? pos - a.window + 1 : 0;
+            const int seen_end = a.causal ? min(walk.x.kv, walk.p0 + (walk.row0 + warp * 32) / group + 1) : walk.x.kv;
+            const int seen_begin = a.window > 0 ? walk.p0 + (walk.row0 + warp * 32 + 31) / group - a.window + 1 : 0;
+            float m = -INFINITY, l = 0.0f;
+            int ve = kLeastExp;
+            for (int i = 0; i < tiles; ++i, ++it) {
+                const int s = it & 1;
+                tc_wait(&sm.s_full[s], (it >> 1) & 1, fail, timeouts);
+                __syncwarp();
+                tc_fence_after();
+                const TcMeta &meta = sm.meta[it & 3];
+                const uint32_t scol = lanes + kColS + s * 128;
+                const int key0 = walk.begin + i * kTcKeys;
+                const bool mask = meta.valid != 0xffu || key0 + kTcKeys > seen_end || key0 < seen_begin;
+                float top = -INFINITY;
+                int e = kLeastExp;
+                if (active) {
+                    // a score below every scale: the maximum of a group of 16
+                    // keys is scaled instead of the scores
+                    e = meta.vexp;
+                    if (!mask) {
+#pragma unroll
+                        for (int cc = 0; cc < 4; ++cc) {
+                            uint32_t v[32];
+                            tc_ld32(scol + cc * 32, v);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int gr = 0; gr < 2; ++gr) {
+                                float x = max_nan(__uint_as_float(v[gr * 16]), __uint_as_float(v[gr * 16 + 1]));
+#pragma unroll
+                                for (int k = 2; k < 16; k += 2)
+                                    x = max3_nan(x, __uint_as_float(v[gr * 16 + k]), __uint_as_float(v[gr * 16 + k + 1]));
+                                top = max_nan(top, x * (row_scale * meta.ks[cc * 2 + gr]));
+                            }
+                        }
+                    } else {
+                        e = kLeastExp;
+#pragma unroll 1
+                        for (int cc = 0; cc < 4; ++cc) {
+                            uint32_t v[32];
+                            tc_ld32(scol + cc * 32, v);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int gr = 0; gr < 2; ++gr) {
+                                const int g8 = cc * 2 + gr, key = key0 + g8 * 16;
+                                const bool ok = meta.valid >> g8 & 1;
+                                float x = -INFINITY;
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    if (ok && key + k < row_end && key + k >= row_begin)
+                                        x = max_nan(x, __uint_as_float(v[gr * 16 + k]));
+                                if (ok && key < row_end && key + 16 > row_begin) {
+                                    top = max_nan(top, x * (row_scale * meta.ks[g8]));
+                                    e = max(e, scale_exp(meta.vs[g8]));
+                                }
+                            }
+                        }
+                    }
+                }
+                // the previous product is done: O may be rescaled, P written
+                if (i > 0) {
+                    tc_wait(&sm.pv_done, (it - 1) & 1, fail, timeouts);
+                    __syncwarp();
+                    tc_fence_after();
+                }
+                if (active) {
+                    const bool grew = !(top <= m + kSlack) || e > ve + kScaleSlack;
+                    if (__any_sync(~0u, grew)) {
+                        const float m_new = grew ? max_nan(m, top) : m;
+                        const int e_new = grew ? max(ve, e) : ve;
+                        const float was = m_new == -INFINITY ? 0.0f : m - m_new;
+                        const float fo = exp2_fast(was + static_cast<float>(ve - e_new));
+                        l *= exp2_fast(was);
+                        m = m_new;
+                        ve = e_new;
+                        if (i > 0) {
+#pragma unroll 1
+                            for (int cc = 0; cc < DP / 32; ++cc) {
+                                uint32_t v[32];
+                                tc_ld32(lanes + kColO + cc * 32, v);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * fo);
+                                tc_st32(lanes + kColO + cc * 32, v);
+                            }
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.0f : -m, up = pow2i(kTcWeightExp - ve);
+                    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+                    for (int cc = 0; cc < 4; ++cc) {
+                        uint32_t v[32], p[16];
+                        tc_ld32(scol + cc * 32, v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int gr = 0; gr < 2; ++gr) {
+                            const int g8 = cc * 2 + gr, key = key0 + g8 * 16;
+                            const float f = row_scale * meta.ks[g8], vs = meta.vs[g8];
+                            // (a group beyond the row's power of two is not seen by it)
+                            const float w = mask && scale_exp(vs) > ve + kScaleSlack ? 0.0f : vs * up;
+                            const bool ok = meta.valid >> g8 & 1;
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) {
+                                float2 y = mul2(make_float2(__uint_as_float(v[gr * 16 + k]), __uint_as_float(v[gr * 16 + k + 1])),
+                                                make_float2(f, f));
+                                if (mask) {
+                                    if (!ok || key + k >= row_end || key + k < row_begin) y.x = -INFINITY;
+                                    if (!ok || key + k + 1 >= row_end || key + k + 1 < row_begin) y.y = -INFINITY;
+                                }
+                                y = add2(y, make_float2(base, base));
+                                y.x = exp2_fast(y.x);
+                                y.y = exp2_fast(y.y);
+                                sum = add2(sum, y);
+                                y = mul2(y, make_float2(w, w));
+                                p[gr * 8 + k / 2] = pack_f16(y.x, y.y);
+                            }
+                        }
+                        tc_st16(lanes + kColP + s * 64 + cc * 16, p);
+                    }
+                    l += sum.x + sum.y;
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(&sm.p_full[s]);
+            }
+
+            // the item's rows
+            auto slot_of = [&](long long cta) { return 2 * cta + (walk.item_first > cta * walk.share ? 1 : 0); };
+            float *const my_slot = partial + slot_of(blockIdx.x) * kTcSlot<DP>;
+            if (tiles > 0) {
+                tc_wait(&sm.pv_done, (it - 1) & 1, fail, timeouts);
+                __syncwarp();
+                tc_fence_after();
+            }
+            if (active) {
+                const float back = pow2i(ve - kTcWeightExp);
+                const int row = walk.row0 + tid;
+                const bool in_item = tid < walk.rows;
+#pragma unroll 1
+                for (int cc = 0; cc < DP / 32; ++cc) {
+                    uint32_t v[32];
+                    if (tiles > 0) {
+                        tc_ld32(lanes + kColO + cc * 32, v);
+                        tc_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = 0;
+                    }
+                    if (in_item) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 y = make_float4(__uint_as_float(v[k]) * back, __uint_as_float(v[k + 1]) * back,
+                                                         __uint_as_float(v[k + 2]) * back, __uint_as_float(v[k + 3]) * back);
+                            if (walk.parts == 1)
+                                attn_write(a, bf16, dim, walk.x.q0 + row / group, walk.head * group + row % group,
+                                           cc * 32 + k, y, m, l);
+                            else
+                                __stcg(reinterpret_cast<float4 *>(my_slot + tid * DP + cc * 32 + k), y);
+                        }
+                    }
+                }
+                if (in_item && walk.parts > 1)
+                    __stcg(reinterpret_cast<float2 *>(my_slot + kTcRows * DP + 2 * tid), make_float2(m, l));
+            }
+            tc_fence_before();
+            if (walk.parts > 1) {
+                // as in qr_kv_split.cuh: groups of kGroup parts, then the groups
+                float *const weight = reinterpret_cast<float *>(sm.q), *const sums = weight + kTcRows * kGroup;
+                static_assert(kTcMostCtas <= kGroup * kGroup && 2 * kTcRows * kGroup * 4 <= S::kTile, "two levels");
+                const int groups = (walk.parts + kGroup - 1) / kGroup;
+                const int my_group = (static_cast<int>(blockIdx.x) - walk.part_first_cta) / kGroup;
+                int at_cta = walk.part_first_cta + my_group * kGroup;
+                int count = min(kGroup, walk.parts - my_group * kGroup), stride = 1;
+                unsigned *counter = counters + slot_of(at_cta);
+                for (int level = 0;; ++level) {
+                    bar_softmax();
+                    if (tid == 0) {
+                        __threadfence();
+                        sm.ticket = atomicInc(counter, static_cast<unsigned>(count - 1));
+                    }
+                    bar_softmax();
+                    if (sm.ticket != static_cast<unsigned>(count - 1)) break;
+                    __threadfence();
+                    for (int i = tid; i < walk.rows * count; i += 128) {
+                        const int rr = i / count, k = i % count;
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
+                            partial + slot_of(at_cta + k * stride) * kTcSlot<DP> + kTcRows * DP + 2 * rr));
+                        weight[rr * kGroup + k] = ml.x;
+                        sums[rr * kGroup + k] = ml.y;
+                    }
+                    bar_softmax();
+                    if (tid < walk.rows) {
+                        float top = -INFINITY, sum = 0.0f;
+                        for (int k = 0; k < count; ++k) top = max_nan(top, weight[tid * kGroup + k]);
+                        for (int k = 0; k < count; ++k) {
+                            const float f = top == -INFINITY ? 0.0f : exp2_fast(weight[tid * kGroup + k] - top);
+                            sum = __fmaf_rn(sums[tid * kGroup + k], f, sum);
+                            weight[tid * kGroup + k] = f;
+                        }
+                        sm.row_scale[tid] = top;
+                        sm.row_sum[tid] = sum;
+                    }
+                    bar_softmax();
+                    const bool last = level == 1 || groups == 1;
+                    float *const to = partial + slot_of(at_cta) * kTcSlot<DP>;
+                    constexpr int kQuads = DP / 4;
+                    for (int i = tid; i < walk.rows * kQuads; i += 128) {
+                        const int rr = i / kQuads, d = i % kQuads * 4, row = walk.row0 + rr;
+                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                        for (int k = 0; k < count; ++k) {
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(
+                                partial + slot_of(at_cta + k * stride) * kTcSlot<DP> + rr * DP + d));
+                            const float f = weight[rr * kGroup + k];
+                            v.x = __fmaf_rn(y.x, f, v.x), v.y = __fmaf_rn(y.y, f, v.y);
+                            v.z = __fmaf_rn(y.z, f, v.z), v.w = __fmaf_rn(y.w, f, v.w);
+                        }
+                        if (last) {
+                            attn_write(a, bf16, dim, walk.x.q0 + row / group, walk.head * group + row % group, d, v,
+                                       sm.row_scale[rr], sm.row_sum[rr]);
+                        } else {
+                            __stcg(reinterpret_cast<float4 *>(to + rr * DP + d), v);
+                            if (d == 0)
+                                __stcg(reinterpret_cast<float2 *>(to + kTcRows * DP + 2 * rr),
+                                       make_float2(sm.row_scale[rr], sm.row_sum[rr]));
+                        }
+                    }
+                    if (last) break;
+                    counter = counters + 2 * kMostCtas + slot_of(walk.part_first_cta);
+                    at_cta = walk.part_first_cta;
+                    count = groups;
+                    stride = kGroup;
+                }
+                bar_softmax();  // the queries' tile and row_scale are free again
+            }
+        }
+    }
+out:
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tc_free(tmem, kColumns);
+}
+
+template <int DP, bool FULL>
+cudaError_t run_kv_tc(int dtype, const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {
+    auto kern = kv_attention_tc_kernel<DP, FULL>;
+    const int bytes = sizeof(TcSmem<DP>) + 1024;
+    cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(kern), bytes);
+    if (err != cudaSuccess) return err;
+    const int sms = sm_count(&err);
+    if (sms <= 0) return err;
+    unsigned *timeouts = wait_timeout_counter(&err);
+    if (!timeouts) return err;
+    return launch_chained(kern, static_cast<unsigned>(sms < kTcMostCtas ? sms : kTcMostCtas), kTcThreads, bytes, s, a, c,
+                          dtype != 0, group, timeouts);
+}
+
+}  // namespace qrk

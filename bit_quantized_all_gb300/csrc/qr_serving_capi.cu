@@ -164,7 +164,9 @@ QR_EXPORT qr_status_t qr_kv_attention(qr_dtype_t dtype, int requests, int64_t to
     if (requests > 65536 || q_heads % cache->heads || q_heads > 65535) return QR_ERR_UNSUPPORTED;
     // positions minus a window stay within an int
     constexpr int kFar = 1 << 30;
-    if (int64_t(table_width) * cache->block_size > INT_MAX - 512 || tokens > kFar) return QR_ERR_SIZE;
+    if (int64_t(table_width) * cache->block_size > INT_MAX - 512 || tokens > kFar ||
+        tokens * (q_heads / cache->heads) > kFar)
+        return QR_ERR_SIZE;
     const size_t need = attention_workspace(requests, tokens, q_heads, cache->heads, cache->head_dim);
     const size_t nq = extent(tokens, q_heads, cache->head_dim, q_token_stride, q_head_stride);
     const size_t no = extent(tokens, q_heads, cache->head_dim, out_token_stride, out_head_stride);
