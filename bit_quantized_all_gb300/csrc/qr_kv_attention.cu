@@ -6,10 +6,13 @@ namespace qrk {
 // The tcgen05 kernel (qr_kv_tc.cu), for head_dim up to 128.
 cudaError_t launch_kv_tc(int dtype, const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s);
 
-size_t kv_attention_workspace(int, long long, int, int, int head_dim) {
-    // two slots per CTA: 640 CTAs of up to 32 rows, or 160 of 128
+size_t kv_attention_workspace(int, long long tokens, int q_heads, int heads, int head_dim) {
+    // two slots per CTA: of at most 640 CTAs of up to 32 rows (16 above 128
+    // dimensions), or of 160 of up to 256
     const size_t dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-    return kWorkspaceCounters + size_t(2 * kMostCtas) * (dp <= 128 ? 32 : 16) * (dp + 2) * 4;
+    size_t rows = size_t(2 * kMostCtas) * (dp <= 128 ? 32 : 16);
+    if (dp <= 128 && tokens * (q_heads / heads) > 16) rows = size_t(2 * 160) * 256;
+    return kWorkspaceCounters + rows * (dp + 2) * 4;
 }
 
 template <int DP, int NT>

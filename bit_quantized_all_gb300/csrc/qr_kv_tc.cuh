@@ -1,27 +1,27 @@
 // qr_kv_tc.cuh -- attention over the 8-bit paged cache for many query rows, on
 // tcgen05.
 //
-// An item is 128 query rows (a row is a query token and one of the group's
-// heads) of one request and key/value head; its keys are taken 128 at a time.
-// As in qr_kv_split.cuh the items' key tiles are cut into equal shares, one
-// per CTA (here counting only tiles that some row sees), and the parts of a
-// divided item are joined by whichever CTA brings the last one.
+// An item is 256 query rows (a row is a query token and one of the group's
+// heads) of one request and key/value head, in two halves of 128; its keys are
+// taken 128 at a time.  As in qr_kv_split.cuh the items' key tiles are cut into
+// equal shares, one per CTA (here counting only tiles that some row sees), and
+// the parts of a divided item are joined by whichever CTA brings the last one.
 //
-// A CTA is nine warps.  Four convert: each tile's codes come through registers
-// and go to shared memory as fp16 (exact), double buffered.  One thread issues
-// the products: S = Q K^T into one of two halves of tensor memory, then
-// O += P V with P read from tensor memory.  Four warps, a thread per row, do
-// the softmax: S is read twice (maximum, then weights, which are written back
-// as fp16), so a thread holds 32 values at a time.  The next tile's S is
-// computed while a tile's weights are.
+// A CTA is thirteen warps.  Four convert: each tile's codes come through
+// registers and go to shared memory as fp16 (exact), double buffered; both
+// halves use them.  One thread issues the products, S = Q K^T and O += P V,
+// with S, P and O in tensor memory.  Four warps per half, a thread per row, do
+// the softmax: S is read twice (maximum, then weights, which replace it as
+// fp16), 32 values at a time with the next 32 on their way.  While one half's
+// weights are computed, the tensor cores work on the other's products.
 //
 // O stays in tensor memory.  It is rescaled only when a row's maximum has
 // grown by more than 2^kSlack, or the power of two under which the values'
 // scales are kept by more than 2^kScaleSlack; weights are then below 2^15, and
 // fp16 keeps them exact to 2^-11 down to 2^-21 of a weight of 1.
 //
-// What bounds it: the tensor cores and, close behind, the softmax (about 800
-// issue slots per scheduler and tile against 1024 cycles of products).
+// What bounds it: the tensor cores (2048 cycles a tile for both halves) and,
+// close behind, instruction issue (softmax and conversion).
 #pragma once
 
 #include "qr_kv_split.cuh"
@@ -29,15 +29,15 @@
 
 namespace qrk {
 
-constexpr int kTcRows = 128, kTcKeys = 128;
-constexpr int kTcThreads = 288;
+constexpr int kTcRows = 256, kTcHalf = 128, kTcKeys = 128;
+constexpr int kTcThreads = 416;  // warps 0-7 softmax, 8-11 conversion, 12 products
 constexpr int kTcMostCtas = 160;
 constexpr float kSlack = 6.0f;
 constexpr int kScaleSlack = 2;
 constexpr int kTcWeightExp = 7;  // weight 1 of the largest scale is 2^7
 
-// Tensor memory columns: S twice, O, P twice.
-constexpr uint32_t kColS = 0, kColO = 256, kColP = 384, kColumns = 512;
+// Tensor memory columns: S of both halves (P in its place), O of both halves.
+constexpr uint32_t kColS = 0, kColO = 256, kColumns = 512;
 
 struct TcMeta {
     float ks[8], vs[8];
@@ -49,20 +49,22 @@ struct TcMeta {
 template <int DP>
 struct TcSmem {
     static constexpr int kSlabs = DP / 64, kTile = kSlabs * 16384;  // 128 rows of fp16
-    uint8_t q[kTile];
+    uint8_t q[2][kTile];
     uint8_t k[2][kTile];
     uint8_t v[2][kTile];
     TcMeta meta[4];
     float row_scale[kTcRows], row_sum[kTcRows];
     long long run_steps[128], warp_sums[4];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done, q_full;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // by buffer
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];    // by half
     uint32_t tmem;
-    unsigned ticket;
+    unsigned ticket[2];
     int fail;
 };
 
+// Floats of one half's part: accumulators, then (max, sum) pairs.
 template <int DP>
-constexpr int kTcSlot = kTcRows * (DP + 2);
+constexpr int kTcSlot = kTcHalf * (DP + 2);
 
 // The items of a CTA's share, in order; every thread keeps its own copy.
 struct TcWalk {
@@ -127,6 +129,28 @@ struct TcWalk {
     __device__ __forceinline__ int tiles() const { return end > begin ? (end - begin + kTcKeys - 1) / kTcKeys : 0; }
 };
 
+// Eight of a row's values from dimension d on, and with d = 0 its lse.
+__device__ __forceinline__ void attn_write8(const KvAttentionArgs &a, bool bf16, int dim, long long token, int head, int d,
+                                            const float *v, float top, float sum) {
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (d < dim) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (bf16) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i] * inv, v[2 * i + 1] * inv);
+                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            } else {
+                w[i] = pack_f16(v[2 * i] * inv, v[2 * i + 1] * inv);
+            }
+        }
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + token * a.out_token + head * a.out_head + d) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (a.lse && d == 0)
+        a.lse[token * a.q_heads + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+}
+
 // Waits for a phase; after a wait that ran out every wait of the CTA fails.
 __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -136,7 +160,8 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *fai
     return false;
 }
 
-__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The 128 threads of one half's softmax.
+__device__ __forceinline__ void bar_half(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 
 template <int DP, bool FULL>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -174,15 +199,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_init(&sm.v_full[i], 128);
                 mbar_init(&sm.k_empty[i], 1);
                 mbar_init(&sm.v_empty[i], 1);
+                mbar_init(&sm.q_full[i], 128);
                 mbar_init(&sm.s_full[i], 1);
                 mbar_init(&sm.p_full[i], 128);
+                mbar_init(&sm.o_full[i], 1);
             }
-            mbar_init(&sm.pv_done, 1);
-            mbar_init(&sm.q_full, 128);
             mbar_init_fence();
             sm.fail = 0;
         }
-        if (warp == 8) tc_alloc(&sm.tmem, kColumns);
+        if (warp == 12) tc_alloc(&sm.tmem, kColumns);
         __syncthreads();
         if (tid < 128) {
             long long before = 0;
@@ -207,9 +232,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     int *const fail = &sm.fail;
 
-    if (warp >= 4 && warp < 8) {
+    if (warp >= 8 && warp < 12) {
         // ---- the codes, through registers, to fp16 tiles in shared memory
-        const int ct = tid - 128;
+        const int ct = tid - 256;
         constexpr int kPer = DP / 16;           // 16-byte pieces of a padded row; also passes
         constexpr int kPassRows = 128 / kPer;
         const int q_l = ct % kPer, row_l = ct / kPer;
@@ -291,8 +316,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (i + 1 < tiles) ids(i + 1);
                 if (it >= 2 && !tc_wait(&sm.k_empty[s], parity, fail, timeouts)) goto out;
                 store(kr, sm.k[s]);
-                if (warp == 4) {
-                    // (entry it % 4: tile it - 4's softmax is done before K of
+                if (warp == 8) {
+                    // (entry it % 4: tile it - 3's softmax is done before K of
                     // tile it may be written)
                     TcMeta &meta = sm.meta[it & 3];
                     const uint32_t valid = __ballot_sync(~0u, ct < 8 && !bad);
@@ -321,44 +346,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (i + 1 < tiles) load(i + 1, vr, c.v, c.v_block, vhead);
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == 12) {
         // ---- the products, by one thread
         if (lane == 0) {
             constexpr uint32_t kDescS = mma_desc(kTcKeys, false), kDescO = mma_desc(DP, true);
-            const uint32_t q = smem_addr(sm.q);
-            uint32_t it = 0, items = 0;
+            uint32_t it = 0, count[2] = {0, 0}, items[2] = {0, 0};
             while (walk.next(a, c, group, sm.run_steps)) {
-                const int tiles = walk.tiles();
+                const int tiles = walk.tiles(), halves = walk.rows > kTcHalf ? 2 : 1;
                 if (tiles == 0) continue;
-                if (!tc_wait(&sm.q_full, items & 1, fail, timeouts)) goto out;
-                ++items;
                 for (int i = 0; i <= tiles; ++i) {
-                    if (i < tiles) {
-                        const uint32_t t = it + i, s = t & 1;
-                        if (!tc_wait(&sm.k_full[s], (t >> 1) & 1, fail, timeouts)) goto out;
-                        tc_fence_after();
-                        const uint32_t k = smem_addr(sm.k[s]);
+                    const uint32_t t = it + i, s = t & 1, was = s ^ 1;
+                    for (int h = 0; h < halves; ++h) {
+                        if (i > 0) {
+                            // O += P V of the tile before
+                            if (h == 0 && !tc_wait(&sm.v_full[was], ((t - 1) >> 1) & 1, fail, timeouts)) goto out;
+                            if (!tc_wait(&sm.p_full[h], count[h] & 1, fail, timeouts)) goto out;
+                            ++count[h];
+                            tc_fence_after();
+                            const uint32_t v = smem_addr(sm.v[was]);
 #pragma unroll
-                        for (int n = 0; n < DP / 16; ++n) {
-                            const uint32_t at = (n >> 2) * 16384 + (n & 3) * 32;
-                            tc_mma_ss(tmem + kColS + s * 128, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024), kDescS,
-                                      n > 0);
+                            for (int n = 0; n < kTcKeys / 16; ++n)
+                                tc_mma_ts(tmem + kColO + h * 128, tmem + kColS + h * 128 + n * 8,
+                                          smem_desc(v + n * 2048, 16384, 1024), kDescO, i > 1 || n > 0);
+                            if (h == halves - 1) tc_commit(&sm.v_empty[was]);
+                            if (i == tiles) tc_commit(&sm.o_full[h]);
                         }
-                        tc_commit(&sm.k_empty[s]);
-                        tc_commit(&sm.s_full[s]);
-                    }
-                    if (i > 0) {
-                        const uint32_t t = it + i - 1, s = t & 1;
-                        if (!tc_wait(&sm.v_full[s], (t >> 1) & 1, fail, timeouts)) goto out;
-                        if (!tc_wait(&sm.p_full[s], (t >> 1) & 1, fail, timeouts)) goto out;
-                        tc_fence_after();
-                        const uint32_t v = smem_addr(sm.v[s]);
+                        if (i < tiles) {
+                            // S = Q K^T of this tile
+                            if (h == 0 && !tc_wait(&sm.k_full[s], (t >> 1) & 1, fail, timeouts)) goto out;
+                            if (i == 0) {
+                                if (!tc_wait(&sm.q_full[h], items[h] & 1, fail, timeouts)) goto out;
+                                ++items[h];
+                            }
+                            tc_fence_after();
+                            const uint32_t k = smem_addr(sm.k[s]), q = smem_addr(sm.q[h]);
 #pragma unroll
-                        for (int n = 0; n < kTcKeys / 16; ++n)
-                            tc_mma_ts(tmem + kColO, tmem + kColP + s * 64 + n * 8, smem_desc(v + n * 2048, 16384, 1024),
-                                      kDescO, i > 1 || n > 0);
-                        tc_commit(&sm.v_empty[s]);
-                        tc_commit(&sm.pv_done);
+                            for (int n = 0; n < DP / 16; ++n) {
+                                const uint32_t at = (n >> 2) * 16384 + (n & 3) * 32;
+                                tc_mma_ss(tmem + kColS + h * 128, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024),
+                                          kDescS, n > 0);
+                            }
+                            tc_commit(&sm.s_full[h]);
+                            if (h == halves - 1) tc_commit(&sm.k_empty[s]);
+                        }
                     }
                 }
                 it += tiles;
@@ -370,89 +400,110 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // missing at the barriers they share; the results are then void.
         unsigned *const counters = static_cast<unsigned *>(a.workspace);
         float *const partial = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kWorkspaceCounters);
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        uint32_t it = 0;
+        const int half = warp >> 2, hw = warp & 3, ht = tid & 127;  // half, warp and thread within it
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(hw * 32) << 16);
+        const uint32_t scol = lanes + kColS + half * 128, ocol = lanes + kColO + half * 128;
+        float *const row_scales = sm.row_scale + half * kTcHalf;
+        uint32_t it = 0, mine = 0, items = 0;  // tiles of all halves, of this one; its items
         while (walk.next(a, c, group, sm.run_steps)) {
-            const int tiles = walk.tiles();
+            const int tiles = walk.tiles(), rows = min(kTcHalf, walk.rows - half * kTcHalf), row0 = walk.row0 + half * kTcHalf;
+            if (rows <= 0) {
+                it += tiles;
+                continue;
+            }
             // the queries: each row scaled by a power of two to a largest
-            // magnitude in [2^12, 2^13), as in qr_kv_split.cuh
+            // magnitude in [2^12, 2^13), as in qr_kv_split.cuh; kBatch loads of
+            // a thread at a time
             if (tiles > 0) {
-                constexpr int kRowLanes = DP / 4;
+                constexpr int kRowLanes = DP / 4, kBatch = 16, kRowsStep = 32 / kRowLanes;
                 const int d = 4 * (lane % kRowLanes);
-#pragma unroll 4
-                for (int i = 0; i < 32; i += 32 / kRowLanes) {
-                    const int rr = warp * 32 + i + lane / kRowLanes, row = walk.row0 + rr;
-                    uint2 raw2 = make_uint2(0, 0);
-                    if (rr < walk.rows && d < dim)
-                        raw2 = *reinterpret_cast<const uint2 *>(
-                            static_cast<const uint16_t *>(a.q) + (walk.x.q0 + row / group) * a.q_token +
-                            (static_cast<long long>(walk.head) * group + row % group) * a.q_head + d);
-                    float f[4] = {widen1(bf16, raw2.x & 0xffff), widen1(bf16, raw2.x >> 16), widen1(bf16, raw2.y & 0xffff),
-                                  widen1(bf16, raw2.y >> 16)};
-                    float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32; i0 += kBatch * kRowsStep) {
+                    uint2 raw2[kBatch];
 #pragma unroll
-                    for (int o = kRowLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-                    int e = 0;
-                    if (amax > 0.0f && amax < INFINITY) {
-                        frexpf(amax, &e);
-                        e -= 13;
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int rr = hw * 32 + i0 + u * kRowsStep + lane / kRowLanes, row = row0 + rr;
+                        raw2[u] = make_uint2(0, 0);
+                        if (rr < rows && d < dim) {
+                            const int token = row / group;
+                            raw2[u] = *reinterpret_cast<const uint2 *>(
+                                static_cast<const uint16_t *>(a.q) + (walk.x.q0 + token) * a.q_token +
+                                (static_cast<long long>(walk.head) * group + (row - token * group)) * a.q_head + d);
+                        }
                     }
-                    const float down1 = pow2i(-(e / 2)) * (a.scale < 0.0f ? -1.0f : 1.0f), down2 = pow2i(-(e - e / 2));
-                    if (lane % kRowLanes == 0) sm.row_scale[rr] = ldexpf(fabsf(a.scale) * 1.4426950408889634f, e);
-                    *reinterpret_cast<uint2 *>(sm.q + (d >> 6) * 16384 + swizzled(rr, (d & 63) >> 3) + (d & 4) * 2) =
-                        make_uint2(pack_f16(f[0] * down1 * down2, f[1] * down1 * down2),
-                                   pack_f16(f[2] * down1 * down2, f[3] * down1 * down2));
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int rr = hw * 32 + i0 + u * kRowsStep + lane / kRowLanes;
+                        const float f[4] = {widen1(bf16, raw2[u].x & 0xffff), widen1(bf16, raw2[u].x >> 16),
+                                            widen1(bf16, raw2[u].y & 0xffff), widen1(bf16, raw2[u].y >> 16)};
+                        float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+#pragma unroll
+                        for (int o = kRowLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+                        int e = 0;
+                        if (amax > 0.0f && amax < INFINITY) {
+                            frexpf(amax, &e);
+                            e -= 13;
+                        }
+                        const float down1 = pow2i(-(e / 2)) * (a.scale < 0.0f ? -1.0f : 1.0f), down2 = pow2i(-(e - e / 2));
+                        if (lane % kRowLanes == 0) row_scales[rr] = ldexpf(fabsf(a.scale) * 1.4426950408889634f, e);
+                        *reinterpret_cast<uint2 *>(sm.q[half] + (d >> 6) * 16384 + swizzled(rr, (d & 63) >> 3) + (d & 4) * 2) =
+                            make_uint2(pack_f16(f[0] * down1 * down2, f[1] * down1 * down2),
+                                       pack_f16(f[2] * down1 * down2, f[3] * down1 * down2));
+                    }
                 }
                 smem_to_tensor_fence();
-                mbar_arrive(&sm.q_full);
+                mbar_arrive(&sm.q_full[half]);
                 __syncwarp();
             }
-            const float row_scale = tiles > 0 ? sm.row_scale[tid] : 0.0f;
-            const bool active = warp * 32 < walk.rows;  // else no row of the warp is the item's
-            const int pos = walk.p0 + (walk.row0 + tid) / group;
+            const float row_scale = tiles > 0 ? row_scales[ht] : 0.0f;
+            const bool active = hw * 32 < rows;  // else no row of the warp is the item's
+            const int pos = walk.p0 + (row0 + ht) / group;
             const int row_end = a.causal ? min(walk.x.kv, pos + 1) : walk.x.kv;
             const int row_begin = a.window > 0 ? pos - a.window + 1 : 0;
-            const int seen_end = a.causal ? min(walk.x.kv, walk.p0 + (walk.row0 + warp * 32) / group + 1) : walk.x.kv;
-            const int seen_begin = a.window > 0 ? walk.p0 + (walk.row0 + warp * 32 + 31) / group - a.window + 1 : 0;
+            // keys that every row of the warp sees
+            const int seen_end = __reduce_min_sync(~0u, row_end), seen_begin = __reduce_max_sync(~0u, row_begin);
             float m = -INFINITY, l = 0.0f;
             int ve = kLeastExp;
-            for (int i = 0; i < tiles; ++i, ++it) {
-                const int s = it & 1;
-                tc_wait(&sm.s_full[s], (it >> 1) & 1, fail, timeouts);
+            for (int i = 0; i < tiles; ++i, ++it, ++mine) {
+                tc_wait(&sm.s_full[half], mine & 1, fail, timeouts);
                 __syncwarp();
                 tc_fence_after();
-                const TcMeta &meta = sm.meta[it & 3];
-                const uint32_t scol = lanes + kColS + s * 128;
-                const int key0 = walk.begin + i * kTcKeys;
-                const bool mask = meta.valid != 0xffu || key0 + kTcKeys > seen_end || key0 < seen_begin;
-                float top = -INFINITY;
-                int e = kLeastExp;
+                // S is there, and with it the product before is done: O may be
+                // rescaled, P written
                 if (active) {
-                    // a score below every scale: the maximum of a group of 16
-                    // keys is scaled instead of the scores
-                    e = meta.vexp;
+                    const TcMeta &meta = sm.meta[it & 3];
+                    const int key0 = walk.begin + i * kTcKeys;
+                    const bool mask = meta.valid != 0xffu || key0 + kTcKeys > seen_end || key0 < seen_begin;
+                    float top = -INFINITY;
+                    int e;
+                    uint32_t v[2][32];
+                    tc_ld32(scol, v[0]);
                     if (!mask) {
+                        // scales are not negative: a group's largest score is
+                        // its largest product, scaled
+                        e = meta.vexp;
 #pragma unroll
                         for (int cc = 0; cc < 4; ++cc) {
-                            uint32_t v[32];
-                            tc_ld32(scol + cc * 32, v);
-                            tc_wait_ld();
+                            tc_wait_ld(v[cc & 1]);
+                            if (cc < 3) tc_ld32(scol + (cc + 1) * 32, v[(cc + 1) & 1]);
 #pragma unroll
                             for (int gr = 0; gr < 2; ++gr) {
-                                float x = max_nan(__uint_as_float(v[gr * 16]), __uint_as_float(v[gr * 16 + 1]));
+                                const uint32_t *w = v[cc & 1] + gr * 16;
+                                float x[4];
 #pragma unroll
-                                for (int k = 2; k < 16; k += 2)
-                                    x = max3_nan(x, __uint_as_float(v[gr * 16 + k]), __uint_as_float(v[gr * 16 + k + 1]));
-                                top = max_nan(top, x * (row_scale * meta.ks[cc * 2 + gr]));
+                                for (int k = 0; k < 4; ++k)
+                                    x[k] = max3_nan(max_nan(__uint_as_float(w[4 * k]), __uint_as_float(w[4 * k + 1])),
+                                                    __uint_as_float(w[4 * k + 2]), __uint_as_float(w[4 * k + 3]));
+                                const float y = max3_nan(max_nan(x[0], x[1]), x[2], x[3]);
+                                top = max_nan(top, y * (row_scale * meta.ks[cc * 2 + gr]));
                             }
                         }
                     } else {
                         e = kLeastExp;
-#pragma unroll 1
+#pragma unroll
                         for (int cc = 0; cc < 4; ++cc) {
-                            uint32_t v[32];
-                            tc_ld32(scol + cc * 32, v);
-                            tc_wait_ld();
+                            tc_wait_ld(v[cc & 1]);
+                            if (cc < 3) tc_ld32(scol + (cc + 1) * 32, v[(cc + 1) & 1]);
 #pragma unroll
                             for (int gr = 0; gr < 2; ++gr) {
                                 const int g8 = cc * 2 + gr, key = key0 + g8 * 16;
@@ -461,7 +512,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                                 for (int k = 0; k < 16; ++k)
                                     if (ok && key + k < row_end && key + k >= row_begin)
-                                        x = max_nan(x, __uint_as_float(v[gr * 16 + k]));
+                                        x = max_nan(x, __uint_as_float(v[cc & 1][gr * 16 + k]));
                                 if (ok && key < row_end && key + 16 > row_begin) {
                                     top = max_nan(top, x * (row_scale * meta.ks[g8]));
                                     e = max(e, scale_exp(meta.vs[g8]));
@@ -469,14 +520,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                     }
-                }
-                // the previous product is done: O may be rescaled, P written
-                if (i > 0) {
-                    tc_wait(&sm.pv_done, (it - 1) & 1, fail, timeouts);
-                    __syncwarp();
-                    tc_fence_after();
-                }
-                if (active) {
                     const bool grew = !(top <= m + kSlack) || e > ve + kScaleSlack;
                     if (__any_sync(~0u, grew)) {
                         const float m_new = grew ? max_nan(m, top) : m;
@@ -489,162 +532,184 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (i > 0) {
 #pragma unroll 1
                             for (int cc = 0; cc < DP / 32; ++cc) {
-                                uint32_t v[32];
-                                tc_ld32(lanes + kColO + cc * 32, v);
-                                tc_wait_ld();
+                                tc_ld32(ocol + cc * 32, v[0]);
+                                tc_wait_ld(v[0]);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * fo);
-                                tc_st32(lanes + kColO + cc * 32, v);
+                                for (int k = 0; k < 32; ++k) v[0][k] = __float_as_uint(__uint_as_float(v[0][k]) * fo);
+                                tc_st32(ocol + cc * 32, v[0]);
                             }
                         }
                     }
                     const float base = m == -INFINITY ? 0.0f : -m, up = pow2i(kTcWeightExp - ve);
-                    float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll 1
-                    for (int cc = 0; cc < 4; ++cc) {
-                        uint32_t v[32], p[16];
-                        tc_ld32(scol + cc * 32, v);
-                        tc_wait_ld();
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    auto weigh = [&](const uint32_t (&sv)[32], int cc, auto masked) {
+                        constexpr bool kMasked = decltype(masked)::value;
+                        uint32_t p[16];
 #pragma unroll
                         for (int gr = 0; gr < 2; ++gr) {
                             const int g8 = cc * 2 + gr, key = key0 + g8 * 16;
                             const float f = row_scale * meta.ks[g8], vs = meta.vs[g8];
                             // (a group beyond the row's power of two is not seen by it)
-                            const float w = mask && scale_exp(vs) > ve + kScaleSlack ? 0.0f : vs * up;
-                            const bool ok = meta.valid >> g8 & 1;
+                            const float w = kMasked && scale_exp(vs) > ve + kScaleSlack ? 0.0f : vs * up;
+                            const bool ok = !kMasked || (meta.valid >> g8 & 1);
 #pragma unroll
                             for (int k = 0; k < 16; k += 2) {
-                                float2 y = mul2(make_float2(__uint_as_float(v[gr * 16 + k]), __uint_as_float(v[gr * 16 + k + 1])),
+                                float2 y = mul2(make_float2(__uint_as_float(sv[gr * 16 + k]), __uint_as_float(sv[gr * 16 + k + 1])),
                                                 make_float2(f, f));
-                                if (mask) {
+                                if (kMasked) {
                                     if (!ok || key + k >= row_end || key + k < row_begin) y.x = -INFINITY;
                                     if (!ok || key + k + 1 >= row_end || key + k + 1 < row_begin) y.y = -INFINITY;
                                 }
                                 y = add2(y, make_float2(base, base));
                                 y.x = exp2_fast(y.x);
                                 y.y = exp2_fast(y.y);
-                                sum = add2(sum, y);
+                                sum[gr] = add2(sum[gr], y);
                                 y = mul2(y, make_float2(w, w));
                                 p[gr * 8 + k / 2] = pack_f16(y.x, y.y);
                             }
                         }
-                        tc_st16(lanes + kColP + s * 64 + cc * 16, p);
+                        // P of 32 keys takes 16 columns, all of them read before
+                        tc_st16(scol + cc * 16, p);
+                    };
+                    tc_ld32(scol, v[0]);
+                    if (!mask) {
+#pragma unroll
+                        for (int cc = 0; cc < 4; ++cc) {
+                            tc_wait_ld(v[cc & 1]);
+                            if (cc < 3) tc_ld32(scol + (cc + 1) * 32, v[(cc + 1) & 1]);
+                            weigh(v[cc & 1], cc, std::false_type());
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int cc = 0; cc < 4; ++cc) {
+                            tc_wait_ld(v[0]);
+                            weigh(v[0], cc, std::true_type());
+                            if (cc < 3) tc_ld32(scol + (cc + 1) * 32, v[0]);
+                        }
                     }
-                    l += sum.x + sum.y;
+                    l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                     tc_wait_st();
                 }
                 tc_fence_before();
-                mbar_arrive(&sm.p_full[s]);
+                mbar_arrive(&sm.p_full[half]);
             }
 
             // the item's rows
             auto slot_of = [&](long long cta) { return 2 * cta + (walk.item_first > cta * walk.share ? 1 : 0); };
-            float *const my_slot = partial + slot_of(blockIdx.x) * kTcSlot<DP>;
+            auto part_of = [&](long long cta) { return partial + (slot_of(cta) * 2 + half) * kTcSlot<DP>; };
+            float *const my_part = part_of(blockIdx.x);
             if (tiles > 0) {
-                tc_wait(&sm.pv_done, (it - 1) & 1, fail, timeouts);
+                tc_wait(&sm.o_full[half], items & 1, fail, timeouts);
+                ++items;
                 __syncwarp();
                 tc_fence_after();
             }
             if (active) {
                 const float back = pow2i(ve - kTcWeightExp);
-                const int row = walk.row0 + tid;
-                const bool in_item = tid < walk.rows;
+                const int row = row0 + ht, token = row / group;
+                const bool in_item = ht < rows;
+                const long long out_token = walk.x.q0 + token;
+                const int out_head = walk.head * group + (row - token * group);
 #pragma unroll 1
                 for (int cc = 0; cc < DP / 32; ++cc) {
                     uint32_t v[32];
                     if (tiles > 0) {
-                        tc_ld32(lanes + kColO + cc * 32, v);
-                        tc_wait_ld();
+                        tc_ld32(ocol + cc * 32, v);
+                        tc_wait_ld(v);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] = 0;
                     }
                     if (in_item) {
+                        float y[32];
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 y = make_float4(__uint_as_float(v[k]) * back, __uint_as_float(v[k + 1]) * back,
-                                                         __uint_as_float(v[k + 2]) * back, __uint_as_float(v[k + 3]) * back);
-                            if (walk.parts == 1)
-                                attn_write(a, bf16, dim, walk.x.q0 + row / group, walk.head * group + row % group,
-                                           cc * 32 + k, y, m, l);
-                            else
-                                __stcg(reinterpret_cast<float4 *>(my_slot + tid * DP + cc * 32 + k), y);
+                        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(v[k]) * back;
+                        if (walk.parts == 1) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 8)
+                                attn_write8(a, bf16, dim, out_token, out_head, cc * 32 + k, y + k, m, l);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4)
+                                __stcg(reinterpret_cast<float4 *>(my_part + ht * DP + cc * 32 + k),
+                                       make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]));
                         }
                     }
                 }
                 if (in_item && walk.parts > 1)
-                    __stcg(reinterpret_cast<float2 *>(my_slot + kTcRows * DP + 2 * tid), make_float2(m, l));
+                    __stcg(reinterpret_cast<float2 *>(my_part + kTcHalf * DP + 2 * ht), make_float2(m, l));
             }
             tc_fence_before();
             if (walk.parts > 1) {
-                // as in qr_kv_split.cuh: groups of kGroup parts, then the groups
-                float *const weight = reinterpret_cast<float *>(sm.q), *const sums = weight + kTcRows * kGroup;
-                static_assert(kTcMostCtas <= kGroup * kGroup && 2 * kTcRows * kGroup * 4 <= S::kTile, "two levels");
+                // as in qr_kv_split.cuh: groups of kGroup parts, then the groups,
+                // each half for itself
+                float *const weight = reinterpret_cast<float *>(sm.q[half]), *const sums = weight + kTcHalf * kGroup;
+                static_assert(kTcMostCtas <= kGroup * kGroup && 2 * kTcHalf * kGroup * 4 <= S::kTile, "two levels");
+                static_assert(2 * 4 * kTcMostCtas * 4 <= kWorkspaceCounters, "two counters per slot and half");
+                float *const row_sums = sm.row_sum + half * kTcHalf;
                 const int groups = (walk.parts + kGroup - 1) / kGroup;
                 const int my_group = (static_cast<int>(blockIdx.x) - walk.part_first_cta) / kGroup;
                 int at_cta = walk.part_first_cta + my_group * kGroup;
                 int count = min(kGroup, walk.parts - my_group * kGroup), stride = 1;
-                unsigned *counter = counters + slot_of(at_cta);
+                unsigned *counter = counters + slot_of(at_cta) * 2 + half;
                 for (int level = 0;; ++level) {
-                    bar_softmax();
-                    if (tid == 0) {
+                    bar_half(half);
+                    if (ht == 0) {
                         __threadfence();
-                        sm.ticket = atomicInc(counter, static_cast<unsigned>(count - 1));
+                        sm.ticket[half] = atomicInc(counter, static_cast<unsigned>(count - 1));
                     }
-                    bar_softmax();
-                    if (sm.ticket != static_cast<unsigned>(count - 1)) break;
+                    bar_half(half);
+                    if (sm.ticket[half] != static_cast<unsigned>(count - 1)) break;
                     __threadfence();
-                    for (int i = tid; i < walk.rows * count; i += 128) {
+                    for (int i = ht; i < rows * count; i += kTcHalf) {
                         const int rr = i / count, k = i % count;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
-                            partial + slot_of(at_cta + k * stride) * kTcSlot<DP> + kTcRows * DP + 2 * rr));
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_of(at_cta + k * stride) + kTcHalf * DP + 2 * rr));
                         weight[rr * kGroup + k] = ml.x;
                         sums[rr * kGroup + k] = ml.y;
                     }
-                    bar_softmax();
-                    if (tid < walk.rows) {
+                    bar_half(half);
+                    if (ht < rows) {
                         float top = -INFINITY, sum = 0.0f;
-                        for (int k = 0; k < count; ++k) top = max_nan(top, weight[tid * kGroup + k]);
+                        for (int k = 0; k < count; ++k) top = max_nan(top, weight[ht * kGroup + k]);
                         for (int k = 0; k < count; ++k) {
-                            const float f = top == -INFINITY ? 0.0f : exp2_fast(weight[tid * kGroup + k] - top);
-                            sum = __fmaf_rn(sums[tid * kGroup + k], f, sum);
-                            weight[tid * kGroup + k] = f;
+                            const float f = top == -INFINITY ? 0.0f : exp2_fast(weight[ht * kGroup + k] - top);
+                            sum = __fmaf_rn(sums[ht * kGroup + k], f, sum);
+                            weight[ht * kGroup + k] = f;
                         }
-                        sm.row_scale[tid] = top;
-                        sm.row_sum[tid] = sum;
+                        row_scales[ht] = top;
+                        row_sums[ht] = sum;
                     }
-                    bar_softmax();
+                    bar_half(half);
                     const bool last = level == 1 || groups == 1;
-                    float *const to = partial + slot_of(at_cta) * kTcSlot<DP>;
+                    float *const to = part_of(at_cta);
                     constexpr int kQuads = DP / 4;
-                    for (int i = tid; i < walk.rows * kQuads; i += 128) {
-                        const int rr = i / kQuads, d = i % kQuads * 4, row = walk.row0 + rr;
+                    for (int i = ht; i < rows * kQuads; i += kTcHalf) {
+                        const int rr = i / kQuads, d = i % kQuads * 4, row = row0 + rr;
                         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
                         for (int k = 0; k < count; ++k) {
-                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(
-                                partial + slot_of(at_cta + k * stride) * kTcSlot<DP> + rr * DP + d));
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part_of(at_cta + k * stride) + rr * DP + d));
                             const float f = weight[rr * kGroup + k];
                             v.x = __fmaf_rn(y.x, f, v.x), v.y = __fmaf_rn(y.y, f, v.y);
                             v.z = __fmaf_rn(y.z, f, v.z), v.w = __fmaf_rn(y.w, f, v.w);
                         }
                         if (last) {
                             attn_write(a, bf16, dim, walk.x.q0 + row / group, walk.head * group + row % group, d, v,
-                                       sm.row_scale[rr], sm.row_sum[rr]);
+                                       row_scales[rr], row_sums[rr]);
                         } else {
                             __stcg(reinterpret_cast<float4 *>(to + rr * DP + d), v);
                             if (d == 0)
-                                __stcg(reinterpret_cast<float2 *>(to + kTcRows * DP + 2 * rr),
-                                       make_float2(sm.row_scale[rr], sm.row_sum[rr]));
+                                __stcg(reinterpret_cast<float2 *>(to + kTcHalf * DP + 2 * rr),
+                                       make_float2(row_scales[rr], row_sums[rr]));
                         }
                     }
                     if (last) break;
-                    counter = counters + 2 * kMostCtas + slot_of(walk.part_first_cta);
+                    counter = counters + 4 * kTcMostCtas + slot_of(walk.part_first_cta) * 2 + half;
                     at_cta = walk.part_first_cta;
                     count = groups;
                     stride = kGroup;
                 }
-                bar_softmax();  // the queries' tile and row_scale are free again
+                bar_half(half);  // the queries' tile and row_scale are free again
             }
         }
     }
@@ -652,7 +717,7 @@ out:
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tc_free(tmem, kColumns);
+    if (warp == 12) tc_free(tmem, kColumns);
 }
 
 template <int DP, bool FULL>

@@ -62,7 +62,6 @@ __device__ __forceinline__ void tc_free(uint32_t tmem, uint32_t columns) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Makes this thread's writes to shared memory visible to the tensor cores.
@@ -73,6 +72,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
 }
 
 #define QR_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define QR_T8(v, i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7])
 #define QR_I8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
 
 // 32 columns of this thread's lane (lane l of warp w: lane 32 (w % 4) + l).
@@ -83,6 +83,11 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
         : QR_R8(v, 0), QR_R8(v, 8), QR_R8(v, 16), QR_R8(v, 24)
         : "r"(addr)
         : "memory");
+}
+// Waits for this thread's loads; the registers pass through, so that nothing
+// uses them before.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : QR_T8(v, 0), QR_T8(v, 8), QR_T8(v, 16), QR_T8(v, 24)::"memory");
 }
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) {
     asm volatile(
@@ -98,6 +103,7 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&v)[16]) 
         : "memory");
 }
 #undef QR_R8
+#undef QR_T8
 #undef QR_I8
 
 // Pairs of fp32 in one instruction.
