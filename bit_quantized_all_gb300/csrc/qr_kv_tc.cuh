@@ -41,9 +41,11 @@ constexpr uint32_t kColS = 0, kColO = 256, kColumns = 512;
 
 struct TcMeta {
     float ks[8], vs[8];
+    float vlog[8], vinv[8];  // log2 and reciprocal of vs
     uint32_t valid;
-    int vexp;  // the largest scale_exp of the tile's valid groups
-    int pad[2];
+    int vexp;   // the largest scale_exp of the tile's valid groups
+    int plain;  // every group is valid and no vs is zero (or near it)
+    int pad;
 };
 
 template <int DP>
@@ -158,6 +160,11 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *fai
     if (mbar_wait(bar, parity)) return true;
     if (atomicExch(fail, 1) == 0) atomicAdd(timeouts, 1u);
     return false;
+}
+
+// ... by a whole warp, whose lanes then go on together.
+__device__ __forceinline__ bool tc_wait_warp(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {
+    return __all_sync(~0u, tc_wait(bar, parity, fail, timeouts));
 }
 
 // The 128 threads of one half's softmax.
@@ -322,15 +329,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     TcMeta &meta = sm.meta[it & 3];
                     const uint32_t valid = __ballot_sync(~0u, ct < 8 && !bad);
                     int e = ct < 8 && !bad ? scale_exp(vs_now) : kLeastExp;
+                    const uint32_t sized = __ballot_sync(~0u, e > kLeastExp && e < 120);
 #pragma unroll
                     for (int d = 1; d < 8; d <<= 1) e = max(e, __shfl_xor_sync(~0u, e, d));
                     if (ct < 8) {
                         meta.ks[ct] = ks_now;
                         meta.vs[ct] = vs_now;
+                        meta.vlog[ct] = log2_fast(vs_now);
+                        meta.vinv[ct] = 1.0f / vs_now;
                     }
                     if (ct == 0) {
                         meta.valid = valid;
                         meta.vexp = e;
+                        meta.plain = (valid & sized) == 0xffu;
                     }
                 }
                 smem_to_tensor_fence();
@@ -347,8 +358,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     } else if (warp == 12) {
-        // ---- the products, by one thread
-        if (lane == 0) {
+        // ---- the products: the warp goes together, one lane issues
+        {
+            const bool leader = elect_lane();
             constexpr uint32_t kDescS = mma_desc(kTcKeys, false), kDescO = mma_desc(DP, true);
             uint32_t it = 0, count[2] = {0, 0}, items[2] = {0, 0};
             while (walk.next(a, c, group, sm.run_steps)) {
@@ -359,23 +371,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int h = 0; h < halves; ++h) {
                         if (i > 0) {
                             // O += P V of the tile before
-                            if (h == 0 && !tc_wait(&sm.v_full[was], ((t - 1) >> 1) & 1, fail, timeouts)) goto out;
-                            if (!tc_wait(&sm.p_full[h], count[h] & 1, fail, timeouts)) goto out;
+                            if (h == 0 && !tc_wait_warp(&sm.v_full[was], ((t - 1) >> 1) & 1, fail, timeouts)) goto out;
+                            if (!tc_wait_warp(&sm.p_full[h], count[h] & 1, fail, timeouts)) goto out;
                             ++count[h];
                             tc_fence_after();
                             const uint32_t v = smem_addr(sm.v[was]);
 #pragma unroll
                             for (int n = 0; n < kTcKeys / 16; ++n)
-                                tc_mma_ts(tmem + kColO + h * 128, tmem + kColS + h * 128 + n * 8,
+                                tc_mma_ts(leader, tmem + kColO + h * 128, tmem + kColS + h * 128 + n * 8,
                                           smem_desc(v + n * 2048, 16384, 1024), kDescO, i > 1 || n > 0);
-                            if (h == halves - 1) tc_commit(&sm.v_empty[was]);
-                            if (i == tiles) tc_commit(&sm.o_full[h]);
+                            if (h == halves - 1) tc_commit(leader, &sm.v_empty[was]);
+                            if (i == tiles) tc_commit(leader, &sm.o_full[h]);
                         }
                         if (i < tiles) {
                             // S = Q K^T of this tile
-                            if (h == 0 && !tc_wait(&sm.k_full[s], (t >> 1) & 1, fail, timeouts)) goto out;
+                            if (h == 0 && !tc_wait_warp(&sm.k_full[s], (t >> 1) & 1, fail, timeouts)) goto out;
                             if (i == 0) {
-                                if (!tc_wait(&sm.q_full[h], items[h] & 1, fail, timeouts)) goto out;
+                                if (!tc_wait_warp(&sm.q_full[h], items[h] & 1, fail, timeouts)) goto out;
                                 ++items[h];
                             }
                             tc_fence_after();
@@ -383,11 +395,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                             for (int n = 0; n < DP / 16; ++n) {
                                 const uint32_t at = (n >> 2) * 16384 + (n & 3) * 32;
-                                tc_mma_ss(tmem + kColS + h * 128, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024),
+                                tc_mma_ss(leader, tmem + kColS + h * 128, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024),
                                           kDescS, n > 0);
                             }
-                            tc_commit(&sm.s_full[h]);
-                            if (h == halves - 1) tc_commit(&sm.k_empty[s]);
+                            tc_commit(leader, &sm.s_full[h]);
+                            if (h == halves - 1) tc_commit(leader, &sm.k_empty[s]);
                         }
                     }
                 }
@@ -473,7 +485,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (active) {
                     const TcMeta &meta = sm.meta[it & 3];
                     const int key0 = walk.begin + i * kTcKeys;
-                    const bool mask = meta.valid != 0xffu || key0 + kTcKeys > seen_end || key0 < seen_begin;
+                    const bool mask = !meta.plain || key0 + kTcKeys > seen_end || key0 < seen_begin;
                     float top = -INFINITY;
                     int e;
                     uint32_t v[2][32];
@@ -540,54 +552,71 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                     }
-                    const float base = m == -INFINITY ? 0.0f : -m, up = pow2i(kTcWeightExp - ve);
-                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    auto weigh = [&](const uint32_t (&sv)[32], int cc, auto masked) {
-                        constexpr bool kMasked = decltype(masked)::value;
-                        uint32_t p[16];
-#pragma unroll
-                        for (int gr = 0; gr < 2; ++gr) {
-                            const int g8 = cc * 2 + gr, key = key0 + g8 * 16;
-                            const float f = row_scale * meta.ks[g8], vs = meta.vs[g8];
-                            // (a group beyond the row's power of two is not seen by it)
-                            const float w = kMasked && scale_exp(vs) > ve + kScaleSlack ? 0.0f : vs * up;
-                            const bool ok = !kMasked || (meta.valid >> g8 & 1);
-#pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                float2 y = mul2(make_float2(__uint_as_float(sv[gr * 16 + k]), __uint_as_float(sv[gr * 16 + k + 1])),
-                                                make_float2(f, f));
-                                if (kMasked) {
-                                    if (!ok || key + k >= row_end || key + k < row_begin) y.x = -INFINITY;
-                                    if (!ok || key + k + 1 >= row_end || key + k + 1 < row_begin) y.y = -INFINITY;
-                                }
-                                y = add2(y, make_float2(base, base));
-                                y.x = exp2_fast(y.x);
-                                y.y = exp2_fast(y.y);
-                                sum[gr] = add2(sum[gr], y);
-                                y = mul2(y, make_float2(w, w));
-                                p[gr * 8 + k / 2] = pack_f16(y.x, y.y);
-                            }
-                        }
-                        // P of 32 keys takes 16 columns, all of them read before
-                        tc_st16(scol + cc * 16, p);
-                    };
+                    const float base = m == -INFINITY ? 0.0f : -m;
                     tc_ld32(scol, v[0]);
-                    if (!mask) {
+                    // Weight: 2^(s f - m) w with w the values' scale under the
+                    // row's power of two, taken in one exponent; a group's sum
+                    // is then divided by w.  Not for scores so large that the
+                    // fused product's unrounded part would matter.
+                    if (!mask && !__any_sync(~0u, !(fabsf(m) < 65536.0f))) {
+                        const float lift = base + static_cast<float>(kTcWeightExp - ve);
+                        float sums = 0.0f;
 #pragma unroll
                         for (int cc = 0; cc < 4; ++cc) {
                             tc_wait_ld(v[cc & 1]);
                             if (cc < 3) tc_ld32(scol + (cc + 1) * 32, v[(cc + 1) & 1]);
-                            weigh(v[cc & 1], cc, std::false_type());
+                            const uint32_t(&sv)[32] = v[cc & 1];
+                            uint32_t p[16];
+#pragma unroll
+                            for (int gr = 0; gr < 2; ++gr) {
+                                const float f = row_scale * meta.ks[cc * 2 + gr], add = lift + meta.vlog[cc * 2 + gr];
+                                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                                for (int k = 0; k < 16; k += 2) {
+                                    float2 y = fma2(make_float2(__uint_as_float(sv[gr * 16 + k]), __uint_as_float(sv[gr * 16 + k + 1])),
+                                                    make_float2(f, f), make_float2(add, add));
+                                    y.x = exp2_fast(y.x);
+                                    y.y = exp2_fast(y.y);
+                                    part[k >> 1 & 1] = add2(part[k >> 1 & 1], y);
+                                    p[gr * 8 + k / 2] = pack_f16(y.x, y.y);
+                                }
+                                part[0] = add2(part[0], part[1]);
+                                sums = __fmaf_rn(part[0].x + part[0].y, meta.vinv[cc * 2 + gr], sums);
+                            }
+                            // P of 32 keys takes 16 columns, all of them read before
+                            tc_st16(scol + cc * 16, p);
                         }
+                        l = __fmaf_rn(sums, pow2i(ve - kTcWeightExp), l);
                     } else {
+                        const float up = pow2i(kTcWeightExp - ve);
 #pragma unroll 1
                         for (int cc = 0; cc < 4; ++cc) {
                             tc_wait_ld(v[0]);
-                            weigh(v[0], cc, std::true_type());
+                            uint32_t p[16];
+#pragma unroll
+                            for (int gr = 0; gr < 2; ++gr) {
+                                const int g8 = cc * 2 + gr, key = key0 + g8 * 16;
+                                const float f = row_scale * meta.ks[g8], vs = meta.vs[g8];
+                                // (a group beyond the row's power of two is not seen by it)
+                                const float w = scale_exp(vs) > ve + kScaleSlack ? 0.0f : vs * up;
+                                const bool ok = meta.valid >> g8 & 1;
+#pragma unroll
+                                for (int k = 0; k < 16; k += 2) {
+                                    float y[2];
+#pragma unroll
+                                    for (int u = 0; u < 2; ++u) {
+                                        const float x = __uint_as_float(v[0][gr * 16 + k + u]) * f;
+                                        const bool sees = ok && key + k + u < row_end && key + k + u >= row_begin;
+                                        y[u] = exp2_fast(sees ? x + base : -INFINITY);
+                                        l += y[u];
+                                    }
+                                    p[gr * 8 + k / 2] = pack_f16(y[0] * w, y[1] * w);
+                                }
+                            }
+                            tc_st16(scol + cc * 16, p);
                             if (cc < 3) tc_ld32(scol + (cc + 1) * 32, v[0]);
                         }
                     }
-                    l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                     tc_wait_st();
                 }
                 tc_fence_before();
