@@ -11,7 +11,7 @@ size_t kv_attention_workspace(int, long long tokens, int q_heads, int heads, int
     // dimensions), or of 160 of up to 256
     const size_t dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
     size_t rows = size_t(2 * kMostCtas) * (dp <= 128 ? 32 : 16);
-    if (dp <= 128 && tokens * (q_heads / heads) > 16) rows = size_t(2 * 160) * 256;
+    if (dp <= 128 && tokens * (q_heads / heads) > 32) rows = size_t(2 * 160) * 256;
     return kWorkspaceCounters + rows * (dp + 2) * 4;
 }
 
@@ -25,7 +25,7 @@ cudaError_t launch_kv_attention(int dtype, const KvAttentionArgs &a, const qr_kv
     const KvView c = kv_view(cache);
     const int group = a.q_heads / c.heads;
     const long long rows = static_cast<long long>(a.max_q) * group;
-    if (c.dim <= 128 && rows > 16) return launch_kv_tc(dtype, a, c, group, s);
+    if (c.dim <= 128 && rows > 32) return launch_kv_tc(dtype, a, c, group, s);
     if (c.dim <= 64)
         return rows <= 8    ? run_split<64, 1>(dtype, a, c, group, s)
                : rows <= 16 ? run_split<64, 2>(dtype, a, c, group, s)

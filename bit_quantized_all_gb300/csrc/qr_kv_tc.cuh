@@ -131,26 +131,10 @@ struct TcWalk {
     __device__ __forceinline__ int tiles() const { return end > begin ? (end - begin + kTcKeys - 1) / kTcKeys : 0; }
 };
 
-// Eight of a row's values from dimension d on, and with d = 0 its lse.
-__device__ __forceinline__ void attn_write8(const KvAttentionArgs &a, bool bf16, int dim, long long token, int head, int d,
-                                            const float *v, float top, float sum) {
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (d < dim) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (bf16) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i] * inv, v[2 * i + 1] * inv);
-                w[i] = *reinterpret_cast<const uint32_t *>(&b);
-            } else {
-                w[i] = pack_f16(v[2 * i] * inv, v[2 * i + 1] * inv);
-            }
-        }
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + token * a.out_token + head * a.out_head + d) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    if (a.lse && d == 0)
-        a.lse[token * a.q_heads + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+__device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
+    if (!bf16) return pack_f16(lo, hi);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
 }
 
 // Waits for a phase; after a wait that ran out every wait of the CTA fails.
@@ -423,53 +407,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 it += tiles;
                 continue;
             }
-            // the queries: each row scaled by a power of two to a largest
-            // magnitude in [2^12, 2^13), as in qr_kv_split.cuh; kBatch loads of
-            // a thread at a time
+            // this thread's query: scaled by a power of two to a largest
+            // magnitude in [2^12, 2^13), as in qr_kv_split.cuh
+            const int row = row0 + ht, token = row / group, head = walk.head * group + (row - token * group);
+            float row_scale = 0.0f;
             if (tiles > 0) {
-                constexpr int kRowLanes = DP / 4, kBatch = 16, kRowsStep = 32 / kRowLanes;
-                const int d = 4 * (lane % kRowLanes);
-#pragma unroll 1
-                for (int i0 = 0; i0 < 32; i0 += kBatch * kRowsStep) {
-                    uint2 raw2[kBatch];
+                constexpr int kPieces = DP / 8;
+                uint4 piece[kPieces];
+                const uint16_t *const src = static_cast<const uint16_t *>(a.q) + (walk.x.q0 + token) * a.q_token + head * a.q_head;
 #pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
-                        const int rr = hw * 32 + i0 + u * kRowsStep + lane / kRowLanes, row = row0 + rr;
-                        raw2[u] = make_uint2(0, 0);
-                        if (rr < rows && d < dim) {
-                            const int token = row / group;
-                            raw2[u] = *reinterpret_cast<const uint2 *>(
-                                static_cast<const uint16_t *>(a.q) + (walk.x.q0 + token) * a.q_token +
-                                (static_cast<long long>(walk.head) * group + (row - token * group)) * a.q_head + d);
-                        }
-                    }
+                for (int i = 0; i < kPieces; ++i) {
+                    piece[i] = make_uint4(0, 0, 0, 0);
+                    if (ht < rows && (FULL || i * 8 < dim)) piece[i] = reinterpret_cast<const uint4 *>(src)[i];
+                }
+                float amax = 0.0f;
 #pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
-                        const int rr = hw * 32 + i0 + u * kRowsStep + lane / kRowLanes;
-                        const float f[4] = {widen1(bf16, raw2[u].x & 0xffff), widen1(bf16, raw2[u].x >> 16),
-                                            widen1(bf16, raw2[u].y & 0xffff), widen1(bf16, raw2[u].y >> 16)};
-                        float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+                for (int i = 0; i < kPieces; ++i) {
+                    float f[8];
+                    if (bf16) widen8<1>(piece[i], f); else widen8<0>(piece[i], f);
 #pragma unroll
-                        for (int o = kRowLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-                        int e = 0;
-                        if (amax > 0.0f && amax < INFINITY) {
-                            frexpf(amax, &e);
-                            e -= 13;
-                        }
-                        const float down1 = pow2i(-(e / 2)) * (a.scale < 0.0f ? -1.0f : 1.0f), down2 = pow2i(-(e - e / 2));
-                        if (lane % kRowLanes == 0) row_scales[rr] = ldexpf(fabsf(a.scale) * 1.4426950408889634f, e);
-                        *reinterpret_cast<uint2 *>(sm.q[half] + (d >> 6) * 16384 + swizzled(rr, (d & 63) >> 3) + (d & 4) * 2) =
-                            make_uint2(pack_f16(f[0] * down1 * down2, f[1] * down1 * down2),
-                                       pack_f16(f[2] * down1 * down2, f[3] * down1 * down2));
-                    }
+                    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+                }
+                int e = 0;
+                if (amax > 0.0f && amax < INFINITY) {
+                    frexpf(amax, &e);
+                    e -= 13;
+                }
+                const float down1 = pow2i(-(e / 2)) * (a.scale < 0.0f ? -1.0f : 1.0f), down2 = pow2i(-(e - e / 2));
+                row_scale = ldexpf(fabsf(a.scale) * 1.4426950408889634f, e);
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    float f[8];
+                    if (bf16) widen8<1>(piece[i], f); else widen8<0>(piece[i], f);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[k] = f[k] * down1 * down2;
+                    *reinterpret_cast<uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(ht, i & 7)) =
+                        make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
                 }
                 smem_to_tensor_fence();
                 mbar_arrive(&sm.q_full[half]);
                 __syncwarp();
             }
-            const float row_scale = tiles > 0 ? row_scales[ht] : 0.0f;
             const bool active = hw * 32 < rows;  // else no row of the warp is the item's
-            const int pos = walk.p0 + (row0 + ht) / group;
+            const int pos = walk.p0 + token;
             const int row_end = a.causal ? min(walk.x.kv, pos + 1) : walk.x.kv;
             const int row_begin = a.window > 0 ? pos - a.window + 1 : 0;
             // keys that every row of the warp sees
@@ -634,11 +614,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_after();
             }
             if (active) {
-                const float back = pow2i(ve - kTcWeightExp);
-                const int row = row0 + ht, token = row / group;
+                const float back = pow2i(ve - kTcWeightExp), inv = walk.parts > 1 || l == 0.0f ? 1.0f : 1.0f / l;
                 const bool in_item = ht < rows;
-                const long long out_token = walk.x.q0 + token;
-                const int out_head = walk.head * group + (row - token * group);
+                // whole rows go out through the queries' tile, which the
+                // products have left: 16-byte pieces, swizzled, then each row by
+                // neighbouring lanes
+                uint8_t *const stage = sm.q[half];
 #pragma unroll 1
                 for (int cc = 0; cc < DP / 32; ++cc) {
                     uint32_t v[32];
@@ -649,24 +630,45 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] = 0;
                     }
-                    if (in_item) {
-                        float y[32];
+                    float y[32];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(v[k]) * back;
-                        if (walk.parts == 1) {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 8)
-                                attn_write8(a, bf16, dim, out_token, out_head, cc * 32 + k, y + k, m, l);
-                        } else {
+                    for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(v[k]) * back * inv;
+                    if (walk.parts > 1) {
+                        if (in_item)
 #pragma unroll
                             for (int k = 0; k < 32; k += 4)
                                 __stcg(reinterpret_cast<float4 *>(my_part + ht * DP + cc * 32 + k),
                                        make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            const int i = cc * 4 + k / 8;
+                            *reinterpret_cast<uint4 *>(stage + (i >> 3) * 16384 + swizzled(ht, i & 7)) =
+                                make_uint4(pack_out(bf16, y[k], y[k + 1]), pack_out(bf16, y[k + 2], y[k + 3]),
+                                           pack_out(bf16, y[k + 4], y[k + 5]), pack_out(bf16, y[k + 6], y[k + 7]));
                         }
                     }
                 }
-                if (in_item && walk.parts > 1)
-                    __stcg(reinterpret_cast<float2 *>(my_part + kTcHalf * DP + 2 * ht), make_float2(m, l));
+                if (walk.parts > 1) {
+                    if (in_item) __stcg(reinterpret_cast<float2 *>(my_part + kTcHalf * DP + 2 * ht), make_float2(m, l));
+                } else {
+                    if (in_item && a.lse)
+                        a.lse[(walk.x.q0 + token) * static_cast<long long>(a.q_heads) + head] =
+                            l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                    __syncwarp();
+                    constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces;  // pieces of a row, rows per instruction
+                    const int i = lane % kPieces;
+#pragma unroll 4
+                    for (int u = 0; u < 32; u += kAtOnce) {
+                        const int in_warp = u + lane / kPieces, rr = hw * 32 + in_warp;
+                        const long long tok = walk.x.q0 + __shfl_sync(~0u, token, in_warp);
+                        const long long hd = __shfl_sync(~0u, head, in_warp);
+                        if (rr < rows && (FULL || i * 8 < dim))
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + tok * a.out_token + hd * a.out_head + i * 8) =
+                                *reinterpret_cast<const uint4 *>(stage + (i >> 3) * 16384 + swizzled(rr, i & 7));
+                    }
+                    __syncwarp();
+                }
             }
             tc_fence_before();
             if (walk.parts > 1) {
@@ -713,7 +715,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     float *const to = part_of(at_cta);
                     constexpr int kQuads = DP / 4;
                     for (int i = ht; i < rows * kQuads; i += kTcHalf) {
-                        const int rr = i / kQuads, d = i % kQuads * 4, row = row0 + rr;
+                        const int rr = i / kQuads, d = i % kQuads * 4, out_row = row0 + rr;
                         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
                         for (int k = 0; k < count; ++k) {
@@ -723,7 +725,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             v.z = __fmaf_rn(y.z, f, v.z), v.w = __fmaf_rn(y.w, f, v.w);
                         }
                         if (last) {
-                            attn_write(a, bf16, dim, walk.x.q0 + row / group, walk.head * group + row % group, d, v,
+                            attn_write(a, bf16, dim, walk.x.q0 + out_row / group, walk.head * group + out_row % group, d, v,
                                        row_scales[rr], row_sums[rr]);
                         } else {
                             __stcg(reinterpret_cast<float4 *>(to + rr * DP + d), v);
