@@ -7,7 +7,7 @@
 // equal shares, one per CTA (here counting only tiles that some row sees), and
 // the parts of a divided item are joined by whichever CTA brings the last one.
 //
-// A CTA is thirteen warps.  Four convert: each tile's codes come through
+// Thirteen warps of a CTA work.  Four convert: each tile's codes come through
 // registers and go to shared memory as fp16 (exact), double buffered; both
 // halves use them.  One thread issues the products, S = Q K^T and O += P V,
 // with S, P and O in tensor memory.  Four warps per half, a thread per row, do
@@ -31,6 +31,9 @@ namespace qrk {
 
 constexpr int kTcRows = 256, kTcHalf = 128, kTcKeys = 128;
 constexpr int kTcThreads = 416;  // warps 0-7 softmax, 8-11 conversion, 12 products
+// An item's queries, output and empty pipeline take about as long as this many
+// tiles; the shares count them, as tiles before the first one.
+constexpr int kItemSteps = 3;
 constexpr int kTcMostCtas = 160;
 constexpr float kSlack = 6.0f;
 constexpr int kScaleSlack = 2;
@@ -39,7 +42,7 @@ constexpr int kTcWeightExp = 7;  // weight 1 of the largest scale is 2^7
 // Tensor memory columns: S of both halves (P in its place), O of both halves.
 constexpr uint32_t kColS = 0, kColO = 256, kColumns = 512;
 
-struct TcMeta {
+struct alignas(16) TcMeta {
     float ks[8], vs[8];
     float vlog[8], vinv[8];  // log2 and reciprocal of vs
     uint32_t valid;
@@ -48,27 +51,12 @@ struct TcMeta {
     int pad;
 };
 
-template <int DP>
-struct TcSmem {
-    static constexpr int kSlabs = DP / 64, kTile = kSlabs * 16384;  // 128 rows of fp16
-    uint8_t q[2][kTile];
-    uint8_t k[2][kTile];
-    uint8_t v[2][kTile];
-    TcMeta meta[4];
-    float row_scale[kTcRows], row_sum[kTcRows];
-    long long run_steps[128], warp_sums[4];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // by buffer
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];    // by half
-    uint32_t tmem;
-    unsigned ticket[2];
-    int fail;
-};
-
 // Floats of one half's part: accumulators, then (max, sum) pairs.
 template <int DP>
 constexpr int kTcSlot = kTcHalf * (DP + 2);
 
-// The items of a CTA's share, in order; every thread keeps its own copy.
+// The items of a CTA's share, in order; every warp keeps its own copy, in
+// shared memory, which its first lane moves on.
 struct TcWalk {
     long long step, last, share, at;
     int r, j, tiles_of_r;
@@ -77,6 +65,7 @@ struct TcWalk {
     long long item_first;
     int head, row0, rows, begin, end, steps, p0;
     int part_first_cta, parts;
+    bool more;
 
     // The keys that some row of row tile `jj` sees, [b, e).
     __device__ __forceinline__ static int range(const KvAttentionArgs &a, const AttnRequest &x, int group, int jj, int *b,
@@ -85,7 +74,7 @@ struct TcWalk {
         const int pos_first = p0 + jj * kTcRows / group, pos_last = p0 + (jj * kTcRows + rows - 1) / group;
         *e = a.causal ? max(0, min(x.kv, pos_last + 1)) : x.kv;
         *b = a.window > 0 ? max(0, pos_first - a.window + 1) / 16 * 16 : 0;
-        return *e > *b ? (*e - *b + kTcKeys - 1) / kTcKeys : 1;
+        return kItemSteps + (*e > *b ? (*e - *b + kTcKeys - 1) / kTcKeys : 0);
     }
     __device__ __forceinline__ void enter(const KvAttentionArgs &a, const KvView &c, int group, int request) {
         r = request;
@@ -94,6 +83,12 @@ struct TcWalk {
         tiles_of_r = x.items / c.heads;
     }
     __device__ __forceinline__ bool next(const KvAttentionArgs &a, const KvView &c, int group, const long long *run_steps) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) more = advance(a, c, group, run_steps);
+        __syncwarp();
+        return more;
+    }
+    __device__ __forceinline__ bool advance(const KvAttentionArgs &a, const KvView &c, int group, const long long *run_steps) {
         if (step >= last) return false;
         if (r < 0) {
             int lo = 0, hi = 127;
@@ -118,8 +113,8 @@ struct TcWalk {
         head = static_cast<int>((step - at) / steps);
         item_first = at + static_cast<long long>(head) * steps;
         const int s0 = static_cast<int>(step - item_first), s1 = static_cast<int>(min(item_first + steps, last) - item_first);
-        begin = b + s0 * kTcKeys;
-        end = min(b + s1 * kTcKeys, e);
+        begin = b + max(0, s0 - kItemSteps) * kTcKeys;
+        end = min(b + max(0, s1 - kItemSteps) * kTcKeys, e);
         row0 = j * kTcRows;
         rows = min(kTcRows, x.nq * group - row0);
         p0 = x.kv - x.nq;
@@ -131,6 +126,23 @@ struct TcWalk {
     __device__ __forceinline__ int tiles() const { return end > begin ? (end - begin + kTcKeys - 1) / kTcKeys : 0; }
 };
 
+template <int DP>
+struct TcSmem {
+    static constexpr int kSlabs = DP / 64, kTile = kSlabs * 16384;  // 128 rows of fp16
+    uint8_t q[2][kTile];
+    uint8_t k[2][kTile];
+    uint8_t v[2][kTile];
+    TcMeta meta[4];
+    float row_scale[kTcRows], row_sum[kTcRows];
+    long long run_steps[128], warp_sums[4];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // by buffer
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];    // by half
+    TcWalk walk[13];
+    uint32_t tmem;
+    unsigned ticket[2];
+    int fail;
+};
+
 __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
     if (!bf16) return pack_f16(lo, hi);
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -139,9 +151,8 @@ __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
 
 // Waits for a phase; after a wait that ran out every wait of the CTA fails.
 __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*static_cast<volatile int *>(fail)) return false;
-    if (mbar_wait(bar, parity)) return true;
+    if (*static_cast<volatile int *>(fail)) return mbar_try_wait(bar, parity);
+    if (mbar_wait_suspended(bar, parity)) return true;
     if (atomicExch(fail, 1) == 0) atomicAdd(timeouts, 1u);
     return false;
 }
@@ -212,8 +223,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
     }
     const uint32_t tmem = sm.tmem;
-    TcWalk walk;
-    {
+    TcWalk &walk = sm.walk[warp];
+    if (lane == 0) {
         const long long all = sm.warp_sums[0] + sm.warp_sums[1] + sm.warp_sums[2] + sm.warp_sums[3];
         walk.share = (all + gridDim.x - 1) / gridDim.x;
         walk.step = walk.share * blockIdx.x;
@@ -305,7 +316,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool bad = mid < 0;
                 const float ks_now = mks, vs_now = mvs;
                 if (i + 1 < tiles) ids(i + 1);
-                if (it >= 2 && !tc_wait(&sm.k_empty[s], parity, fail, timeouts)) goto out;
+                if (it >= 2 && !tc_wait_warp(&sm.k_empty[s], parity, fail, timeouts)) goto out;
                 store(kr, sm.k[s]);
                 if (warp == 8) {
                     // (entry it % 4: tile it - 3's softmax is done before K of
@@ -334,7 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     load(i + 1, kr, c.k, c.k_block, khead);
                     scales();
                 }
-                if (it >= 2 && !tc_wait(&sm.v_empty[s], parity, fail, timeouts)) goto out;
+                if (it >= 2 && !tc_wait_warp(&sm.v_empty[s], parity, fail, timeouts)) goto out;
                 store(vr, sm.v[s]);
                 smem_to_tensor_fence();
                 mbar_arrive(&sm.v_full[s]);
@@ -390,7 +401,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 it += tiles;
             }
         }
-    } else {
+    } else if (warp < 8) {
         // ---- the softmax, a thread per row.  After a wait that ran out these
         // warps go on (every later wait fails at once), so that none of them is
         // missing at the barriers they share; the results are then void.
@@ -454,6 +465,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int row_begin = a.window > 0 ? pos - a.window + 1 : 0;
             // keys that every row of the warp sees
             const int seen_end = __reduce_min_sync(~0u, row_end), seen_begin = __reduce_max_sync(~0u, row_begin);
+            const int begin = walk.begin;
             float m = -INFINITY, l = 0.0f;
             int ve = kLeastExp;
             for (int i = 0; i < tiles; ++i, ++it, ++mine) {
@@ -464,12 +476,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // rescaled, P written
                 if (active) {
                     const TcMeta &meta = sm.meta[it & 3];
-                    const int key0 = walk.begin + i * kTcKeys;
+                    const int key0 = begin + i * kTcKeys;
                     const bool mask = !meta.plain || key0 + kTcKeys > seen_end || key0 < seen_begin;
                     float top = -INFINITY;
                     int e;
                     uint32_t v[2][32];
                     tc_ld32(scol, v[0]);
+                    float f8[8];  // the groups' score factors
+#pragma unroll
+                    for (int k = 0; k < 8; k += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(meta.ks + k);
+                        f8[k] = row_scale * x.x, f8[k + 1] = row_scale * x.y;
+                        f8[k + 2] = row_scale * x.z, f8[k + 3] = row_scale * x.w;
+                    }
                     if (!mask) {
                         // scales are not negative: a group's largest score is
                         // its largest product, scaled
@@ -487,7 +506,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     x[k] = max3_nan(max_nan(__uint_as_float(w[4 * k]), __uint_as_float(w[4 * k + 1])),
                                                     __uint_as_float(w[4 * k + 2]), __uint_as_float(w[4 * k + 3]));
                                 const float y = max3_nan(max_nan(x[0], x[1]), x[2], x[3]);
-                                top = max_nan(top, y * (row_scale * meta.ks[cc * 2 + gr]));
+                                top = max_nan(top, y * f8[cc * 2 + gr]);
                             }
                         }
                     } else {
@@ -533,7 +552,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                     const float base = m == -INFINITY ? 0.0f : -m;
-                    tc_ld32(scol, v[0]);
+                    uint32_t x[2][16];
+                    tc_ld16(scol, x[0]);
                     // Weight: 2^(s f - m) w with w the values' scale under the
                     // row's power of two, taken in one exponent; a group's sum
                     // is then divided by w.  Not for scores so large that the
@@ -541,60 +561,73 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!mask && !__any_sync(~0u, !(fabsf(m) < 65536.0f))) {
                         const float lift = base + static_cast<float>(kTcWeightExp - ve);
                         float sums = 0.0f;
+                        auto exponents = [&](uint32_t (&y)[16], int g8) {
+                            const float f = f8[g8], add = lift + meta.vlog[g8];
 #pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) {
-                            tc_wait_ld(v[cc & 1]);
-                            if (cc < 3) tc_ld32(scol + (cc + 1) * 32, v[(cc + 1) & 1]);
-                            const uint32_t(&sv)[32] = v[cc & 1];
-                            uint32_t p[16];
-#pragma unroll
-                            for (int gr = 0; gr < 2; ++gr) {
-                                const float f = row_scale * meta.ks[cc * 2 + gr], add = lift + meta.vlog[cc * 2 + gr];
-                                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                                for (int k = 0; k < 16; k += 2) {
-                                    float2 y = fma2(make_float2(__uint_as_float(sv[gr * 16 + k]), __uint_as_float(sv[gr * 16 + k + 1])),
-                                                    make_float2(f, f), make_float2(add, add));
-                                    y.x = exp2_fast(y.x);
-                                    y.y = exp2_fast(y.y);
-                                    part[k >> 1 & 1] = add2(part[k >> 1 & 1], y);
-                                    p[gr * 8 + k / 2] = pack_f16(y.x, y.y);
-                                }
-                                part[0] = add2(part[0], part[1]);
-                                sums = __fmaf_rn(part[0].x + part[0].y, meta.vinv[cc * 2 + gr], sums);
+                            for (int k = 0; k < 16; k += 2) {
+                                const float2 z = fma2(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])),
+                                                      make_float2(f, f), make_float2(add, add));
+                                y[k] = __float_as_uint(z.x);
+                                y[k + 1] = __float_as_uint(z.y);
                             }
-                            // P of 32 keys takes 16 columns, all of them read before
-                            tc_st16(scol + cc * 16, p);
+                        };
+                        // a group at a time, the exponentials of the next one
+                        // between the conversions and sums of this: one after
+                        // the other they would each wait for their own latency
+                        tc_wait_ld(x[0]);
+                        tc_ld16(scol + 16, x[1]);
+                        exponents(x[0], 0);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) x[0][k] = __float_as_uint(exp2_fast(__uint_as_float(x[0][k])));
+#pragma unroll
+                        for (int g8 = 0; g8 < 8; ++g8) {
+                            uint32_t(&now)[16] = x[g8 & 1], (&next)[16] = x[(g8 + 1) & 1];
+                            if (g8 < 7) {
+                                tc_wait_ld(next);
+                                exponents(next, g8 + 1);
+                            }
+                            uint32_t p[8];
+                            float2 part[2];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float2 y = make_float2(__uint_as_float(now[2 * k]), __uint_as_float(now[2 * k + 1]));
+                                if (g8 < 7) next[2 * k] = __float_as_uint(exp2_fast(__uint_as_float(next[2 * k])));
+                                p[k] = pack_f16(y.x, y.y);
+                                if (g8 < 7) next[2 * k + 1] = __float_as_uint(exp2_fast(__uint_as_float(next[2 * k + 1])));
+                                part[k & 1] = k < 2 ? y : add2(part[k & 1], y);
+                            }
+                            part[0] = add2(part[0], part[1]);
+                            sums = __fmaf_rn(part[0].x + part[0].y, meta.vinv[g8], sums);
+                            if (g8 < 6) tc_ld16(scol + (g8 + 2) * 16, now);
+                            // P of 16 keys takes 8 columns, all of them read before
+                            tc_st8(scol + g8 * 8, p);
                         }
                         l = __fmaf_rn(sums, pow2i(ve - kTcWeightExp), l);
                     } else {
                         const float up = pow2i(kTcWeightExp - ve);
 #pragma unroll 1
-                        for (int cc = 0; cc < 4; ++cc) {
-                            tc_wait_ld(v[0]);
-                            uint32_t p[16];
+                        for (int g8 = 0; g8 < 8; ++g8) {
+                            const int key = key0 + g8 * 16;
+                            const float f = row_scale * meta.ks[g8], vs = meta.vs[g8];
+                            // (a group beyond the row's power of two is not seen by it)
+                            const float w = scale_exp(vs) > ve + kScaleSlack ? 0.0f : vs * up;
+                            const bool ok = meta.valid >> g8 & 1;
+                            uint32_t p[8];
+                            tc_wait_ld(x[0]);
 #pragma unroll
-                            for (int gr = 0; gr < 2; ++gr) {
-                                const int g8 = cc * 2 + gr, key = key0 + g8 * 16;
-                                const float f = row_scale * meta.ks[g8], vs = meta.vs[g8];
-                                // (a group beyond the row's power of two is not seen by it)
-                                const float w = scale_exp(vs) > ve + kScaleSlack ? 0.0f : vs * up;
-                                const bool ok = meta.valid >> g8 & 1;
+                            for (int k = 0; k < 16; k += 2) {
+                                float y[2];
 #pragma unroll
-                                for (int k = 0; k < 16; k += 2) {
-                                    float y[2];
-#pragma unroll
-                                    for (int u = 0; u < 2; ++u) {
-                                        const float x = __uint_as_float(v[0][gr * 16 + k + u]) * f;
-                                        const bool sees = ok && key + k + u < row_end && key + k + u >= row_begin;
-                                        y[u] = exp2_fast(sees ? x + base : -INFINITY);
-                                        l += y[u];
-                                    }
-                                    p[gr * 8 + k / 2] = pack_f16(y[0] * w, y[1] * w);
+                                for (int u = 0; u < 2; ++u) {
+                                    const float score = __uint_as_float(x[0][k + u]) * f;
+                                    const bool sees = ok && key + k + u < row_end && key + k + u >= row_begin;
+                                    y[u] = exp2_fast(sees ? score + base : -INFINITY);
+                                    l += y[u];
                                 }
+                                p[k / 2] = pack_f16(y[0] * w, y[1] * w);
                             }
-                            tc_st16(scol + cc * 16, p);
-                            if (cc < 3) tc_ld32(scol + (cc + 1) * 32, v[0]);
+                            tc_st8(scol + g8 * 8, p);
+                            if (g8 < 7) tc_ld16(scol + (g8 + 1) * 16, x[0]);
                         }
                     }
                     tc_wait_st();

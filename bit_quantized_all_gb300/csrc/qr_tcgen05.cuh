@@ -74,10 +74,32 @@ __device__ __forceinline__ void tc_free(uint32_t tmem, uint32_t columns) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;"); }
 
 // Makes this thread's writes to shared memory visible to the tensor cores.
 __device__ __forceinline__ void smem_to_tensor_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// As mbar_wait, but the thread is suspended for up to kSuspendNs at a time
+// instead of asking again and again: warps that wait beside others that
+// compute leave them the issue slots.
+constexpr uint32_t kSuspendNs = 1000000;
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t parity) {
+    unsigned long long t0 = 0;
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+        if (done) return true;
+        const unsigned long long now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) return false;
+    }
+}
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -88,31 +110,37 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
 #define QR_I8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
 
 // 32 columns of this thread's lane (lane l of warp w: lane 32 (w % 4) + l).
+// (These keep their order among themselves and the fences and barriers, and
+// touch no addressable memory: loads may be moved across them.)
 __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : QR_R8(v, 0), QR_R8(v, 8), QR_R8(v, 16), QR_R8(v, 24)
-        : "r"(addr)
-        : "memory");
+        : "r"(addr));
+}
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : QR_R8(v, 0), QR_R8(v, 8)
+        : "r"(addr));
+}
+__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), QR_I8(v, 0));
+}
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : QR_T8(v, 0), QR_T8(v, 8));
 }
 // Waits for this thread's loads; the registers pass through, so that nothing
 // uses them before.
 __device__ __forceinline__ void tc_wait_ld(uint32_t (&v)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : QR_T8(v, 0), QR_T8(v, 8), QR_T8(v, 16), QR_T8(v, 24)::"memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : QR_T8(v, 0), QR_T8(v, 8), QR_T8(v, 16), QR_T8(v, 24));
 }
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
         "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        QR_I8(v, 0), QR_I8(v, 8), QR_I8(v, 16), QR_I8(v, 24)
-        : "memory");
-}
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-        QR_I8(v, 0), QR_I8(v, 8)
-        : "memory");
+        QR_I8(v, 0), QR_I8(v, 8), QR_I8(v, 16), QR_I8(v, 24));
 }
 #undef QR_R8
 #undef QR_T8
