@@ -133,7 +133,6 @@ struct TcSmem {
     uint8_t k[2][kTile];
     uint8_t v[2][kTile];
     TcMeta meta[4];
-    float row_scale[kTcRows], row_sum[kTcRows];
     long long run_steps[128], warp_sums[4];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // by buffer
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];    // by half
@@ -410,7 +409,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int half = warp >> 2, hw = warp & 3, ht = tid & 127;  // half, warp and thread within it
         const uint32_t lanes = tmem + (static_cast<uint32_t>(hw * 32) << 16);
         const uint32_t scol = lanes + kColS + half * 128, ocol = lanes + kColO + half * 128;
-        float *const row_scales = sm.row_scale + half * kTcHalf;
         uint32_t it = 0, mine = 0, items = 0;  // tiles of all halves, of this one; its items
         while (walk.next(a, c, group, sm.run_steps)) {
             const int tiles = walk.tiles(), rows = min(kTcHalf, walk.rows - half * kTcHalf), row0 = walk.row0 + half * kTcHalf;
@@ -420,17 +418,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             // this thread's query: scaled by a power of two to a largest
             // magnitude in [2^12, 2^13), as in qr_kv_split.cuh
-            const int row = row0 + ht, token = row / group, head = walk.head * group + (row - token * group);
+            const int row = row0 + ht, token = row / group, head = walk.head * group + (row - token * group), walk_q0 = walk.x.q0;
+            // The warp's rows between global memory and the queries' tile, each
+            // row by neighbouring lanes in 16-byte pieces: a thread reading its
+            // own row would touch 32 lines with every instruction.
+            auto rows_move = [&](bool in) {
+                constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces;  // pieces of a row, rows per instruction
+                const int i = lane % kPieces;
+                const bool on = FULL || i * 8 < dim;
+#pragma unroll 8
+                for (int u = 0; u < 32; u += kAtOnce) {
+                    const int in_warp = u + lane / kPieces, rr = hw * 32 + in_warp;
+                    const long long tok = walk_q0 + __shfl_sync(~0u, token, in_warp), hd = __shfl_sync(~0u, head, in_warp);
+                    uint4 *const tile = reinterpret_cast<uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(rr, i & 7));
+                    if (in) {
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        if (rr < rows && on)
+                            w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + tok * a.q_token + hd * a.q_head + i * 8);
+                        *tile = w;
+                    } else if (rr < rows && on) {
+                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + tok * a.out_token + hd * a.out_head + i * 8) = *tile;
+                    }
+                }
+                __syncwarp();
+            };
             float row_scale = 0.0f;
             if (tiles > 0) {
                 constexpr int kPieces = DP / 8;
                 uint4 piece[kPieces];
-                const uint16_t *const src = static_cast<const uint16_t *>(a.q) + (walk.x.q0 + token) * a.q_token + head * a.q_head;
+                rows_move(true);
+                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    piece[i] = make_uint4(0, 0, 0, 0);
-                    if (ht < rows && (FULL || i * 8 < dim)) piece[i] = reinterpret_cast<const uint4 *>(src)[i];
-                }
+                for (int i = 0; i < kPieces; ++i)
+                    piece[i] = *reinterpret_cast<const uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(ht, i & 7));
                 float amax = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
@@ -646,13 +666,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 tc_fence_after();
             }
+            // 32 of a row's values, 32 cc and on: to the tile for the output, or
+            // to a part.  A part is [piece of four][row], so that a warp's rows
+            // are neighbours in memory.
+            const bool in_item = ht < rows;
+            auto put = [&](float *part, int cc, const float (&y)[32], float inv) {
+                if (part) {
+                    if (in_item)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            __stcg(reinterpret_cast<float4 *>(part + ((cc * 8 + k / 4) * kTcHalf + ht) * 4),
+                                   make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        const int i = cc * 4 + k / 8;
+                        *reinterpret_cast<uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(ht, i & 7)) =
+                            make_uint4(pack_out(bf16, y[k] * inv, y[k + 1] * inv), pack_out(bf16, y[k + 2] * inv, y[k + 3] * inv),
+                                       pack_out(bf16, y[k + 4] * inv, y[k + 5] * inv),
+                                       pack_out(bf16, y[k + 6] * inv, y[k + 7] * inv));
+                    }
+                }
+            };
+            // the row's maximum and sum, and the warp's rows out of the tile
+            auto finish = [&](float *part, float top, float sum) {
+                if (part) {
+                    if (in_item) __stcg(reinterpret_cast<float2 *>(part + kTcHalf * DP + 2 * ht), make_float2(top, sum));
+                    return;
+                }
+                if (in_item && a.lse)
+                    a.lse[(walk_q0 + token) * static_cast<long long>(a.q_heads) + head] =
+                        sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+                __syncwarp();
+                rows_move(false);
+            };
             if (active) {
-                const float back = pow2i(ve - kTcWeightExp), inv = walk.parts > 1 || l == 0.0f ? 1.0f : 1.0f / l;
-                const bool in_item = ht < rows;
-                // whole rows go out through the queries' tile, which the
-                // products have left: 16-byte pieces, swizzled, then each row by
-                // neighbouring lanes
-                uint8_t *const stage = sm.q[half];
+                const float back = pow2i(ve - kTcWeightExp), inv = l == 0.0f ? 1.0f : 1.0f / l;
+                float *const to = walk.parts > 1 ? my_part : nullptr;
 #pragma unroll 1
                 for (int cc = 0; cc < DP / 32; ++cc) {
                     uint32_t v[32];
@@ -665,52 +715,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     float y[32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(v[k]) * back * inv;
-                    if (walk.parts > 1) {
-                        if (in_item)
-#pragma unroll
-                            for (int k = 0; k < 32; k += 4)
-                                __stcg(reinterpret_cast<float4 *>(my_part + ht * DP + cc * 32 + k),
-                                       make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
-                            const int i = cc * 4 + k / 8;
-                            *reinterpret_cast<uint4 *>(stage + (i >> 3) * 16384 + swizzled(ht, i & 7)) =
-                                make_uint4(pack_out(bf16, y[k], y[k + 1]), pack_out(bf16, y[k + 2], y[k + 3]),
-                                           pack_out(bf16, y[k + 4], y[k + 5]), pack_out(bf16, y[k + 6], y[k + 7]));
-                        }
-                    }
+                    for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(v[k]) * back;
+                    put(to, cc, y, inv);
                 }
-                if (walk.parts > 1) {
-                    if (in_item) __stcg(reinterpret_cast<float2 *>(my_part + kTcHalf * DP + 2 * ht), make_float2(m, l));
-                } else {
-                    if (in_item && a.lse)
-                        a.lse[(walk.x.q0 + token) * static_cast<long long>(a.q_heads) + head] =
-                            l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-                    __syncwarp();
-                    constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces;  // pieces of a row, rows per instruction
-                    const int i = lane % kPieces;
-#pragma unroll 4
-                    for (int u = 0; u < 32; u += kAtOnce) {
-                        const int in_warp = u + lane / kPieces, rr = hw * 32 + in_warp;
-                        const long long tok = walk.x.q0 + __shfl_sync(~0u, token, in_warp);
-                        const long long hd = __shfl_sync(~0u, head, in_warp);
-                        if (rr < rows && (FULL || i * 8 < dim))
-                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + tok * a.out_token + hd * a.out_head + i * 8) =
-                                *reinterpret_cast<const uint4 *>(stage + (i >> 3) * 16384 + swizzled(rr, i & 7));
-                    }
-                    __syncwarp();
-                }
+                finish(to, m, l);
             }
             tc_fence_before();
             if (walk.parts > 1) {
                 // as in qr_kv_split.cuh: groups of kGroup parts, then the groups,
-                // each half for itself
-                float *const weight = reinterpret_cast<float *>(sm.q[half]), *const sums = weight + kTcHalf * kGroup;
-                static_assert(kTcMostCtas <= kGroup * kGroup && 2 * kTcHalf * kGroup * 4 <= S::kTile, "two levels");
+                // each half for itself, a thread per row
+                static_assert(kTcMostCtas <= kGroup * kGroup, "two levels");
                 static_assert(2 * 4 * kTcMostCtas * 4 <= kWorkspaceCounters, "two counters per slot and half");
-                float *const row_sums = sm.row_sum + half * kTcHalf;
                 const int groups = (walk.parts + kGroup - 1) / kGroup;
                 const int my_group = (static_cast<int>(blockIdx.x) - walk.part_first_cta) / kGroup;
                 int at_cta = walk.part_first_cta + my_group * kGroup;
@@ -725,47 +740,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     bar_half(half);
                     if (sm.ticket[half] != static_cast<unsigned>(count - 1)) break;
                     __threadfence();
-                    for (int i = ht; i < rows * count; i += kTcHalf) {
-                        const int rr = i / count, k = i % count;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_of(at_cta + k * stride) + kTcHalf * DP + 2 * rr));
-                        weight[rr * kGroup + k] = ml.x;
-                        sums[rr * kGroup + k] = ml.y;
-                    }
-                    bar_half(half);
-                    if (ht < rows) {
-                        float top = -INFINITY, sum = 0.0f;
-                        for (int k = 0; k < count; ++k) top = max_nan(top, weight[ht * kGroup + k]);
-                        for (int k = 0; k < count; ++k) {
-                            const float f = top == -INFINITY ? 0.0f : exp2_fast(weight[ht * kGroup + k] - top);
-                            sum = __fmaf_rn(sums[ht * kGroup + k], f, sum);
-                            weight[ht * kGroup + k] = f;
-                        }
-                        row_scales[ht] = top;
-                        row_sums[ht] = sum;
-                    }
-                    bar_half(half);
                     const bool last = level == 1 || groups == 1;
-                    float *const to = part_of(at_cta);
-                    constexpr int kQuads = DP / 4;
-                    for (int i = ht; i < rows * kQuads; i += kTcHalf) {
-                        const int rr = i / kQuads, d = i % kQuads * 4, out_row = row0 + rr;
-                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
+                    if (active) {
+                        float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
                         for (int k = 0; k < count; ++k) {
-                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part_of(at_cta + k * stride) + rr * DP + d));
-                            const float f = weight[rr * kGroup + k];
-                            v.x = __fmaf_rn(y.x, f, v.x), v.y = __fmaf_rn(y.y, f, v.y);
-                            v.z = __fmaf_rn(y.z, f, v.z), v.w = __fmaf_rn(y.w, f, v.w);
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_of(at_cta + k * stride) + kTcHalf * DP + 2 * ht));
+                            const float next = max_nan(top, ml.x);
+                            const float zero = next == -INFINITY ? 0.0f : next;
+                            sum = __fmaf_rn(ml.y, exp2_fast(ml.x - zero), sum * exp2_fast(top - zero));
+                            top = next;
                         }
-                        if (last) {
-                            attn_write(a, bf16, dim, walk.x.q0 + out_row / group, walk.head * group + out_row % group, d, v,
-                                       row_scales[rr], row_sums[rr]);
-                        } else {
-                            __stcg(reinterpret_cast<float4 *>(to + rr * DP + d), v);
-                            if (d == 0)
-                                __stcg(reinterpret_cast<float2 *>(to + kTcHalf * DP + 2 * rr),
-                                       make_float2(row_scales[rr], row_sums[rr]));
+                        const float zero = top == -INFINITY ? 0.0f : top, inv = sum == 0.0f ? 1.0f : 1.0f / sum;
+                        float *const to = last ? nullptr : part_of(at_cta);
+#pragma unroll 1
+                        for (int cc = 0; cc < DP / 32; ++cc) {
+                            float y[32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) y[k] = 0.0f;
+#pragma unroll 2
+                            for (int k = 0; k < count; ++k) {
+                                const float *const src = part_of(at_cta + k * stride);
+                                const float f = exp2_fast(__ldcg(src + kTcHalf * DP + 2 * ht) - zero);
+                                float4 w[8];
+#pragma unroll
+                                for (int u = 0; u < 8; ++u)
+                                    w[u] = __ldcg(reinterpret_cast<const float4 *>(src + ((cc * 8 + u) * kTcHalf + ht) * 4));
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) {
+                                    y[4 * u] = __fmaf_rn(w[u].x, f, y[4 * u]), y[4 * u + 1] = __fmaf_rn(w[u].y, f, y[4 * u + 1]);
+                                    y[4 * u + 2] = __fmaf_rn(w[u].z, f, y[4 * u + 2]), y[4 * u + 3] = __fmaf_rn(w[u].w, f, y[4 * u + 3]);
+                                }
+                            }
+                            put(to, cc, y, inv);
                         }
+                        finish(to, top, sum);
                     }
                     if (last) break;
                     counter = counters + 4 * kTcMostCtas + slot_of(walk.part_first_cta) * 2 + half;
@@ -773,7 +782,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     count = groups;
                     stride = kGroup;
                 }
-                bar_half(half);  // the queries' tile and row_scale are free again
             }
         }
     }
