@@ -238,7 +238,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int ct = tid - 256;
         constexpr int kPer = DP / 16;           // 16-byte pieces of a padded row; also passes
         constexpr int kPassRows = 128 / kPer;
-        const int q_l = ct % kPer, row_l = ct / kPer;
+        // a thread's piece and row of a pass: the eight lanes of one phase hold
+        // four pieces of an even and of an odd row, whose swizzled places differ
+        const int q_l = kPer == 8 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
+        const int row_l = kPer == 8 ? (warp & 3) * 4 + (lane >> 4) * 2 + (lane >> 2 & 1) : (warp & 3) * 8 + (lane >> 2);
         const bool in_row = FULL || q_l * 16 < dim;
         const int in_block = (1 << c.shift) - 1;
         uint32_t it = 0;
@@ -289,18 +292,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     uint32_t h[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) codes_f16(w[i], h[2 * i], h[2 * i + 1]);
-                    // two 16-byte pieces; lanes of the second slab store theirs
-                    // in the other order, so that a phase meets no bank twice
-                    const bool swap = (q_l >> 2) & 1;
-                    const int piece = (q_l & 3) * 2;
-                    const uint32_t first = base + swizzled(row, piece + (swap ? 1 : 0));
-                    const uint32_t second = base + swizzled(row, piece + (swap ? 0 : 1));
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(first), "r"(swap ? h[4] : h[0]),
-                                 "r"(swap ? h[5] : h[1]), "r"(swap ? h[6] : h[2]), "r"(swap ? h[7] : h[3])
-                                 : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(second), "r"(swap ? h[0] : h[4]),
-                                 "r"(swap ? h[1] : h[5]), "r"(swap ? h[2] : h[6]), "r"(swap ? h[3] : h[7])
-                                 : "memory");
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(base + swizzled(row, (q_l & 3) * 2 + i)),
+                                     "r"(h[4 * i]), "r"(h[4 * i + 1]), "r"(h[4 * i + 2]), "r"(h[4 * i + 3])
+                                     : "memory");
                 }
             };
             if (tiles > 0) {
@@ -426,7 +422,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces;  // pieces of a row, rows per instruction
                 const int i = lane % kPieces;
                 const bool on = FULL || i * 8 < dim;
-#pragma unroll 8
+#pragma unroll 4
                 for (int u = 0; u < 32; u += kAtOnce) {
                     const int in_warp = u + lane / kPieces, rr = hw * 32 + in_warp;
                     const long long tok = walk_q0 + __shfl_sync(~0u, token, in_warp), hd = __shfl_sync(~0u, head, in_warp);
@@ -444,18 +440,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             float row_scale = 0.0f;
             if (tiles > 0) {
-                constexpr int kPieces = DP / 8;
-                uint4 piece[kPieces];
+                // (loops kept rolled here and below: code that runs once an item
+                // comes through the instruction cache each time)
                 rows_move(true);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i)
-                    piece[i] = *reinterpret_cast<const uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(ht, i & 7));
                 float amax = 0.0f;
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
+#pragma unroll 2
+                for (int i = 0; i < DP / 8; ++i) {
                     float f[8];
-                    if (bf16) widen8<1>(piece[i], f); else widen8<0>(piece[i], f);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(ht, i & 7));
+                    if (bf16) widen8<1>(w, f); else widen8<0>(w, f);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
                 }
@@ -466,14 +459,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 const float down1 = pow2i(-(e / 2)) * (a.scale < 0.0f ? -1.0f : 1.0f), down2 = pow2i(-(e - e / 2));
                 row_scale = ldexpf(fabsf(a.scale) * 1.4426950408889634f, e);
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
+#pragma unroll 2
+                for (int i = 0; i < DP / 8; ++i) {
                     float f[8];
-                    if (bf16) widen8<1>(piece[i], f); else widen8<0>(piece[i], f);
+                    uint4 *const at = reinterpret_cast<uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(ht, i & 7));
+                    const uint4 w = *at;
+                    if (bf16) widen8<1>(w, f); else widen8<0>(w, f);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) f[k] = f[k] * down1 * down2;
-                    *reinterpret_cast<uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(ht, i & 7)) =
-                        make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
+                    *at = make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
                 }
                 smem_to_tensor_fence();
                 mbar_arrive(&sm.q_full[half]);
@@ -500,55 +494,50 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const bool mask = !meta.plain || key0 + kTcKeys > seen_end || key0 < seen_begin;
                     float top = -INFINITY;
                     int e;
-                    uint32_t v[2][32];
-                    tc_ld32(scol, v[0]);
-                    float f8[8];  // the groups' score factors
-#pragma unroll
-                    for (int k = 0; k < 8; k += 4) {
-                        const float4 x = *reinterpret_cast<const float4 *>(meta.ks + k);
-                        f8[k] = row_scale * x.x, f8[k + 1] = row_scale * x.y;
-                        f8[k + 2] = row_scale * x.z, f8[k + 3] = row_scale * x.w;
-                    }
                     if (!mask) {
                         // scales are not negative: a group's largest score is
                         // its largest product, scaled
                         e = meta.vexp;
+                        uint32_t v[2][32];
+                        tc_ld32(scol, v[0]);
+#pragma unroll 1
+                        for (int cc = 0; cc < 4; cc += 2) {
 #pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) {
-                            tc_wait_ld(v[cc & 1]);
-                            if (cc < 3) tc_ld32(scol + (cc + 1) * 32, v[(cc + 1) & 1]);
+                            for (int u = 0; u < 2; ++u) {
+                                tc_wait_ld(v[u]);
+                                // (past the last 32 the first ones again, unused)
+                                tc_ld32(scol + ((cc + u + 1) & 3) * 32, v[u ^ 1]);
 #pragma unroll
-                            for (int gr = 0; gr < 2; ++gr) {
-                                const uint32_t *w = v[cc & 1] + gr * 16;
-                                float x[4];
+                                for (int gr = 0; gr < 2; ++gr) {
+                                    const uint32_t *w = v[u] + gr * 16;
+                                    float x[4];
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    x[k] = max3_nan(max_nan(__uint_as_float(w[4 * k]), __uint_as_float(w[4 * k + 1])),
-                                                    __uint_as_float(w[4 * k + 2]), __uint_as_float(w[4 * k + 3]));
-                                const float y = max3_nan(max_nan(x[0], x[1]), x[2], x[3]);
-                                top = max_nan(top, y * f8[cc * 2 + gr]);
+                                    for (int k = 0; k < 4; ++k)
+                                        x[k] = max3_nan(max_nan(__uint_as_float(w[4 * k]), __uint_as_float(w[4 * k + 1])),
+                                                        __uint_as_float(w[4 * k + 2]), __uint_as_float(w[4 * k + 3]));
+                                    const float y = max3_nan(max_nan(x[0], x[1]), x[2], x[3]);
+                                    top = max_nan(top, y * (row_scale * meta.ks[(cc + u) * 2 + gr]));
+                                }
                             }
                         }
+                        tc_wait_ld(v[0]);
                     } else {
                         e = kLeastExp;
-#pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) {
-                            tc_wait_ld(v[cc & 1]);
-                            if (cc < 3) tc_ld32(scol + (cc + 1) * 32, v[(cc + 1) & 1]);
-#pragma unroll
-                            for (int gr = 0; gr < 2; ++gr) {
-                                const int g8 = cc * 2 + gr, key = key0 + g8 * 16;
-                                const bool ok = meta.valid >> g8 & 1;
+#pragma unroll 1
+                        for (int g8 = 0; g8 < 8; ++g8) {
+                            uint32_t y[16];
+                            tc_ld16(scol + g8 * 16, y);
+                            tc_wait_ld(y);
+                            const int key = key0 + g8 * 16;
+                            if ((meta.valid >> g8 & 1) && key < row_end && key + 16 > row_begin) {
                                 float x = -INFINITY;
 #pragma unroll
                                 for (int k = 0; k < 16; ++k)
-                                    if (ok && key + k < row_end && key + k >= row_begin)
-                                        x = max_nan(x, __uint_as_float(v[cc & 1][gr * 16 + k]));
-                                if (ok && key < row_end && key + 16 > row_begin) {
-                                    top = max_nan(top, x * (row_scale * meta.ks[g8]));
-                                    e = max(e, scale_exp(meta.vs[g8]));
-                                }
+                                    if (key + k < row_end && key + k >= row_begin) x = max_nan(x, __uint_as_float(y[k]));
+                                top = max_nan(top, x * (row_scale * meta.ks[g8]));
+                                e = max(e, scale_exp(meta.vs[g8]));
                             }
+                            __syncwarp();
                         }
                     }
                     const bool grew = !(top <= m + kSlack) || e > ve + kScaleSlack;
@@ -563,11 +552,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (i > 0) {
 #pragma unroll 1
                             for (int cc = 0; cc < DP / 32; ++cc) {
-                                tc_ld32(ocol + cc * 32, v[0]);
-                                tc_wait_ld(v[0]);
+                                uint32_t v[32];
+                                tc_ld32(ocol + cc * 32, v);
+                                tc_wait_ld(v);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) v[0][k] = __float_as_uint(__uint_as_float(v[0][k]) * fo);
-                                tc_st32(ocol + cc * 32, v[0]);
+                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * fo);
+                                tc_st32(ocol + cc * 32, v);
                             }
                         }
                     }
@@ -582,7 +572,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const float lift = base + static_cast<float>(kTcWeightExp - ve);
                         float sums = 0.0f;
                         auto exponents = [&](uint32_t (&y)[16], int g8) {
-                            const float f = f8[g8], add = lift + meta.vlog[g8];
+                            const float f = row_scale * meta.ks[g8], add = lift + meta.vlog[g8];
 #pragma unroll
                             for (int k = 0; k < 16; k += 2) {
                                 const float2 z = fma2(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])),
@@ -599,29 +589,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         exponents(x[0], 0);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) x[0][k] = __float_as_uint(exp2_fast(__uint_as_float(x[0][k])));
+#pragma unroll 1
+                        for (int g0 = 0; g0 < 8; g0 += 2) {
 #pragma unroll
-                        for (int g8 = 0; g8 < 8; ++g8) {
-                            uint32_t(&now)[16] = x[g8 & 1], (&next)[16] = x[(g8 + 1) & 1];
-                            if (g8 < 7) {
+                            for (int u = 0; u < 2; ++u) {
+                                // (past the last group the first ones again, unused:
+                                // P of 16 keys takes 8 columns, all of them read before)
+                                const int g8 = g0 + u;
+                                uint32_t(&now)[16] = x[u], (&next)[16] = x[u ^ 1];
                                 tc_wait_ld(next);
-                                exponents(next, g8 + 1);
-                            }
-                            uint32_t p[8];
-                            float2 part[2];
+                                exponents(next, (g8 + 1) & 7);
+                                uint32_t p[8];
+                                float2 part[2];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float2 y = make_float2(__uint_as_float(now[2 * k]), __uint_as_float(now[2 * k + 1]));
-                                if (g8 < 7) next[2 * k] = __float_as_uint(exp2_fast(__uint_as_float(next[2 * k])));
-                                p[k] = pack_f16(y.x, y.y);
-                                if (g8 < 7) next[2 * k + 1] = __float_as_uint(exp2_fast(__uint_as_float(next[2 * k + 1])));
-                                part[k & 1] = k < 2 ? y : add2(part[k & 1], y);
+                                for (int k = 0; k < 8; ++k) {
+                                    const float2 y = make_float2(__uint_as_float(now[2 * k]), __uint_as_float(now[2 * k + 1]));
+                                    next[2 * k] = __float_as_uint(exp2_fast(__uint_as_float(next[2 * k])));
+                                    p[k] = pack_f16(y.x, y.y);
+                                    next[2 * k + 1] = __float_as_uint(exp2_fast(__uint_as_float(next[2 * k + 1])));
+                                    part[k & 1] = k < 2 ? y : add2(part[k & 1], y);
+                                }
+                                part[0] = add2(part[0], part[1]);
+                                sums = __fmaf_rn(part[0].x + part[0].y, meta.vinv[g8], sums);
+                                tc_ld16(scol + ((g8 + 2) & 7) * 16, now);
+                                tc_st8(scol + g8 * 8, p);
                             }
-                            part[0] = add2(part[0], part[1]);
-                            sums = __fmaf_rn(part[0].x + part[0].y, meta.vinv[g8], sums);
-                            if (g8 < 6) tc_ld16(scol + (g8 + 2) * 16, now);
-                            // P of 16 keys takes 8 columns, all of them read before
-                            tc_st8(scol + g8 * 8, p);
                         }
+                        tc_wait_ld(x[1]);
                         l = __fmaf_rn(sums, pow2i(ve - kTcWeightExp), l);
                     } else {
                         const float up = pow2i(kTcWeightExp - ve);
