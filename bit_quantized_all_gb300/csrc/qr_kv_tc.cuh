@@ -42,13 +42,13 @@ constexpr int kTcWeightExp = 7;  // weight 1 of the largest scale is 2^7
 // Tensor memory columns: S of both halves (P in its place), O of both halves.
 constexpr uint32_t kColS = 0, kColO = 256, kColumns = 512;
 
+// A tile's scales and what follows from them, read a 16-key group ahead of
+// its use: beside the products, which read shared memory at its full rate, a
+// load of it takes 100 to 170 cycles.
 struct alignas(16) TcMeta {
-    float ks[8], vs[8];
-    float vlog[8], vinv[8];  // log2 and reciprocal of vs
-    uint32_t valid;
-    int vexp;   // the largest scale_exp of the tile's valid groups
-    int plain;  // every group is valid and no vs is zero (or near it)
-    int pad;
+    float4 group[8];  // key scale; log2 of, one over, and the value scale
+    int4 tile;        // valid groups; the largest scale_exp among them; whether
+                      // every group is valid and no value scale is zero or near it
 };
 
 // Floats of one half's part: accumulators, then (max, sum) pairs.
@@ -322,17 +322,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t sized = __ballot_sync(~0u, e > kLeastExp && e < 120);
 #pragma unroll
                     for (int d = 1; d < 8; d <<= 1) e = max(e, __shfl_xor_sync(~0u, e, d));
-                    if (ct < 8) {
-                        meta.ks[ct] = ks_now;
-                        meta.vs[ct] = vs_now;
-                        meta.vlog[ct] = log2_fast(vs_now);
-                        meta.vinv[ct] = 1.0f / vs_now;
-                    }
-                    if (ct == 0) {
-                        meta.valid = valid;
-                        meta.vexp = e;
-                        meta.plain = (valid & sized) == 0xffu;
-                    }
+                    if (ct < 8) meta.group[ct] = make_float4(ks_now, log2_fast(vs_now), 1.0f / vs_now, vs_now);
+                    if (ct == 0) meta.tile = make_int4(static_cast<int>(valid), e, (valid & sized) == 0xffu, 0);
                 }
                 smem_to_tensor_fence();
                 mbar_arrive(&sm.k_full[s]);
@@ -422,18 +413,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces;  // pieces of a row, rows per instruction
                 const int i = lane % kPieces;
                 const bool on = FULL || i * 8 < dim;
-#pragma unroll 4
-                for (int u = 0; u < 32; u += kAtOnce) {
-                    const int in_warp = u + lane / kPieces, rr = hw * 32 + in_warp;
+                auto place = [&](int u, const uint16_t *base, long long token_stride, long long head_stride) {
+                    const int in_warp = u + lane / kPieces;
                     const long long tok = walk_q0 + __shfl_sync(~0u, token, in_warp), hd = __shfl_sync(~0u, head, in_warp);
-                    uint4 *const tile = reinterpret_cast<uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(rr, i & 7));
-                    if (in) {
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (rr < rows && on)
-                            w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + tok * a.q_token + hd * a.q_head + i * 8);
-                        *tile = w;
-                    } else if (rr < rows && on) {
-                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + tok * a.out_token + hd * a.out_head + i * 8) = *tile;
+                    return base + tok * token_stride + hd * head_stride + i * 8;
+                };
+                auto tile = [&](int u) {
+                    return reinterpret_cast<uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(hw * 32 + u + lane / kPieces, i & 7));
+                };
+                auto there = [&](int u) { return hw * 32 + u + lane / kPieces < rows && on; };
+                if (in) {
+                    uint4 w[32 / kAtOnce];  // all on their way at once
+#pragma unroll
+                    for (int u = 0; u < 32; u += kAtOnce) {
+                        const uint16_t *src = place(u, static_cast<const uint16_t *>(a.q), a.q_token, a.q_head);
+                        w[u / kAtOnce] = make_uint4(0, 0, 0, 0);
+                        if (there(u)) w[u / kAtOnce] = *reinterpret_cast<const uint4 *>(src);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 32; u += kAtOnce) *tile(u) = w[u / kAtOnce];
+                } else {
+#pragma unroll 4
+                    for (int u = 0; u < 32; u += kAtOnce) {
+                        const uint16_t *to = place(u, static_cast<uint16_t *>(a.out), a.out_token, a.out_head);
+                        if (there(u)) *reinterpret_cast<uint4 *>(const_cast<uint16_t *>(to)) = *tile(u);
                     }
                 }
                 __syncwarp();
@@ -491,22 +494,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (active) {
                     const TcMeta &meta = sm.meta[it & 3];
                     const int key0 = begin + i * kTcKeys;
-                    const bool mask = !meta.plain || key0 + kTcKeys > seen_end || key0 < seen_begin;
+                    const int4 tile = meta.tile;
+                    float4 now4 = meta.group[0], next4 = meta.group[1];
+                    const bool mask = !tile.z || key0 + kTcKeys > seen_end || key0 < seen_begin;
                     float top = -INFINITY;
                     int e;
                     if (!mask) {
                         // scales are not negative: a group's largest score is
                         // its largest product, scaled
-                        e = meta.vexp;
+                        e = tile.y;
                         uint32_t v[2][32];
                         tc_ld32(scol, v[0]);
+                        float ks0 = now4.x, ks1 = next4.x;
 #pragma unroll 1
                         for (int cc = 0; cc < 4; cc += 2) {
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
+                                const int ahead = (cc + u + 1) & 3;
                                 tc_wait_ld(v[u]);
                                 // (past the last 32 the first ones again, unused)
-                                tc_ld32(scol + ((cc + u + 1) & 3) * 32, v[u ^ 1]);
+                                tc_ld32(scol + ahead * 32, v[u ^ 1]);
+                                const float f0 = row_scale * ks0, f1 = row_scale * ks1;
+                                ks0 = meta.group[ahead * 2].x;
+                                ks1 = meta.group[ahead * 2 + 1].x;
 #pragma unroll
                                 for (int gr = 0; gr < 2; ++gr) {
                                     const uint32_t *w = v[u] + gr * 16;
@@ -516,7 +526,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                         x[k] = max3_nan(max_nan(__uint_as_float(w[4 * k]), __uint_as_float(w[4 * k + 1])),
                                                         __uint_as_float(w[4 * k + 2]), __uint_as_float(w[4 * k + 3]));
                                     const float y = max3_nan(max_nan(x[0], x[1]), x[2], x[3]);
-                                    top = max_nan(top, y * (row_scale * meta.ks[(cc + u) * 2 + gr]));
+                                    top = max_nan(top, y * (gr ? f1 : f0));
                                 }
                             }
                         }
@@ -529,13 +539,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tc_ld16(scol + g8 * 16, y);
                             tc_wait_ld(y);
                             const int key = key0 + g8 * 16;
-                            if ((meta.valid >> g8 & 1) && key < row_end && key + 16 > row_begin) {
+                            const float4 scales = meta.group[g8];
+                            if ((tile.x >> g8 & 1) && key < row_end && key + 16 > row_begin) {
                                 float x = -INFINITY;
 #pragma unroll
                                 for (int k = 0; k < 16; ++k)
                                     if (key + k < row_end && key + k >= row_begin) x = max_nan(x, __uint_as_float(y[k]));
-                                top = max_nan(top, x * (row_scale * meta.ks[g8]));
-                                e = max(e, scale_exp(meta.vs[g8]));
+                                top = max_nan(top, x * (row_scale * scales.x));
+                                e = max(e, scale_exp(scales.w));
                             }
                             __syncwarp();
                         }
@@ -571,8 +582,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!mask && !__any_sync(~0u, !(fabsf(m) < 65536.0f))) {
                         const float lift = base + static_cast<float>(kTcWeightExp - ve);
                         float sums = 0.0f;
-                        auto exponents = [&](uint32_t (&y)[16], int g8) {
-                            const float f = row_scale * meta.ks[g8], add = lift + meta.vlog[g8];
+                        auto exponents = [&](uint32_t (&y)[16], const float4 &scales) {
+                            const float f = row_scale * scales.x, add = lift + scales.y;
 #pragma unroll
                             for (int k = 0; k < 16; k += 2) {
                                 const float2 z = fma2(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])),
@@ -586,7 +597,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         // the other they would each wait for their own latency
                         tc_wait_ld(x[0]);
                         tc_ld16(scol + 16, x[1]);
-                        exponents(x[0], 0);
+                        exponents(x[0], now4);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) x[0][k] = __float_as_uint(exp2_fast(__uint_as_float(x[0][k])));
 #pragma unroll 1
@@ -598,7 +609,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 const int g8 = g0 + u;
                                 uint32_t(&now)[16] = x[u], (&next)[16] = x[u ^ 1];
                                 tc_wait_ld(next);
-                                exponents(next, (g8 + 1) & 7);
+                                const float4 ahead4 = meta.group[(g8 + 2) & 7];
+                                exponents(next, next4);
                                 uint32_t p[8];
                                 float2 part[2];
 #pragma unroll
@@ -610,7 +622,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     part[k & 1] = k < 2 ? y : add2(part[k & 1], y);
                                 }
                                 part[0] = add2(part[0], part[1]);
-                                sums = __fmaf_rn(part[0].x + part[0].y, meta.vinv[g8], sums);
+                                sums = __fmaf_rn(part[0].x + part[0].y, now4.z, sums);
+                                now4 = next4;
+                                next4 = ahead4;
                                 tc_ld16(scol + ((g8 + 2) & 7) * 16, now);
                                 tc_st8(scol + g8 * 8, p);
                             }
@@ -622,10 +636,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                         for (int g8 = 0; g8 < 8; ++g8) {
                             const int key = key0 + g8 * 16;
-                            const float f = row_scale * meta.ks[g8], vs = meta.vs[g8];
+                            const float4 scales = meta.group[g8];
+                            const float f = row_scale * scales.x, vs = scales.w;
                             // (a group beyond the row's power of two is not seen by it)
                             const float w = scale_exp(vs) > ve + kScaleSlack ? 0.0f : vs * up;
-                            const bool ok = meta.valid >> g8 & 1;
+                            const bool ok = tile.x >> g8 & 1;
                             uint32_t p[8];
                             tc_wait_ld(x[0]);
 #pragma unroll
