@@ -148,19 +148,6 @@ __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// Waits for a phase; after a wait that ran out every wait of the CTA fails.
-__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {
-    if (*static_cast<volatile int *>(fail)) return mbar_try_wait(bar, parity);
-    if (mbar_wait_suspended(bar, parity)) return true;
-    if (atomicExch(fail, 1) == 0) atomicAdd(timeouts, 1u);
-    return false;
-}
-
-// ... by a whole warp, whose lanes then go on together.
-__device__ __forceinline__ bool tc_wait_warp(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {
-    return __all_sync(~0u, tc_wait(bar, parity, fail, timeouts));
-}
-
 // The 128 threads of one half's softmax.
 __device__ __forceinline__ void bar_half(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 

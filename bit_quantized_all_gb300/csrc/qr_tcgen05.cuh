@@ -24,10 +24,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t slab, uint
            static_cast<uint64_t>((group >> 4) & 0x3fff) << 32 | 1ull << 46 | 2ull << 61;
 }
 
-// Instruction descriptor: fp16 x fp16 -> fp32, M = 128, N = n; b_rows_k: the
-// rows of B's tile run along K (else along N).
-__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_rows_k) {
-    return 1u << 4 | (b_rows_k ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
+// Instruction descriptor: fp16 x fp16 (or bf16 x bf16) -> fp32, M = 128, N = n;
+// b_rows_k: the rows of B's tile run along K (else along N).
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_rows_k, bool bf16 = false) {
+    return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_rows_k ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
 }
 
 // One lane of the calling warp, the same at every call.
@@ -101,6 +101,19 @@ __device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t pari
     }
 }
 
+// Waits for a phase; after a wait that ran out (counted once a CTA) every wait
+// of the CTA fails at once.
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {
+    if (*static_cast<volatile int *>(fail)) return mbar_try_wait(bar, parity);
+    if (mbar_wait_suspended(bar, parity)) return true;
+    if (atomicExch(fail, 1) == 0) atomicAdd(timeouts, 1u);
+    return false;
+}
+// ... by a whole warp, whose lanes then go on together.
+__device__ __forceinline__ bool tc_wait_warp(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {
+    return __all_sync(~0u, tc_wait(bar, parity, fail, timeouts));
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -127,6 +140,14 @@ __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&v)[16]) {
 }
 __device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), QR_I8(v, 0));
+}
+// 16 lanes x 32 columns in the order of the m16n8k16 instructions' A fragments:
+// lane 4 g + t of the warp holds columns 8 i + 2 t and the next of lane g in
+// v[4 i], v[4 i + 1] and of lane g + 8 in v[4 i + 2], v[4 i + 3].
+__device__ __forceinline__ void tc_st_fragments(uint32_t addr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        QR_I8(v, 0), QR_I8(v, 8));
 }
 __device__ __forceinline__ void tc_wait_ld(uint32_t (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : QR_T8(v, 0), QR_T8(v, 8));

@@ -14,10 +14,8 @@
 // distributed shared memory: no workspace, no second launch.
 #include <cooperative_groups.h>
 
-#include "qr_device.cuh"
-#include "qr_kv_device.cuh"
 #include "qr_launch.h"
-#include "qr_serving.h"
+#include "qr_w4.cuh"
 
 namespace qrk {
 
@@ -25,15 +23,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kMvWarps = 8, kMvThreads = 32 * kMvWarps;
 constexpr int kMvDepth = 4;  // chunks of weights in flight per warp
-
-struct W4MatvecArgs {
-    const uint16_t *x;
-    uint16_t *y;
-    const uint8_t *packed;
-    long long x_stride, y_stride, tokens;
-    int rows, cols, group_shift;  // group = 32 << group_shift
-    W4Layout l;
-};
 
 template <int DT>
 __device__ __forceinline__ void mma_typed(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool first) {
@@ -45,50 +34,6 @@ __device__ __forceinline__ void mma_typed(float (&d)[4], const uint32_t (&a)[4],
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     }
-}
-
-// A fragment register from a word shifted so that its pair of codes is in
-// bits 0..3 and 16..19, minus the offset pair `zero` (1024 + z or 128 + z).
-template <int DT>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t zero) {
-    uint32_t v = (w & 0x000f000fu) | (DT == 0 ? 0x64006400u : 0x43004300u);
-    if constexpr (DT == 0) {
-        const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&zero));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    } else {
-        const __nv_bfloat162 r =
-            __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&zero));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    }
-}
-
-// The first `have` (at most 8; none if below 1) 16-bit values from a 2-byte
-// aligned address, zeros after them: from the one or two aligned 16-byte words
-// that hold them.
-__device__ __forceinline__ uint4 load8_any(const uint16_t *p, int have) {
-    if (have <= 0) return make_uint4(0, 0, 0, 0);
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const uint32_t off = static_cast<uint32_t>(at & 15);
-    const uint4 *src = reinterpret_cast<const uint4 *>(at - off);
-    const uint4 a = *src;
-    uint4 b = make_uint4(0, 0, 0, 0);
-    if (off + 2 * have > 16) b = src[1];
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (off & 8) {
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (off & 4) {
-#pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-    const uint32_t bits = (off & 2) * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = __funnelshift_r(w[i], w[i + 1], bits);
-        if (2 * i + 1 >= have) w[i] = 2 * i >= have ? 0u : w[i] & 0xffffu;
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int NT>
@@ -308,8 +253,7 @@ template <int DT>
 static cudaError_t pick_tokens(const W4MatvecArgs &a, bool zeros, cudaStream_t s) {
     if (a.tokens <= 8) return pick_group<DT, 1, 1>(a, zeros, s);
     if (a.tokens <= 16) return pick_group<DT, 2, 2>(a, zeros, s);
-    if (a.tokens <= 32) return pick_group<DT, 2, 4>(a, zeros, s);
-    return pick_group<DT, 2, 8>(a, zeros, s);
+    return launch_w4_tc(DT, a, zeros, s);
 }
 
 cudaError_t launch_w4_matvec(int dtype, long long tokens, const void *x, long long x_stride, int rows, int cols,
