@@ -79,35 +79,33 @@ __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sy
 // Makes this thread's writes to shared memory visible to the tensor cores.
 __device__ __forceinline__ void smem_to_tensor_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// As mbar_wait, but the thread is suspended for up to kSuspendNs at a time
-// instead of asking again and again: warps that wait beside others that
-// compute leave them the issue slots.
+// Waits for a phase, the thread suspended for up to kSuspendNs at a time rather
+// than asking again and again: warps that wait beside others that compute leave
+// them the issue slots.  After a wait that ran out (counted once a CTA) every
+// wait of the CTA fails at its next look.
 constexpr uint32_t kSuspendNs = 1000000;
-__device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t parity) {
-    unsigned long long t0 = 0;
-    for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendNs)
-            : "memory");
-        if (done) return true;
-        const unsigned long long now = global_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > kWaitLimitNs) return false;
-    }
+__device__ __forceinline__ bool mbar_try_suspended(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    return done != 0;
 }
-
-// Waits for a phase; after a wait that ran out (counted once a CTA) every wait
-// of the CTA fails at once.
 __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {
-    if (*static_cast<volatile int *>(fail)) return mbar_try_wait(bar, parity);
-    if (mbar_wait_suspended(bar, parity)) return true;
-    if (atomicExch(fail, 1) == 0) atomicAdd(timeouts, 1u);
-    return false;
+    if (mbar_try_suspended(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    while (!*static_cast<volatile int *>(fail)) {
+        if (mbar_try_suspended(bar, parity)) return true;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            if (atomicExch(fail, 1) == 0) atomicAdd(timeouts, 1u);
+            return false;
+        }
+    }
+    return mbar_try_wait(bar, parity);
 }
 // ... by a whole warp, whose lanes then go on together.
 __device__ __forceinline__ bool tc_wait_warp(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {

@@ -1,16 +1,16 @@
 // qr_w4.cu -- 4-bit weights with group scales: packing and quantizing
 // (qr_w4_pack, qr_w4_quantize); the product is in qr_w4_matvec.cu.
 //
-// Packed order.  y^T = W x^T runs on m16n8k16 matrix instructions with 16
-// weight rows as M and 8 tokens as N.  A tile of 16 rows x 64 columns is 512
-// bytes, lane l = 4g + t of a warp owning 16 of them: word j (j = 0..3) is its
-// A fragment of the j-th instruction, eight codes of rows g and g + 8 at the
-// four columns 32*(j/2) + 8t + 4*(j%2) + 0..3.  Which column stands at which k
-// of the instruction is free as long as x is loaded alike, and this order
-// keeps a group of 32 columns within two instructions and lets a lane read
-// its x values as two 16-byte pieces.  In a word, nibble i and nibble i + 4
-// are the two codes of fragment register i, so that (word >> 4i) & 0x000f000f
-// is a register's pair of codes.
+// Packed order.  y^T = W x^T runs on 16-bit matrix instructions with 16 weight
+// rows as M and tokens as N.  A tile of 16 rows x 64 columns is 512 bytes, lane
+// l = 4g + t of a warp owning 16 of them: word j (j = 0..3) is its A fragment of
+// the j-th instruction of 16 columns, eight codes of rows g and g + 8 at the
+// four columns 16 j + 4 t + 0..3.  Which of an instruction's sixteen columns
+// stands at which of its places is free as long as x is read alike; so a lane
+// reads its x values as four 8-byte pieces, and the fragments stored to
+// tensor memory (qr_w4_tc.cu) have the columns in their own order.  In a word,
+// nibble i and nibble i + 4 are the two codes of fragment register i, so that
+// (word >> 4i) & 0x000f000f is a register's pair of codes.
 #include "qr_device.cuh"
 #include "qr_launch.h"
 #include "qr_serving.h"
@@ -22,7 +22,7 @@ constexpr int kW4Threads = 256;
 // Column (within 64) of nibble `nib` of word j of lane t; its row is
 // g + 8 * (nib & 1).
 __device__ __forceinline__ int w4_column(int t, int j, int nib) {
-    return 32 * (j >> 1) + 8 * t + 4 * (j & 1) + 2 * ((nib & 3) >> 1) + (nib >> 2);
+    return 16 * j + 4 * t + 2 * ((nib & 3) >> 1) + (nib >> 2);
 }
 
 // One thread per word of codes, scale pair and zero pair.

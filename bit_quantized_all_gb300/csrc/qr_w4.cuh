@@ -31,17 +31,9 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t zero) {
     }
 }
 
-// The first `have` (at most 8; none if below 1) 16-bit values from a 2-byte
-// aligned address, zeros after them: from the one or two aligned 16-byte words
-// that hold them.
-__device__ __forceinline__ uint4 load8_any(const uint16_t *p, int have) {
-    if (have <= 0) return make_uint4(0, 0, 0, 0);
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const uint32_t off = static_cast<uint32_t>(at & 15);
-    const uint4 *src = reinterpret_cast<const uint4 *>(at - off);
-    const uint4 a = *src;
-    uint4 b = make_uint4(0, 0, 0, 0);
-    if (off + 2 * have > 16) b = src[1];
+// Eight 16-bit values from byte `off` (even) of two 16-byte words on, those
+// past the first `have` zero.
+__device__ __forceinline__ uint4 take8(const uint4 &a, const uint4 &b, uint32_t off, int have) {
     uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (off & 8) {
 #pragma unroll
@@ -58,6 +50,20 @@ __device__ __forceinline__ uint4 load8_any(const uint16_t *p, int have) {
         if (2 * i + 1 >= have) w[i] = 2 * i >= have ? 0u : w[i] & 0xffffu;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The first `have` (at most 8; none if below 1) 16-bit values from a 2-byte
+// aligned address, zeros after them: from the one or two aligned 16-byte words
+// that hold them.
+__device__ __forceinline__ uint4 load8_any(const uint16_t *p, int have) {
+    if (have <= 0) return make_uint4(0, 0, 0, 0);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint32_t off = static_cast<uint32_t>(at & 15);
+    const uint4 *src = reinterpret_cast<const uint4 *>(at - off);
+    const uint4 a = *src;
+    uint4 b = make_uint4(0, 0, 0, 0);
+    if (off + 2 * min(have, 8) > 16) b = src[1];
+    return take8(a, b, off, have);
 }
 
 // The tcgen05 kernel (qr_w4_tc.cu), for more tokens than matrix-vector

@@ -39,7 +39,7 @@ __device__ __forceinline__ void mma_typed(float (&d)[4], const uint32_t (&a)[4],
 template <int NT>
 struct MatvecSmem {
     static constexpr int kPanel = NT <= 2 ? 16 : 32 / NT;  // chunks of x held at a time
-    static constexpr int kPitch = kPanel * 128 + 64;       // bytes of a token's row: no bank conflicts
+    static constexpr int kPitch = kPanel * 128 + 32;       // bytes of a token's row: no bank conflicts
     static constexpr int kBuffer = 8 * NT * kPitch;
     static constexpr int kBytes = 2 * kBuffer;
 };
@@ -133,18 +133,17 @@ __global__ void __launch_bounds__(kMvThreads, RT *NT <= 8 ? 2 : 1) w4_matvec_ker
             }
             __syncthreads();
         }
-        const uint32_t xb = base + (i0 / S::kPanel & 1) * S::kBuffer + g * S::kPitch + t * 16;
+        const uint32_t xb = base + (i0 / S::kPanel & 1) * S::kBuffer + g * S::kPitch + t * 8;
 #pragma unroll
         for (int d = 0; d < kMvDepth; ++d) {
             const int i = i0 + d;
             if (i >= count) break;
             const uint32_t xa = xb + (i % S::kPanel) * 128;
-            uint4 xv[NT][2];
+            uint2 xv[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                xv[n][0] = lds128(xa + n * 8 * S::kPitch);
-                xv[n][1] = lds128(xa + n * 8 * S::kPitch + 64);
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) xv[n][j] = lds64(xa + n * 8 * S::kPitch + j * 32);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const uint32_t ww[4] = {w[d][r].x, w[d][r].y, w[d][r].z, w[d][r].w};
@@ -161,8 +160,7 @@ __global__ void __launch_bounds__(kMvThreads, RT *NT <= 8 ? 2 : 1) w4_matvec_ker
                                             code_pair<DT>(ww[j] >> 8, z0), code_pair<DT>(ww[j] >> 12, z1)};
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const uint4 &v = xv[n][j >> 1];
-                        mma_typed<DT>(part[n], af, j & 1 ? v.z : v.x, j & 1 ? v.w : v.y, NG == 2 ? (j & 1) == 0 : j == 0);
+                        mma_typed<DT>(part[n], af, xv[n][j].x, xv[n][j].y, NG == 2 ? (j & 1) == 0 : j == 0);
                     }
                     if (NG == 2 ? (j & 1) == 1 : j == 3) {
                         const float2 sc = __half22float2(*reinterpret_cast<const __half2 *>(&s[d][r][NG == 2 ? j >> 1 : 0]));

@@ -5,8 +5,7 @@
 // the columns, 64 columns (a chunk) at a time.  Four warps turn codes into the
 // type's exact integers u - z and store them as the A operand in tensor memory:
 // the packed words are the fragments of that store, so nothing is exchanged.
-// Four warps bring x into shared memory, its columns in the order that the
-// codes stand in.  One warp issues the products.  As scales differ from group
+// Four warps bring x into shared memory.  One warp issues the products.  As scales differ from group
 // to group, each group's (or chunk's, for groups of 128) products go to a ring
 // of accumulators of their own, and four warps, a thread per row, add them
 // scaled in fp32: the weights are never rounded.  The CTAs of a cluster add
@@ -29,6 +28,7 @@ constexpr int kWtThreads = 416;  // warps 0-3 codes, 4-7 sums, 8 products, 9-12 
 constexpr int kWtRows = 128;
 constexpr int kWtA = 4, kWtD = 4, kWtX = 8;  // buffers of codes, accumulators, x chunks
 constexpr int kWtAhead = 16;                 // chunks of codes on their way
+constexpr int kWtRaw = 6;                    // chunks of unaligned x on their way
 constexpr uint32_t kWtColD = kWtA * 32, kWtColumns = 512;
 
 template <int N>
@@ -37,14 +37,11 @@ struct WtSmem {
     uint8_t codes[4][kWtAhead][1024];               // by warp: its two row tiles
     uint8_t zeros[4][kWtAhead][64];
     uint8_t scales[4][kWtAhead][128];
+    uint8_t raw[kWtRaw][N][160];                    // chunks of unaligned x as they lie in memory
     uint64_t a_full[kWtA], a_done[kWtA], x_full[kWtX], x_done[kWtX], d_full[kWtD], d_done[kWtD];
     uint32_t tmem;
     int fail;
 };
-
-__device__ __forceinline__ void copy8_async(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 
 // N: tokens of a CTA; NG: groups of a 64-column chunk (2 for groups of 32, else 1).
 template <int DT, int N, int NG, bool ZEROS>
@@ -225,46 +222,96 @@ __global__ void __launch_bounds__(kWtThreads, 1) w4_tc_kernel(W4MatvecArgs a, in
             }
         }
     } else {
-        // ---- x: [token][64 columns], column 32 h + 8 t + 4 j + i of a chunk at
-        // place 32 h + 16 j + 4 t + i, as the codes stand
+        // ---- x: [token][64 columns]
         const int xt = tid - 288;
         for (int i = xt; i < kWtX * (N - tokens) * 8; i += 128) {  // rows past the tokens stay zero
             const int buf = i / ((N - tokens) * 8), row = tokens + i / 8 % (N - tokens);
             reinterpret_cast<uint4 *>(sm.x[buf])[row * 8 + i % 8] = make_uint4(0, 0, 0, 0);
         }
-        constexpr int kLag = kWtX - 2;  // chunks on their way
+        // this thread's pieces of a chunk: 16 bytes of rows m0, m0 + 16, ...
+        constexpr int kEach = N / 16;
+        const int m0 = xt >> 3, q = xt & 7;
+        const uint16_t *const src = a.x + (token0 + m0) * a.x_stride + static_cast<long long>(first) * 64 + q * 8;
+        auto tc_wait_if = [&](bool wanted, uint64_t *bar, uint32_t parity, int *f, unsigned *t) {
+            if (wanted) tc_wait_warp(bar, parity, f, t);
+        };
+        auto ready = [&](int i) {
+            return i < kWtX || tc_wait_warp(&sm.x_done[i % kWtX], (i / kWtX - 1) & 1, fail, timeouts);
+        };
         auto announce = [&](int i) {
             smem_to_tensor_fence();
             mbar_arrive(&sm.x_full[i % kWtX]);
         };
-        bool ok = true;
-        for (int i = 0; i < count + kLag && ok; ++i) {
-            if (i < count) {
-                if (i >= kWtX) ok = tc_wait_warp(&sm.x_done[i % kWtX], (i / kWtX - 1) & 1, fail, timeouts);
-                if (!ok) break;
-                const uint32_t buf = smem_addr(sm.x[i % kWtX]);
-                for (int p = xt; p < tokens * 8; p += 128) {
-                    const int m = p >> 3, q = p & 7, col = (first + i) * 64 + q * 8, have = min(8, a.cols - col);
-                    const uint16_t *src = a.x + (token0 + m) * a.x_stride + col;
-                    const uint32_t piece = (q >> 2) * 4 + ((q & 3) >> 1), half = (q & 1) * 8;
-                    const uint32_t lo = buf + swizzled(m, piece) + half, hi = buf + swizzled(m, piece + 2) + half;
-                    if (vector && have == 8) {
-                        copy8_async(lo, src);
-                        copy8_async(hi, src + 4);
-                    } else {
-                        const uint4 w = load8_any(src, have);
-                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(lo), "r"(w.x), "r"(w.y) : "memory");
-                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(hi), "r"(w.z), "r"(w.w) : "memory");
+        if (vector) {
+            constexpr int kLag = kWtX - 2;  // chunks on their way
+            for (int i = 0; i < count + kLag; ++i) {
+                if (i < count) {
+                    if (!ready(i)) break;
+                    const uint32_t buf = smem_addr(sm.x[i % kWtX]);
+                    const int have = a.cols - (first + i) * 64 - q * 8;
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        const int m = m0 + 16 * e;
+                        if (m >= tokens) break;
+                        const uint16_t *const at = src + 16ll * e * a.x_stride + i * 64;
+                        if (have >= 8) {
+                            copy16_async(buf + swizzled(m, q), at);
+                        } else {
+                            const uint4 w = load8_any(at, have);
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + swizzled(m, q)), "r"(w.x), "r"(w.y),
+                                         "r"(w.z), "r"(w.w)
+                                         : "memory");
+                        }
                     }
                 }
+                copy_commit();
+                if (i >= kLag) {
+                    copy_wait<kLag>();
+                    announce(i - kLag);
+                }
             }
-            copy_commit();
-            if (i >= kLag) {
-                copy_wait<kLag>();
-                announce(i - kLag);
+            copy_wait<0>();
+        } else {
+            // rows that are not 16-byte aligned: the aligned pieces that hold a
+            // chunk of one (nine at most, of 16 bytes) are copied as they are,
+            // then shifted into place
+            auto fetch = [&](int i) {
+                if (i < count) {
+                    const uint32_t buf = smem_addr(sm.raw[i % kWtRaw]);
+                    const int bytes = 2 * min(64, a.cols - (first + i) * 64);
+                    for (int p = xt; p < tokens * 9; p += 128) {
+                        const int m = p / 9, k = p - m * 9;
+                        const uintptr_t row = reinterpret_cast<uintptr_t>(a.x + (token0 + m) * a.x_stride + (first + i) * 64ll);
+                        const int off = static_cast<int>(row & 15);
+                        if (k * 16 < off + bytes) copy16_async(buf + m * 160 + k * 16, reinterpret_cast<const void *>(row - off + k * 16));
+                    }
+                }
+                copy_commit();
+            };
+            for (int i = 0; i < kWtRaw - 1; ++i) fetch(i);
+            for (int i = 0; i < count; ++i) {
+                copy_wait<kWtRaw - 2>();
+                asm volatile("bar.sync 1, 128;" ::: "memory");  // the four warps' pieces; the buffer filled next is left
+                fetch(i + kWtRaw - 1);
+                // (after a wait that ran out the four warps go on together)
+                tc_wait_if(i >= kWtX, &sm.x_done[i % kWtX], (i / kWtX - 1) & 1, fail, timeouts);
+                const uint32_t buf = smem_addr(sm.x[i % kWtX]), raw_buf = smem_addr(sm.raw[i % kWtRaw]);
+                const int have = a.cols - (first + i) * 64 - q * 8;
+#pragma unroll 2
+                for (int e = 0; e < kEach; ++e) {
+                    const int m = m0 + 16 * e;
+                    if (m >= tokens) break;
+                    const uint32_t off = reinterpret_cast<uintptr_t>(src + 16ll * e * a.x_stride) & 15;
+                    const uint4 lo = lds128(raw_buf + m * 160 + q * 16), hi = lds128(raw_buf + m * 160 + q * 16 + 16);
+                    const uint4 w = take8(lo, hi, off, have);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + swizzled(m, q)), "r"(w.x), "r"(w.y), "r"(w.z),
+                                 "r"(w.w)
+                                 : "memory");
+                }
+                announce(i);
             }
+            copy_wait<0>();
         }
-        copy_wait<0>();
     }
 
     // the slice's sums as [token][row], then every CTA of the cluster adds the
@@ -315,7 +362,7 @@ static cudaError_t run_w4_tc(const W4MatvecArgs &a, cudaStream_t s) {
         if (best < 0 || cost < best) best = cost, splits = n;
     }
     const int slice = (a.l.chunks + splits - 1) / splits;
-    const bool vector = (reinterpret_cast<uintptr_t>(a.x) & 7) == 0 && (a.tokens == 1 || a.x_stride % 4 == 0);
+    const bool vector = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && (a.tokens == 1 || a.x_stride % 8 == 0);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
