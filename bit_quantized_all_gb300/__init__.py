@@ -50,7 +50,8 @@ EXPORTS = ("qr_tile_values", "qr_tile_bytes", "qr_wire_bytes", "qr_encode", "qr_
            "qr_fc_twoshot_peer_send", "qr_fc_twoshot_peer_reduce", "qr_fc_twoshot_peer_decode",
            "qr_fp4_twoshot_peer_workspace_bytes", "qr_fp4_twoshot_peer_send", "qr_fp4_twoshot_peer_reduce",
            "qr_fp4_twoshot_peer_decode", "qr_kv_plan", "qr_kv_append", "qr_kv_attention_workspace_bytes",
-           "qr_kv_attention", "qr_w4_bytes", "qr_w4_pack", "qr_w4_quantize", "qr_w4_matvec")
+           "qr_kv_attention", "qr_w4_bytes", "qr_w4_pack", "qr_w4_quantize", "qr_w4_matvec_workspace_bytes",
+           "qr_w4_matvec")
 TWOSHOT_STATIC_WORKSPACE_BYTES = 32 << 20  # QR_TWOSHOT_STATIC_WORKSPACE_BYTES
 FC_BITS = (4, 8)
 FC_PAIRS = ((4, 4), (4, 8), (8, 8))  # (reduce-scatter, all-gather) widths; (4, 8) is the mixed "INT6"
@@ -769,4 +770,4 @@ def qr_fp4_allreduce(xs, y: torch.Tensor | None = None, stream=None, ctas: int =
 # the serving operators (they use the helpers above)
 from .serving import (KVCache, KVPlan, W4Weight, qr_kv_append, qr_kv_attention,  # noqa: E402
                       qr_kv_attention_workspace, qr_kv_attention_workspace_bytes, qr_kv_plan, qr_w4_bytes,
-                      qr_w4_matvec, qr_w4_pack, qr_w4_quantize)
+                      qr_w4_matvec, qr_w4_matvec_workspace_bytes, qr_w4_pack, qr_w4_quantize)

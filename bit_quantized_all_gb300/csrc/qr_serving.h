@@ -31,6 +31,15 @@ inline W4Layout w4_layout(int rows, int cols, int group, bool has_zeros) {
     return l;
 }
 
+// Up to so many tokens the product runs on mma.sync, above on tcgen05 (16 and
+// 17 tokens through 8192 x 8192: 17 and 22 us).
+constexpr int kW4FewTokens = 16;
+
+// Rows of x that 16-byte copies can read.
+inline bool w4_x_aligned(const void *x, long long tokens, long long stride) {
+    return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (tokens == 1 || stride % 8 == 0);
+}
+
 struct KvPlanArgs {
     const int32_t *cached, *fresh;
     const int32_t *free_blocks;
@@ -65,6 +74,6 @@ cudaError_t launch_w4_quantize(int dtype, int rows, int cols, int group, const v
                                void *packed, cudaStream_t s);
 cudaError_t launch_w4_matvec(int dtype, long long tokens, const void *x, long long x_stride, int rows, int cols,
                              int group, bool has_zeros, const void *packed, void *y, long long y_stride,
-                             cudaStream_t s);
+                             void *workspace, cudaStream_t s);
 
 }  // namespace qrk

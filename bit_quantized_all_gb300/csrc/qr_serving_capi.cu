@@ -229,17 +229,28 @@ QR_EXPORT qr_status_t qr_w4_quantize(qr_dtype_t dtype, int rows, int cols, int g
                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
+QR_EXPORT size_t qr_w4_matvec_workspace_bytes(int64_t tokens, int cols) {
+    if (tokens < 1 || tokens > INT_MAX || cols < 1 || cols > INT_MAX - 128) return 0;
+    return size_t(tokens) * (size_t(cols) / 64 + (cols % 64 != 0)) * 128;
+}
+
 QR_EXPORT qr_status_t qr_w4_matvec(qr_dtype_t dtype, int64_t tokens, const void *x, int64_t x_row_stride, int rows,
                                    int cols, int group, int has_zeros, const void *packed, void *y,
-                                   int64_t y_row_stride, qr_stream_t stream) {
+                                   int64_t y_row_stride, void *workspace, size_t workspace_bytes, qr_stream_t stream) {
     if (!x || !packed || !y || tokens < 1 || rows < 1 || cols < 1) return QR_ERR_INVALID_ARG;
     if (!dtype_ok(dtype) || !group_ok(group)) return QR_ERR_UNSUPPORTED;
     const size_t need = qr_w4_bytes(rows, cols, group, has_zeros);
     if (need == 0 || tokens > INT_MAX) return QR_ERR_SIZE;
     const size_t nx = extent(tokens, 1, cols, x_row_stride, 0), ny = extent(tokens, 1, rows, y_row_stride, 0);
     if (nx == 0 || ny == 0) return QR_ERR_SIZE;
-    if (!aligned(packed, 16) || !aligned(x, 2) || !aligned(y, 2)) return QR_ERR_MISALIGNED;
+    const bool copies = tokens > qrk::kW4FewTokens && !qrk::w4_x_aligned(x, tokens, x_row_stride);
+    const size_t nw = copies ? qr_w4_matvec_workspace_bytes(tokens, cols) : 0;
+    if (copies && (!workspace || workspace_bytes < nw)) return QR_ERR_SIZE;
+    if (!aligned(packed, 16) || !aligned(x, 2) || !aligned(y, 2) || (copies && !aligned(workspace, 16)))
+        return QR_ERR_MISALIGNED;
     if (overlaps(y, ny, x, nx) || overlaps(y, ny, packed, need)) return QR_ERR_INVALID_ARG;
+    if (copies && (overlaps(workspace, nw, x, nx) || overlaps(workspace, nw, packed, need) || overlaps(workspace, nw, y, ny)))
+        return QR_ERR_INVALID_ARG;
     return from_cuda(qrk::launch_w4_matvec(dtype, tokens, x, x_row_stride, rows, cols, group, has_zeros != 0, packed, y,
-                                           y_row_stride, reinterpret_cast<cudaStream_t>(stream)));
+                                           y_row_stride, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }

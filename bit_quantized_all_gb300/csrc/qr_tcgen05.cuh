@@ -96,7 +96,15 @@ __device__ __forceinline__ bool mbar_try_suspended(uint64_t *bar, uint32_t parit
     return done != 0;
 }
 __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *fail, unsigned *timeouts) {
-    if (mbar_try_suspended(bar, parity)) return true;
+    uint32_t done;  // (asked first without suspension: cheaper when the phase is over)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (done || mbar_try_suspended(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
     while (!*static_cast<volatile int *>(fail)) {
         if (mbar_try_suspended(bar, parity)) return true;

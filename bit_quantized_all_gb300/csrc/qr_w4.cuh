@@ -66,8 +66,8 @@ __device__ __forceinline__ uint4 load8_any(const uint16_t *p, int have) {
     return take8(a, b, off, have);
 }
 
-// The tcgen05 kernel (qr_w4_tc.cu), for more tokens than matrix-vector
-// instructions take well.
-cudaError_t launch_w4_tc(int dtype, const W4MatvecArgs &a, bool zeros, cudaStream_t s);
+// The tcgen05 kernel (qr_w4_tc.cu), for more than kW4FewTokens tokens; the
+// workspace holds x's rows when they are not aligned.
+cudaError_t launch_w4_tc(int dtype, const W4MatvecArgs &a, bool zeros, void *workspace, cudaStream_t s);
 
 }  // namespace qrk

@@ -222,7 +222,7 @@ static cudaError_t run_matvec(const W4MatvecArgs &a, cudaStream_t s) {
     int splits = 1;
     while (splits < 8 && row_ctas * token_ctas * splits < 2 * sms && a.l.chunks >= 4 * splits) splits *= 2;
     const int slice = ((a.l.chunks + splits - 1) / splits);
-    const bool vector = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && (a.tokens == 1 || a.x_stride % 8 == 0);
+    const bool vector = w4_x_aligned(a.x, a.tokens, a.x_stride);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -248,15 +248,15 @@ static cudaError_t pick_group(const W4MatvecArgs &a, bool zeros, cudaStream_t s)
 }
 
 template <int DT>
-static cudaError_t pick_tokens(const W4MatvecArgs &a, bool zeros, cudaStream_t s) {
+static cudaError_t pick_tokens(const W4MatvecArgs &a, bool zeros, void *workspace, cudaStream_t s) {
     if (a.tokens <= 8) return pick_group<DT, 1, 1>(a, zeros, s);
-    if (a.tokens <= 16) return pick_group<DT, 2, 2>(a, zeros, s);
-    return launch_w4_tc(DT, a, zeros, s);
+    if (a.tokens <= kW4FewTokens) return pick_group<DT, 2, 2>(a, zeros, s);
+    return launch_w4_tc(DT, a, zeros, workspace, s);
 }
 
 cudaError_t launch_w4_matvec(int dtype, long long tokens, const void *x, long long x_stride, int rows, int cols,
                              int group, bool has_zeros, const void *packed, void *y, long long y_stride,
-                             cudaStream_t s) {
+                             void *workspace, cudaStream_t s) {
     W4MatvecArgs a;
     a.x = static_cast<const uint16_t *>(x);
     a.y = static_cast<uint16_t *>(y);
@@ -268,7 +268,7 @@ cudaError_t launch_w4_matvec(int dtype, long long tokens, const void *x, long lo
     a.cols = cols;
     a.group_shift = group == 32 ? 0 : group == 64 ? 1 : 2;
     a.l = w4_layout(rows, cols, group, has_zeros);
-    return dtype ? pick_tokens<1>(a, has_zeros, s) : pick_tokens<0>(a, has_zeros, s);
+    return dtype ? pick_tokens<1>(a, has_zeros, workspace, s) : pick_tokens<0>(a, has_zeros, workspace, s);
 }
 
 }  // namespace qrk

@@ -2,18 +2,19 @@
 // group scales, on tcgen05 (qr_w4_matvec; qr_w4.cu describes the packed order).
 //
 // y^T = W x^T, a CTA taking 128 weight rows by up to 64 tokens over one slice of
-// the columns, 64 columns (a chunk) at a time.  Four warps turn codes into the
-// type's exact integers u - z and store them as the A operand in tensor memory:
-// the packed words are the fragments of that store, so nothing is exchanged.
-// Four warps bring x into shared memory.  One warp issues the products.  As scales differ from group
-// to group, each group's (or chunk's, for groups of 128) products go to a ring
-// of accumulators of their own, and four warps, a thread per row, add them
-// scaled in fp32: the weights are never rounded.  The CTAs of a cluster add
-// their slices' sums, in order, through distributed shared memory.
+// the columns, a step of four chunks of 64 columns at a time.  Eight warps, a row tile each,
+// turn codes into the type's exact integers u - z and store them as the A operand
+// in tensor memory: the packed words are the fragments of that store, so nothing
+// is exchanged.  Four warps bring x into shared memory.  One warp issues the
+// products.  As scales differ from group to group, each group's (or chunk's, for
+// groups of 64 and 128) products go to a ring of accumulators of their own, and
+// eight warps, a thread per row and half of the tokens, add them scaled in fp32:
+// the weights are never rounded.  The CTAs of a cluster add their slices' sums,
+// in order, through distributed shared memory.
 //
-// What bounds it: HBM for the codes (4 KB a chunk: 178 cycles of an SM's
-// share), closely followed by issue (conversion and scaling, about 190 slots a
-// scheduler and chunk).
+// What bounds it: the warps' latencies, of which two a scheduler hide each
+// other's in the conversion and in the sums, above the codes from HBM (4 KB a
+// chunk, 178 cycles of an SM's share).
 #include <cooperative_groups.h>
 
 #include "qr_launch.h"
@@ -24,20 +25,22 @@ namespace qrk {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWtThreads = 416;  // warps 0-3 codes, 4-7 sums, 8 products, 9-12 x
+constexpr int kWtThreads = 672;  // warps 0-7 codes, 8-15 sums, 16 products, 17-20 x
 constexpr int kWtRows = 128;
-constexpr int kWtA = 4, kWtD = 4, kWtX = 8;  // buffers of codes, accumulators, x chunks
-constexpr int kWtAhead = 16;                 // chunks of codes on their way
-constexpr int kWtRaw = 6;                    // chunks of unaligned x on their way
-constexpr uint32_t kWtColD = kWtA * 32, kWtColumns = 512;
+// A barrier's arrival and wait cost about as much as a chunk's work, so buffers
+// are handed on by the step, and accumulators two at a time.
+constexpr int kWtStep = 4;             // chunks
+constexpr int kWtA = 2, kWtD = 2;      // buffers of codes (a step each) and of accumulators (two each)
+constexpr int kWtAhead = 4;            // steps of codes on their way
+constexpr uint32_t kWtColD = kWtA * 32 * kWtStep, kWtColumns = 512;
+constexpr int kWtX = 4, kWtXAhead = 2;  // buffers of x, a step each; of them on their way
 
 template <int N>
 struct WtSmem {
-    uint8_t x[kWtX][N * 128];                       // then the sums
-    uint8_t codes[4][kWtAhead][1024];               // by warp: its two row tiles
-    uint8_t zeros[4][kWtAhead][64];
-    uint8_t scales[4][kWtAhead][128];
-    uint8_t raw[kWtRaw][N][160];                    // chunks of unaligned x as they lie in memory
+    uint8_t x[kWtX * kWtStep * N * 128];        // then the sums
+    uint8_t codes[8][kWtAhead][kWtStep][512];   // by warp: its row tile
+    uint8_t zeros[8][kWtAhead][kWtStep][32];
+    uint8_t scales[8][kWtAhead][kWtStep][128];  // by warp: its quarter's two row tiles
     uint64_t a_full[kWtA], a_done[kWtA], x_full[kWtX], x_done[kWtX], d_full[kWtD], d_done[kWtD];
     uint32_t tmem;
     int fail;
@@ -45,7 +48,7 @@ struct WtSmem {
 
 // N: tokens of a CTA; NG: groups of a 64-column chunk (2 for groups of 32, else 1).
 template <int DT, int N, int NG, bool ZEROS>
-__global__ void __launch_bounds__(kWtThreads, 1) w4_tc_kernel(W4MatvecArgs a, int slice, bool vector, unsigned *timeouts) {
+__global__ void __launch_bounds__(kWtThreads, 1) w4_tc_kernel(W4MatvecArgs a, int slice, unsigned *timeouts) {
     chain_entry();
     using S = WtSmem<N>;
     extern __shared__ uint8_t raw[];
@@ -59,9 +62,10 @@ __global__ void __launch_bounds__(kWtThreads, 1) w4_tc_kernel(W4MatvecArgs a, in
     const int tile0 = blockIdx.x / splits * (kWtRows / 16);
     int *const fail = &sm.fail;
 
+    constexpr int kXStep = kWtStep * N * 128;
     if (tid == 0) {
         for (int i = 0; i < kWtA; ++i) {
-            mbar_init(&sm.a_full[i], 128);
+            mbar_init(&sm.a_full[i], 256);
             mbar_init(&sm.a_done[i], 1);
         }
         for (int i = 0; i < kWtX; ++i) {
@@ -70,150 +74,172 @@ __global__ void __launch_bounds__(kWtThreads, 1) w4_tc_kernel(W4MatvecArgs a, in
         }
         for (int i = 0; i < kWtD; ++i) {
             mbar_init(&sm.d_full[i], 1);
-            mbar_init(&sm.d_done[i], 128);
+            mbar_init(&sm.d_done[i], 256);
         }
         mbar_init_fence();
         sm.fail = 0;
     }
-    if (warp == 8) tc_alloc(&sm.tmem, kWtColumns);
+    if (warp == 16) tc_alloc(&sm.tmem, kWtColumns);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    float acc[N];  // of the sums' threads: this row's
+    const int steps = (count + kWtStep - 1) / kWtStep;
+    const int quarter = warp & 3;  // of tensor memory's lanes, that this warp reaches
+    constexpr int kMine = N / 2;
+    float acc[kMine];  // of the sums' threads: this row's, half of the tokens
+    auto group_of = [&](int i, int n) { return NG == 2 ? (first + i) * 2 + n : (first + i) >> (a.group_shift - 1); };
 
-    if (warp < 4) {
-        // ---- codes: a warp's two row tiles of 16 x 64
-        const uint32_t codes = smem_addr(sm.codes[warp]), zeros = smem_addr(sm.zeros[warp]);
-        const uint8_t *src[2], *zsrc[2];
+    if (warp < 8) {
+        // ---- codes: a row tile of 16
+        const uint32_t codes = smem_addr(sm.codes[warp]);
+        const long long tile = min(tile0 + 2 * quarter + (warp >> 2), a.l.row_tiles - 1);
+        const uint8_t *const src = a.packed + (tile * a.l.chunks + first) * 512 + lane * 16;
+        const uint8_t *const zsrc = a.packed + a.l.zeros_at + tile * a.l.groups * 16;
+        auto fetch = [&](int p) {
+            const uint32_t slot = p % kWtAhead;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const long long tile = min(tile0 + 2 * warp + r, a.l.row_tiles - 1);
-            src[r] = a.packed + (tile * a.l.chunks + first) * 512 + lane * 16;
-            zsrc[r] = a.packed + a.l.zeros_at + tile * a.l.groups * 16;
-        }
-        auto group_of = [&](int i, int n) { return NG == 2 ? (first + i) * 2 + n : (first + i) >> (a.group_shift - 1); };
-        auto fetch = [&](int i) {
-            if (i < count) {
-                const uint32_t slot = i % kWtAhead;
-#pragma unroll
-                for (int r = 0; r < 2; ++r) copy16_async(codes + slot * 1024 + r * 512 + lane * 16, src[r] + i * 512ll);
-                if (ZEROS && lane < 2 * NG)
-                    copy16_async(zeros + slot * 64 + lane * 16, zsrc[lane / NG] + group_of(i, lane % NG) * 16);
-            }
+            for (int u = 0; u < kWtStep; ++u)
+                if (kWtStep * p + u < count)
+                    copy16_async(codes + (slot * kWtStep + u) * 512 + lane * 16, src + (kWtStep * p + u) * 512ll);
+            if (ZEROS && lane < kWtStep * NG && kWtStep * p + lane / NG < count)
+                copy16_async(smem_addr(sm.zeros[warp][slot][lane / NG]) + lane % NG * 16,
+                             zsrc + group_of(kWtStep * p + lane / NG, lane % NG) * 16);
             copy_commit();
         };
-        for (int i = 0; i < kWtAhead - 1; ++i) fetch(i);
-        for (int i = 0; i < count; ++i) {
+        for (int p = 0; p < kWtAhead - 1; ++p) fetch(p);
+        const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32 + (warp >> 2) * 16) << 16);
+        for (int p = 0; p < steps; ++p) {
             copy_wait<kWtAhead - 2>();
             __syncwarp();
-            const uint32_t slot = i % kWtAhead;
-            uint32_t v[2][16];
+            const uint32_t slot = p % kWtAhead;
+            uint4 w4[kWtStep];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint4 w4 = lds128(codes + slot * 1024 + r * 512 + lane * 16);
-                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            for (int u = 0; u < kWtStep; ++u) w4[u] = lds128(codes + (slot * kWtStep + u) * 512 + lane * 16);
+            const int s = p % kWtA;
+            if (p >= kWtA && !tc_wait_warp(&sm.a_done[s], (p / kWtA - 1) & 1, fail, timeouts)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int u = 0; u < kWtStep; ++u) {
+                const uint32_t w[4] = {w4[u].x, w4[u].y, w4[u].z, w4[u].w};
+                uint32_t v[16];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t z0 = DT == 0 ? 0x64086408u : 0x43084308u, z1 = z0;
                     if constexpr (ZEROS) {
-                        const uint32_t zz = *reinterpret_cast<const uint16_t *>(
-                            &sm.zeros[warp][slot][(r * NG + (NG == 2 ? j >> 1 : 0)) * 16 + g * 2]);
+                        const uint32_t zz =
+                            *reinterpret_cast<const uint16_t *>(&sm.zeros[warp][slot][u][(NG == 2 ? j >> 1 : 0) * 16 + g * 2]);
                         z0 = ((zz & 15u) * 0x00010001u) | (DT == 0 ? 0x64006400u : 0x43004300u);
                         z1 = ((zz >> 8) * 0x00010001u) | (DT == 0 ? 0x64006400u : 0x43004300u);
                     }
-                    v[r][4 * j] = code_pair<DT>(w[j], z0);
-                    v[r][4 * j + 1] = code_pair<DT>(w[j] >> 8, z0);
-                    v[r][4 * j + 2] = code_pair<DT>(w[j] >> 4, z1);
-                    v[r][4 * j + 3] = code_pair<DT>(w[j] >> 12, z1);
+                    v[4 * j] = code_pair<DT>(w[j], z0);
+                    v[4 * j + 1] = code_pair<DT>(w[j] >> 8, z0);
+                    v[4 * j + 2] = code_pair<DT>(w[j] >> 4, z1);
+                    v[4 * j + 3] = code_pair<DT>(w[j] >> 12, z1);
                 }
+                tc_st_fragments(to + s * (32 * kWtStep) + u * 32, v);  // (past the last chunk: unused)
             }
-            __syncwarp();
-            fetch(i + kWtAhead - 1);
-            const int s = i % kWtA;
-            if (i >= kWtA && !tc_wait_warp(&sm.a_done[s], (i / kWtA - 1) & 1, fail, timeouts)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int r = 0; r < 2; ++r) tc_st_fragments(tmem + (static_cast<uint32_t>(warp * 32 + r * 16) << 16) + s * 32, v[r]);
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(&sm.a_full[s]);
+            __syncwarp();
+            fetch(p + kWtAhead - 1);
         }
         copy_wait<0>();
-    } else if (warp < 8) {
-        // ---- sums: a thread per row
-        const int q = warp - 4;
+    } else if (warp < 16) {
+        // ---- sums: a thread per row, half of the tokens
+        const int mine = warp - 8, from = (mine >> 2) * kMine;
 #pragma unroll
-        for (int n = 0; n < N; ++n) acc[n] = 0.0f;
-        const uint32_t scales = smem_addr(sm.scales[q]), lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + kWtColD;
+        for (int n = 0; n < kMine; ++n) acc[n] = 0.0f;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kWtColD + from;
         // a row tile's scales of one group are 32 bytes, two pieces
         const uint8_t *const src = a.packed + a.l.scales_at;
-        auto fetch = [&](int i) {
-            if (i < count && lane < 4 * NG) {
-                const int r = lane / (2 * NG), n = lane / 2 % NG;
-                const long long tile = min(tile0 + 2 * q + r, a.l.row_tiles - 1);
-                const int gi = NG == 2 ? (first + i) * 2 + n : (first + i) >> (a.group_shift - 1);
-                copy16_async(scales + (i % kWtAhead) * 128 + lane * 16, src + (tile * a.l.groups + gi) * 32 + (lane & 1) * 16);
+        auto fetch = [&](int p) {
+#pragma unroll
+            for (int i = lane; i < kWtStep * 4 * NG; i += 32) {
+                const int u = i / (4 * NG), at = i % (4 * NG), r = at / (2 * NG), n = at / 2 % NG;
+                if (kWtStep * p + u < count) {
+                    const long long tile = min(tile0 + 2 * quarter + r, a.l.row_tiles - 1);
+                    copy16_async(smem_addr(sm.scales[mine][p % kWtAhead][u]) + at * 16,
+                                 src + (tile * a.l.groups + group_of(kWtStep * p + u, n)) * 32 + (at & 1) * 16);
+                }
             }
             copy_commit();
         };
-        for (int i = 0; i < kWtAhead - 1; ++i) fetch(i);
+        for (int p = 0; p < kWtAhead - 1; ++p) fetch(p);
         bool ok = true;
-        for (int i = 0; i < count && ok; ++i) {
+        for (int p = 0; p < steps && ok; ++p) {
             copy_wait<kWtAhead - 2>();
             __syncwarp();
 #pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                const int use = i * NG + n, d = use % kWtD;
-                const float scale = __half2float(*reinterpret_cast<const __half *>(
-                    &sm.scales[q][i % kWtAhead][((lane >> 4) * NG + n) * 32 + (lane & 7) * 4 + (lane >> 3 & 1) * 2]));
-                if (!tc_wait_warp(&sm.d_full[d], (use / kWtD) & 1, fail, timeouts)) {
-                    ok = false;
-                    break;
-                }
+            for (int un = 0; un < kWtStep * NG; un += 2) {
+                // the unit of accumulators un and un + 1 of the step
+                const int use = p * (kWtStep * NG / 2) + un / 2, d = use % kWtD;
+                if (kWtStep * p + un / NG >= count || !ok) break;
+                float scale[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    scale[k] = __half2float(*reinterpret_cast<const __half *>(
+                        &sm.scales[mine][p % kWtAhead][(un + k) / NG][((lane >> 4) * NG + (un + k) % NG) * 32 + (lane & 7) * 4 +
+                                                                       (lane >> 3 & 1) * 2]));
+                const bool both = kWtStep * p + (un + 1) / NG < count;
+                ok = tc_wait_warp(&sm.d_full[d], (use / kWtD) & 1, fail, timeouts);
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < N / 32; ++h) {
-                    uint32_t v[32];
-                    tc_ld32(lanes + d * N + h * 32, v);
-                    tc_wait_ld(v);
-                    if (h == N / 32 - 1) {
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t v[kMine / 16][16];
+#pragma unroll
+                    for (int h = 0; h < kMine / 16; ++h) tc_ld16(lanes + (2 * d + k) * N + h * 16, v[h]);
+#pragma unroll
+                    for (int h = 0; h < kMine / 16; ++h) tc_wait_ld(v[h]);
+                    if (k == 1) {
                         tc_fence_before();
                         mbar_arrive(&sm.d_done[d]);
+                        if (!both) break;  // (an accumulator that no product wrote)
                     }
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const float2 y = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
-                                              make_float2(scale, scale), make_float2(acc[h * 32 + k], acc[h * 32 + k + 1]));
-                        acc[h * 32 + k] = y.x;
-                        acc[h * 32 + k + 1] = y.y;
-                    }
+                    for (int h = 0; h < kMine / 16; ++h)
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 y = fma2(make_float2(__uint_as_float(v[h][e]), __uint_as_float(v[h][e + 1])),
+                                                  make_float2(scale[k], scale[k]),
+                                                  make_float2(acc[h * 16 + e], acc[h * 16 + e + 1]));
+                            acc[h * 16 + e] = y.x;
+                            acc[h * 16 + e + 1] = y.y;
+                        }
                 }
             }
             __syncwarp();
-            fetch(i + kWtAhead - 1);
+            fetch(p + kWtAhead - 1);
         }
         copy_wait<0>();
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // ---- products
         const bool leader = elect_lane();
         constexpr uint32_t kDesc = mma_desc(N, false, DT == 1);
         bool ok = true;
-        for (int i = 0; i < count && ok; ++i) {
-            const int s = i % kWtA, xs = i % kWtX;
-            ok = tc_wait_warp(&sm.a_full[s], (i / kWtA) & 1, fail, timeouts) &&
-                 tc_wait_warp(&sm.x_full[xs], (i / kWtX) & 1, fail, timeouts);
-            const uint32_t x = smem_addr(sm.x[xs]);
+        for (int p = 0; p < steps && ok; ++p) {
+            const int s = p % kWtA, xs = p % kWtX, chunks = min(kWtStep, count - kWtStep * p);
+            ok = tc_wait_warp(&sm.a_full[s], (p / kWtA) & 1, fail, timeouts) &&
+                 tc_wait_warp(&sm.x_full[xs], (p / kWtX) & 1, fail, timeouts);
+            const uint32_t x = smem_addr(sm.x) + xs * kXStep, codes = tmem + s * (32 * kWtStep);
 #pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                const int use = i * NG + n, d = use % kWtD;
+            for (int un = 0; un < kWtStep * NG; un += 2) {
+                const int use = p * (kWtStep * NG / 2) + un / 2, d = use % kWtD;
+                if (un / NG >= chunks) break;
                 if (ok && use >= kWtD) ok = tc_wait_warp(&sm.d_done[d], (use / kWtD - 1) & 1, fail, timeouts);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int j = n * (4 / NG); j < (n + 1) * (4 / NG); ++j)
-                    tc_mma_ts(leader, tmem + kWtColD + d * N, tmem + s * 32 + j * 8, smem_desc(x + j * 32, 16, 1024), kDesc,
-                              j > n * (4 / NG));
+                for (int k = 0; k < 2; ++k) {
+                    const int u = (un + k) / NG, n = (un + k) % NG;
+                    if (u >= chunks) break;
+#pragma unroll
+                    for (int j = n * (4 / NG); j < (n + 1) * (4 / NG); ++j)
+                        tc_mma_ts(leader, tmem + kWtColD + (2 * d + k) * N, codes + u * 32 + j * 8,
+                                  smem_desc(x + u * (N * 128) + j * 32, 16, 1024), kDesc, j > n * (4 / NG));
+                }
                 tc_commit(leader, &sm.d_full[d]);
             }
             if (ok) {
@@ -223,32 +249,24 @@ __global__ void __launch_bounds__(kWtThreads, 1) w4_tc_kernel(W4MatvecArgs a, in
         }
     } else {
         // ---- x: [token][64 columns]
-        const int xt = tid - 288;
-        for (int i = xt; i < kWtX * (N - tokens) * 8; i += 128) {  // rows past the tokens stay zero
+        const int xt = tid - 544;
+        const uint32_t x0 = smem_addr(sm.x);
+        for (int i = xt; i < kWtX * kWtStep * (N - tokens) * 8; i += 128) {  // rows past the tokens stay zero
             const int buf = i / ((N - tokens) * 8), row = tokens + i / 8 % (N - tokens);
-            reinterpret_cast<uint4 *>(sm.x[buf])[row * 8 + i % 8] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(sm.x + buf * (N * 128))[row * 8 + i % 8] = make_uint4(0, 0, 0, 0);
         }
         // this thread's pieces of a chunk: 16 bytes of rows m0, m0 + 16, ...
         constexpr int kEach = N / 16;
         const int m0 = xt >> 3, q = xt & 7;
         const uint16_t *const src = a.x + (token0 + m0) * a.x_stride + static_cast<long long>(first) * 64 + q * 8;
-        auto tc_wait_if = [&](bool wanted, uint64_t *bar, uint32_t parity, int *f, unsigned *t) {
-            if (wanted) tc_wait_warp(bar, parity, f, t);
-        };
-        auto ready = [&](int i) {
-            return i < kWtX || tc_wait_warp(&sm.x_done[i % kWtX], (i / kWtX - 1) & 1, fail, timeouts);
-        };
-        auto announce = [&](int i) {
-            smem_to_tensor_fence();
-            mbar_arrive(&sm.x_full[i % kWtX]);
-        };
-        if (vector) {
-            constexpr int kLag = kWtX - 2;  // chunks on their way
-            for (int i = 0; i < count + kLag; ++i) {
-                if (i < count) {
-                    if (!ready(i)) break;
-                    const uint32_t buf = smem_addr(sm.x[i % kWtX]);
-                    const int have = a.cols - (first + i) * 64 - q * 8;
+        for (int p = 0; p < steps + kWtXAhead; ++p) {
+            if (p < steps) {
+                if (p >= kWtX && !tc_wait_warp(&sm.x_done[p % kWtX], (p / kWtX - 1) & 1, fail, timeouts)) break;
+#pragma unroll
+                for (int u = 0; u < kWtStep; ++u) {
+                    const int i = kWtStep * p + u;
+                    const uint32_t buf = x0 + (p % kWtX) * kXStep + u * (N * 128);
+                    const int have = i < count ? a.cols - (first + i) * 64 - q * 8 : 0;
 #pragma unroll
                     for (int e = 0; e < kEach; ++e) {
                         const int m = m0 + 16 * e;
@@ -258,75 +276,37 @@ __global__ void __launch_bounds__(kWtThreads, 1) w4_tc_kernel(W4MatvecArgs a, in
                             copy16_async(buf + swizzled(m, q), at);
                         } else {
                             const uint4 w = load8_any(at, have);
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + swizzled(m, q)), "r"(w.x), "r"(w.y),
-                                         "r"(w.z), "r"(w.w)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + swizzled(m, q)), "r"(w.x),
+                                         "r"(w.y), "r"(w.z), "r"(w.w)
                                          : "memory");
                         }
                     }
                 }
-                copy_commit();
-                if (i >= kLag) {
-                    copy_wait<kLag>();
-                    announce(i - kLag);
-                }
             }
-            copy_wait<0>();
-        } else {
-            // rows that are not 16-byte aligned: the aligned pieces that hold a
-            // chunk of one (nine at most, of 16 bytes) are copied as they are,
-            // then shifted into place
-            auto fetch = [&](int i) {
-                if (i < count) {
-                    const uint32_t buf = smem_addr(sm.raw[i % kWtRaw]);
-                    const int bytes = 2 * min(64, a.cols - (first + i) * 64);
-                    for (int p = xt; p < tokens * 9; p += 128) {
-                        const int m = p / 9, k = p - m * 9;
-                        const uintptr_t row = reinterpret_cast<uintptr_t>(a.x + (token0 + m) * a.x_stride + (first + i) * 64ll);
-                        const int off = static_cast<int>(row & 15);
-                        if (k * 16 < off + bytes) copy16_async(buf + m * 160 + k * 16, reinterpret_cast<const void *>(row - off + k * 16));
-                    }
-                }
-                copy_commit();
-            };
-            for (int i = 0; i < kWtRaw - 1; ++i) fetch(i);
-            for (int i = 0; i < count; ++i) {
-                copy_wait<kWtRaw - 2>();
-                asm volatile("bar.sync 1, 128;" ::: "memory");  // the four warps' pieces; the buffer filled next is left
-                fetch(i + kWtRaw - 1);
-                // (after a wait that ran out the four warps go on together)
-                tc_wait_if(i >= kWtX, &sm.x_done[i % kWtX], (i / kWtX - 1) & 1, fail, timeouts);
-                const uint32_t buf = smem_addr(sm.x[i % kWtX]), raw_buf = smem_addr(sm.raw[i % kWtRaw]);
-                const int have = a.cols - (first + i) * 64 - q * 8;
-#pragma unroll 2
-                for (int e = 0; e < kEach; ++e) {
-                    const int m = m0 + 16 * e;
-                    if (m >= tokens) break;
-                    const uint32_t off = reinterpret_cast<uintptr_t>(src + 16ll * e * a.x_stride) & 15;
-                    const uint4 lo = lds128(raw_buf + m * 160 + q * 16), hi = lds128(raw_buf + m * 160 + q * 16 + 16);
-                    const uint4 w = take8(lo, hi, off, have);
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + swizzled(m, q)), "r"(w.x), "r"(w.y), "r"(w.z),
-                                 "r"(w.w)
-                                 : "memory");
-                }
-                announce(i);
+            copy_commit();
+            if (p >= kWtXAhead) {
+                copy_wait<kWtXAhead>();
+                smem_to_tensor_fence();
+                mbar_arrive(&sm.x_full[(p - kWtXAhead) % kWtX]);
             }
-            copy_wait<0>();
         }
+        copy_wait<0>();
     }
 
     // the slice's sums as [token][row], then every CTA of the cluster adds the
     // slices, in order, for its share of them
     constexpr int kPitch = kWtRows + 4;
-    static_assert(N * kPitch * 4 <= kWtX * N * 128, "the sums fit where x was");
-    float *const sums = reinterpret_cast<float *>(sm.x[0]);
+    static_assert(N * kPitch * 4 <= kWtX * kWtStep * N * 128, "the sums fit where x was");
+    float *const sums = reinterpret_cast<float *>(sm.x);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tc_free(tmem, kWtColumns);
-    if (warp >= 4 && warp < 8) {
+    if (warp == 16) tc_free(tmem, kWtColumns);
+    if (warp >= 8 && warp < 16) {
+        const int from = (warp - 8 >> 2) * kMine;
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-            if (n < tokens) sums[n * kPitch + tid - 128] = acc[n];
+        for (int n = 0; n < kMine; ++n)
+            if (from + n < tokens) sums[(from + n) * kPitch + quarter * 32 + lane] = acc[n];
     }
     if (splits > 1) cluster.sync(); else __syncthreads();
     const int row0 = tile0 * 16;
@@ -362,7 +342,6 @@ static cudaError_t run_w4_tc(const W4MatvecArgs &a, cudaStream_t s) {
         if (best < 0 || cost < best) best = cost, splits = n;
     }
     const int slice = (a.l.chunks + splits - 1) / splits;
-    const bool vector = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && (a.tokens == 1 || a.x_stride % 8 == 0);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -376,7 +355,7 @@ static cudaError_t run_w4_tc(const W4MatvecArgs &a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    err = cudaLaunchKernelEx(&cfg, kern, a, slice, vector, timeouts);
+    err = cudaLaunchKernelEx(&cfg, kern, a, slice, timeouts);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -386,7 +365,30 @@ static cudaError_t pick_group(const W4MatvecArgs &a, bool zeros, cudaStream_t s)
     return zeros ? run_w4_tc<DT, N, 1, true>(a, s) : run_w4_tc<DT, N, 1, false>(a, s);
 }
 
-cudaError_t launch_w4_tc(int dtype, const W4MatvecArgs &a, bool zeros, cudaStream_t s) {
+// Rows of x on 16-byte boundaries, columns padded with zeros to whole chunks.
+__global__ void __launch_bounds__(256) w4_align_kernel(W4MatvecArgs a, uint4 *to, int pieces) {
+    chain_entry();
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < a.tokens * pieces; i += gridDim.x * 256ll) {
+        const long long m = i / pieces;
+        const int col = static_cast<int>(i - m * pieces) * 8;
+        to[i] = load8_any(a.x + m * a.x_stride + col, a.cols - col);
+    }
+}
+
+cudaError_t launch_w4_tc(int dtype, const W4MatvecArgs &given, bool zeros, void *workspace, cudaStream_t s) {
+    W4MatvecArgs a = given;
+    if (!w4_x_aligned(a.x, a.tokens, a.x_stride)) {
+        // copied once rather than shifted into place by every CTA: the copy of 64
+        // rows of 5123 is 0.7 MB, which each of 161 CTAs along the rows would read
+        const int pieces = a.l.chunks * 8;
+        const long long blocks = (a.tokens * pieces + 255) / 256;
+        const cudaError_t err = launch_chained(w4_align_kernel, static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, s,
+                                               given, static_cast<uint4 *>(workspace), pieces);
+        if (err != cudaSuccess) return err;
+        a.x = static_cast<const uint16_t *>(workspace);
+        a.x_stride = a.l.chunks * 64;
+        a.cols = a.l.chunks * 64;
+    }
     if (a.tokens <= 32) return dtype ? pick_group<1, 32>(a, zeros, s) : pick_group<0, 32>(a, zeros, s);
     return dtype ? pick_group<1, 64>(a, zeros, s) : pick_group<0, 64>(a, zeros, s);
 }

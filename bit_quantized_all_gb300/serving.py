@@ -53,7 +53,8 @@ def _lib():
             "qr_w4_bytes": (sz, [i32, i32, i32, i32]),
             "qr_w4_pack": (i32, [i32, i32, i32, vp, vp, vp, vp, vp]),
             "qr_w4_quantize": (i32, [i32, i32, i32, i32, vp, i64, vp, vp]),
-            "qr_w4_matvec": (i32, [i32, i64, vp, i64, i32, i32, i32, i32, vp, vp, i64, vp]),
+            "qr_w4_matvec_workspace_bytes": (sz, [i64, i32]),
+            "qr_w4_matvec": (i32, [i32, i64, vp, i64, i32, i32, i32, i32, vp, vp, i64, vp, sz, vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)
@@ -361,8 +362,15 @@ def qr_w4_quantize(w: torch.Tensor, group: int = 32, stream=None) -> W4Weight:
     return out
 
 
-def qr_w4_matvec(x: torch.Tensor, weight: W4Weight, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """y = x @ w.T for fp16/bf16 x [tokens, cols] and 4-bit weights."""
+def qr_w4_matvec_workspace_bytes(tokens: int, cols: int) -> int:
+    return int(_lib().qr_w4_matvec_workspace_bytes(tokens, cols))
+
+
+def qr_w4_matvec(x: torch.Tensor, weight: W4Weight, y: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = x @ w.T for fp16/bf16 x [tokens, cols] and 4-bit weights.  More than
+    16 tokens whose rows are not 16-byte aligned are copied into ``workspace``
+    (uint8, qr_w4_matvec_workspace_bytes) first; without one it is allocated."""
     _matrix(x, "x", weight.cols)
     dt = _dtype_code(x, "x")
     tokens = x.shape[0]
@@ -375,9 +383,18 @@ def qr_w4_matvec(x: torch.Tensor, weight: W4Weight, y: torch.Tensor | None = Non
     dev = weight.packed.device
     _on(dev, "qr_w4_matvec", x, y)
     if tokens:
-        status = (_L or _lib()).qr_w4_matvec(dt, tokens, x.data_ptr(), x.stride(0), weight.rows, weight.cols,
-                                             weight.group, weight.has_zeros, weight.packed.data_ptr(), y.data_ptr(),
-                                             y.stride(0), _current(dev, stream))
+        at, stride, cols = x.data_ptr(), x.stride(0), weight.cols
+        if workspace is not None:
+            _cuda_contig(workspace, "workspace")
+            if workspace.dtype != torch.uint8:
+                raise TypeError(f"workspace must be torch.uint8, got {workspace.dtype}")
+            _on(dev, "qr_w4_matvec", workspace)
+        elif tokens > 16 and (at | 2 * stride) & 15:
+            workspace = torch.empty(qr_w4_matvec_workspace_bytes(tokens, cols), dtype=torch.uint8, device=dev)
+        status = (_L or _lib()).qr_w4_matvec(
+            dt, tokens, at, stride, weight.rows, cols, weight.group, weight.has_zeros, weight.packed.data_ptr(),
+            y.data_ptr(), y.stride(0), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), _current(dev, stream))
         if status:
             _check(status, "qr_w4_matvec")
     return y
@@ -385,4 +402,5 @@ def qr_w4_matvec(x: torch.Tensor, weight: W4Weight, y: torch.Tensor | None = Non
 
 __all__ = ["KVCache", "KVPlan", "W4Weight", "qr_kv_plan", "qr_kv_append", "qr_kv_attention",
            "qr_kv_attention_workspace", "qr_kv_attention_workspace_bytes", "qr_w4_bytes", "qr_w4_pack",
-           "qr_w4_quantize", "qr_w4_matvec"]
+           "qr_w4_quantize", "qr_w4_matvec",
+           "qr_w4_matvec_workspace_bytes"]

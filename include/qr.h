@@ -732,10 +732,15 @@ qr_status_t qr_w4_quantize(qr_dtype_t dtype, int rows, int cols, int group, cons
  * out, row strides in values, accumulated in fp32 (codes and zero points
  * enter the products as exact integers, scales in fp32) and rounded once.
  * Made for few tokens; any number is served.  x and y 2-byte aligned, any
- * stride of at least a row; 16-byte aligned rows of x are read faster. */
+ * stride of at least a row.  For more than 16 tokens whose rows of x are not
+ * all 16-byte aligned the call copies them into `workspace`
+ * (qr_w4_matvec_workspace_bytes, 16-byte aligned) first; otherwise the
+ * workspace may be NULL. */
+size_t qr_w4_matvec_workspace_bytes(int64_t tokens, int cols); /* 0 if unsupported */
 qr_status_t qr_w4_matvec(qr_dtype_t dtype, int64_t tokens, const void *x, int64_t x_row_stride,
                          int rows, int cols, int group, int has_zeros, const void *packed,
-                         void *y, int64_t y_row_stride, qr_stream_t stream);
+                         void *y, int64_t y_row_stride, void *workspace, size_t workspace_bytes,
+                         qr_stream_t stream);
 
 /* A static string naming a status code (never NULL). */
 const char *qr_status_string(qr_status_t status);

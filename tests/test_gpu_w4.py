@@ -80,6 +80,20 @@ def test_strides_and_alignment(tokens, pad, shift):
     assert (out[:, 0] == 9).all() and (out[:, rows + 1:] == 9).all()
 
 
+def test_workspace_for_unaligned_rows():
+    rng = np.random.default_rng(7)
+    rows, cols, tokens = 150, 333, 40
+    w = _weights(rng, rows, cols, 64, True)
+    weight, dense = _pack(*w, cols, 64), ref.w4_dense(*w, cols, 64)
+    x = _x(rng, tokens, cols, 0).cuda()
+    ws = torch.full((qr.qr_w4_matvec_workspace_bytes(tokens, cols),), 255, dtype=torch.uint8, device="cuda")
+    got = qr.qr_w4_matvec(x, weight, workspace=ws)
+    assert torch.equal(got, _check(x, weight, dense, 0))
+    with pytest.raises(qr.QRError) as e:
+        qr.qr_w4_matvec(x, weight, workspace=ws[:-16])
+    assert e.value.status == qr.QR_ERR_SIZE
+
+
 def test_every_code_scale_and_zero_is_read_in_its_place():
     """One-hot x: the product returns the weights themselves."""
     rng = np.random.default_rng(1)

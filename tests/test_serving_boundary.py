@@ -108,6 +108,7 @@ def test_w4_sizes():
     assert qr.qr_w4_bytes(1, 1, 32, True) == 512 + 64 + 32
     for bad in ((0, 64, 32), (16, 0, 32), (16, 64, 16), (16, 64, 0), (-1, 64, 32), (2 ** 31 - 1, 64, 32)):
         assert qr.qr_w4_bytes(*bad) == 0
+    assert qr.qr_w4_matvec_workspace_bytes(17, 65) == 17 * 2 * 128 and qr.qr_w4_matvec_workspace_bytes(0, 65) == 0
     assert qr.qr_kv_attention_workspace_bytes(4, 4, 8, 2, 128) > 0
     for bad in ((0, 4, 8, 2, 128), (4, 0, 8, 2, 128), (4, 4, 8, 3, 128), (4, 4, 1, 2, 128), (4, 4, 8, 2, 100)):
         assert qr.qr_kv_attention_workspace_bytes(*bad) == 0
@@ -118,7 +119,8 @@ def test_w4_refusals():
     L = serving._lib()
     pack = dict(rows=8, cols=64, group=32, codes=A, scales=B, zeros=None, packed=C, stream=None)
     quant = dict(dtype=1, rows=8, cols=64, group=32, w=A, stride=64, packed=C, stream=None)
-    mul = dict(dtype=1, tokens=2, x=A, xs=64, rows=8, cols=64, group=32, zeros=0, packed=B, y=C, ys=8, stream=None)
+    mul = dict(dtype=1, tokens=2, x=A, xs=64, rows=8, cols=64, group=32, zeros=0, packed=B, y=C, ys=8, ws=None,
+               ws_bytes=0, stream=None)
 
     def call(fn, base, **kw):
         return getattr(L, fn)(*{**base, **kw}.values())
@@ -136,7 +138,12 @@ def test_w4_refusals():
             ("qr_w4_matvec", mul, dict(xs=63), 4), ("qr_w4_matvec", mul, dict(ys=7), 4),
             ("qr_w4_matvec", mul, dict(tokens=1 << 31), 4), ("qr_w4_matvec", mul, dict(y=C + 1), 3),
             ("qr_w4_matvec", mul, dict(packed=B + 4), 3), ("qr_w4_matvec", mul, dict(y=A), 1),
-            ("qr_w4_matvec", mul, dict(y=B), 1)):
+            ("qr_w4_matvec", mul, dict(y=B), 1),
+            # 17 unaligned rows need a workspace of their size
+            ("qr_w4_matvec", mul, dict(tokens=17, x=A + 2, ws=D, ws_bytes=17 * 128 - 1), 4),
+            ("qr_w4_matvec", mul, dict(tokens=17, xs=65), 4),
+            ("qr_w4_matvec", mul, dict(tokens=17, xs=65, ws=D + 8, ws_bytes=1 << 20), 3),
+            ("qr_w4_matvec", mul, dict(tokens=17, xs=65, ws=B, ws_bytes=1 << 20), 1)):
         assert call(fn, base, **kw) == want, (fn, kw)
 
 
