@@ -29,10 +29,12 @@ cudaError_t launch_kv_attention(int dtype, const KvAttentionArgs &a, const qr_kv
     if (c.dim <= 64)
         return rows <= 8    ? run_split<64, 1>(dtype, a, c, group, s)
                : rows <= 16 ? run_split<64, 2>(dtype, a, c, group, s)
+               : rows <= 24 ? run_split<64, 3>(dtype, a, c, group, s)
                             : run_split<64, 4>(dtype, a, c, group, s);
     if (c.dim <= 128)
         return rows <= 8    ? run_split<128, 1>(dtype, a, c, group, s)
                : rows <= 16 ? run_split<128, 2>(dtype, a, c, group, s)
+               : rows <= 24 ? run_split<128, 3>(dtype, a, c, group, s)
                             : run_split<128, 4>(dtype, a, c, group, s);
     return rows <= 8 ? run_split<256, 1>(dtype, a, c, group, s) : run_split<256, 2>(dtype, a, c, group, s);
 }
