@@ -46,7 +46,7 @@ struct MatvecSmem {
 
 // NG: groups of a 64-column chunk (2 for groups of 32, else 1).
 template <int DT, int RT, int NT, int NG, bool ZEROS>
-__global__ void __launch_bounds__(kMvThreads, RT *NT <= 8 ? 2 : 1) w4_matvec_kernel(W4MatvecArgs a, int slice, bool vector) {
+__global__ void __launch_bounds__(kMvThreads, RT == 1 ? 3 : 2) w4_matvec_kernel(W4MatvecArgs a, int slice, bool vector) {
     chain_entry();
     using S = MatvecSmem<NT>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -218,9 +218,17 @@ static cudaError_t run_matvec(const W4MatvecArgs &a, cudaStream_t s) {
     if (sms <= 0) return err;
     const long long row_ctas = (a.l.row_tiles + RT * kMvWarps - 1) / (RT * kMvWarps);
     const long long token_ctas = (a.tokens + 8 * NT - 1) / (8 * NT);
-    // slices of the columns until the CTAs fill the SMs twice
+    // the number of slices whose waves of CTAs, each its chunks and about three
+    // more to start and end, are shortest (8192 x 8192, one token: 6 slices 14.3
+    // us, 4 18.0, 8, which no longer fit at once, 16.8; clusters of 5 and 7 leave
+    // SMs of a processing cluster idle)
     int splits = 1;
-    while (splits < 8 && row_ctas * token_ctas * splits < 2 * sms && a.l.chunks >= 4 * splits) splits *= 2;
+    long long best = -1;
+    for (int n : {1, 2, 3, 4, 6, 8}) {
+        const long long slots = (RT == 1 ? 3ll : 2ll) * sms, waves = (row_ctas * token_ctas * n + slots - 1) / slots;
+        const long long cost = waves * ((a.l.chunks + n - 1) / n + 3);
+        if (best < 0 || (n <= a.l.chunks && cost < best)) best = cost, splits = n;
+    }
     const int slice = ((a.l.chunks + splits - 1) / splits);
     const bool vector = w4_x_aligned(a.x, a.tokens, a.x_stride);
     cudaLaunchAttribute attr[2];
@@ -250,7 +258,13 @@ static cudaError_t pick_group(const W4MatvecArgs &a, bool zeros, cudaStream_t s)
 template <int DT>
 static cudaError_t pick_tokens(const W4MatvecArgs &a, bool zeros, void *workspace, cudaStream_t s) {
     if (a.tokens <= 8) return pick_group<DT, 1, 1>(a, zeros, s);
-    if (a.tokens <= kW4FewTokens) return pick_group<DT, 2, 2>(a, zeros, s);
+    if (a.tokens <= kW4FewTokens) {
+        // two row tiles a warp read x half as often, one makes twice the CTAs:
+        // 16 tokens through 8192 x 8192 17.0 and 19.7 us, 12 through 300 x 9000
+        // 10.0 and 6.9
+        if (a.l.row_tiles >= 152) return pick_group<DT, 2, 2>(a, zeros, s);
+        return pick_group<DT, 1, 2>(a, zeros, s);
+    }
     return launch_w4_tc(DT, a, zeros, workspace, s);
 }
 
