@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads, 3) kv_plan_kernel(KvPlanArgs a, 
             int request[kWide];
 #pragma unroll
             for (int u = 0; u < kWide; ++u) {
-                if (u)
+                if (u && t0 + u < to)
                     while (i + 1 < kChunk && s_token[(i + 1) % kEach][(i + 1) / kEach] <= t0 + u) ++i;
                 k = i % kEach, j = i / kEach;
                 request[u] = c0 + i;
