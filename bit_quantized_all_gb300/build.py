@@ -24,8 +24,8 @@ SOURCES = ["qr_capi.cu", "qr_grid.cu", "qr_encode.cu", "qr_decode.cu", "qr_reduc
            "qr_fc.cu", "qr_fc_allreduce_44.cu", "qr_fc_allreduce_48.cu", "qr_fc_allreduce_88.cu",
            "qr_twoshot.cu", "qr_twoshot_static.cu", "qr_twoshot_flags.cu", "qr_twoshot_peer.cu", "qr_timeouts.cu", "qr_fp4.cu",
            "qr_fc_twoshot.cu", "qr_fp4_twoshot.cu", "qr_codec_peer.cu",
-           "qr_serving_capi.cu", "qr_kv_plan.cu", "qr_kv_append.cu", "qr_kv_attention.cu", "qr_kv_tc.cu", "qr_w4.cu",
-           "qr_w4_matvec.cu", "qr_w4_tc.cu"]
+           "qr_serving_capi.cu", "qr_kv_plan.cu", "qr_kv_append.cu", "qr_kv_attention.cu", "qr_kv_split_f16.cu",
+           "qr_kv_split_bf16.cu", "qr_kv_tc.cu", "qr_w4.cu", "qr_w4_matvec.cu", "qr_w4_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-lineinfo", "-std=c++17",

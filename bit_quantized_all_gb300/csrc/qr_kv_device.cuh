@@ -79,6 +79,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// What the rounding of y to the fp16 pair h left, as fp16.
+__device__ __forceinline__ uint32_t rest_f16(float2 y, uint32_t h) {
+    const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack_f16(y.x - r.x, y.y - r.y);
+}
+
 // The transpose of an 8 x 8 matrix of 16-bit values, of which lane 4 g + t
 // holds row g, columns 2t and 2t + 1.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {

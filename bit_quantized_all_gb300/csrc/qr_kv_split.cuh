@@ -18,11 +18,15 @@
 // the head's dimensions within a product is free, so a lane's sixteen
 // consecutive code bytes of a key are the operands of four instructions, and
 // its sixteen bytes of two value rows those of eight.  The weights reach the
-// second product's operand order by an 8 x 8 transpose between registers.  Scores are scaled by
-// the block's scale in fp32.  The values' scale goes into the softmax weight
-// before its rounding to fp16, relative to a power of two kept per row (the
-// largest among the blocks that the row sees), so that the accumulators are
-// the matrix instruction's own.
+// second product's operand order by an 8 x 8 transpose between registers.
+// Scores are scaled by the block's scale in fp32.  The values' scale goes into
+// the softmax weight before its rounding to fp16, relative to a power of two
+// kept per row (the largest among the blocks that the row sees), so that the
+// accumulators are the matrix instruction's own.  For bf16 output the weight is
+// that one fp16 number, whose error (2^-12 of it) is far below the output's;
+// for fp16 output what its rounding left goes through a second product (128
+// requests of up to 8192 keys: 186 -> 190 us; without it the error against 64
+// bits was 1.6 times that of a product in 32 bits, with it the same).
 #pragma once
 
 #include <type_traits>
@@ -64,10 +68,6 @@ __device__ __forceinline__ AttnRequest attn_request(const KvAttentionArgs &a, co
 // written all the same.
 __device__ __forceinline__ int attn_steps(int len) { return len > 0 ? (len - 1) / kStep + 1 : 1; }
 
-__device__ __forceinline__ float widen1(bool bf16, uint16_t u) {
-    return bf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u));
-}
-
 template <int DP>
 __device__ __forceinline__ uint32_t k_offset(int row, int chunk) {
     // the lanes of one 8-lane phase read pieces of two rows: odd rows swap halves
@@ -96,13 +96,14 @@ struct AttnSmem {
 };
 
 // One row's 4 values from dimension d on, and with d = 0 its lse.
-__device__ __forceinline__ void attn_write(const KvAttentionArgs &a, bool bf16, int dim, long long token, int head,
-                                           int d, float4 v, float top, float sum) {
+template <bool BF16>
+__device__ __forceinline__ void attn_write(const KvAttentionArgs &a, int dim, long long token, int head, int d, float4 v,
+                                           float top, float sum) {
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (d < dim) {
         uint16_t *out = static_cast<uint16_t *>(a.out) + token * a.out_token + head * a.out_head + d;
         uint2 w;
-        if (bf16) {
+        if (BF16) {
             const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);
             const __nv_bfloat162 b1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
             w.x = *reinterpret_cast<const uint32_t *>(&b0);
@@ -117,10 +118,11 @@ __device__ __forceinline__ void attn_write(const KvAttentionArgs &a, bool bf16, 
         a.lse[token * a.q_heads + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
-// DP: the head's dimensions padded to 64, 128 or 256; FULL: they are exactly DP.
-template <int DP, int NT, bool FULL>
+// DP: the head's dimensions padded to 64, 128 or 256; FULL: they are exactly DP;
+// BF16: the type of queries and output, otherwise fp16.
+template <int DP, int NT, bool FULL, bool BF16>
 __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
-    kv_attention_split_kernel(KvAttentionArgs a, KvView c, bool bf16, int group) {
+    kv_attention_split_kernel(KvAttentionArgs a, KvView c, int group) {
     chain_entry();
     using S = AttnSmem<DP, NT>;
     constexpr int kRows = S::kRows, kSteps = DP / 16;
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
 #pragma unroll
             for (int i = 0; i < DP / 32; ++i) {
                 const int d = lane + 32 * i;
-                f[i] = rr < rows_here && d < dim ? widen1(bf16, q[d]) : 0.0f;
+                f[i] = rr < rows_here && d < dim ? widen1<BF16>(q[d]) : 0.0f;
                 amax = fmaxf(amax, fabsf(f[i]));
             }
 #pragma unroll
@@ -392,7 +394,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
             // does not see whole is masked first
             const bool mask = !valid[0] || !valid[1] || key0 + kTile > seen_end || key0 < seen_begin;
             const int vexp[2] = {scale_exp(vs_cur[0]), scale_exp(vs_cur[1])};
-            uint32_t p[NT][2][2];  // B fragments of the two 16-key groups
+            uint32_t p[NT][2][2];     // B fragments of the two 16-key groups
+            uint32_t lo_p[NT][2][2];  // what their rounding left (fp16 output)
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
                 // (a score is rounded before the maximum is taken from it: of
@@ -472,8 +475,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
                         l[q][k & 1] += y[k];
                         y[k] *= w[k & 1][kt];
                     }
-                    p[q][kt][0] = transpose8(pack_f16(y[0], y[1]));
-                    p[q][kt][1] = transpose8(pack_f16(y[2], y[3]));
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t hi = pack_f16(y[2 * u], y[2 * u + 1]);
+                        p[q][kt][u] = transpose8(hi);
+                        if constexpr (!BF16)
+                            lo_p[q][kt][u] = transpose8(rest_f16(make_float2(y[2 * u], y[2 * u + 1]), hi));
+                    }
                 }
             }
 
@@ -509,6 +517,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
 #pragma unroll
                             for (int q = 0; q < NT; ++q)
                                 mma_f16_acc(o[q][pc * 8 + wd * 2 + u], va, p[q][kt][0], p[q][kt][1]);
+                            if constexpr (!BF16)
+#pragma unroll
+                                for (int q = 0; q < NT; ++q)
+                                    mma_f16_acc(o[q][pc * 8 + wd * 2 + u], va, lo_p[q][kt][0], lo_p[q][kt][1]);
                         }
                     }
                 }
@@ -571,7 +583,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
             }
             if (parts == 1) {
                 const int row = row0 + rr;
-                attn_write(a, bf16, dim, x.q0 + row / group, h * group + row % group, d, v, top, sum);
+                attn_write<BF16>(a, dim, x.q0 + row / group, h * group + row % group, d, v, top, sum);
             } else {
                 __stcg(reinterpret_cast<float4 *>(my_slot + rr * DP + d), v);
                 if (d == 0) __stcg(reinterpret_cast<float2 *>(my_slot + kRows * DP + 2 * rr), make_float2(top, sum));
@@ -632,7 +644,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
                     }
                     const float2 ts = total[rr];
                     if (last) {
-                        attn_write(a, bf16, dim, x.q0 + row / group, h * group + row % group, d, v, ts.x, ts.y);
+                        attn_write<BF16>(a, dim, x.q0 + row / group, h * group + row % group, d, v, ts.x, ts.y);
                     } else {
                         __stcg(reinterpret_cast<float4 *>(to + rr * DP + d), v);
                         if (d == 0) __stcg(reinterpret_cast<float2 *>(to + kRows * DP + 2 * rr), ts);
@@ -648,10 +660,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
     }
 }
 
-template <int DP, int NT, bool FULL>
-cudaError_t run_kv_split(int dtype, const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {
+template <int DP, int NT, bool FULL, bool BF16>
+cudaError_t run_kv_split(const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {
     using S = AttnSmem<DP, NT>;
-    auto kern = kv_attention_split_kernel<DP, NT, FULL>;
+    auto kern = kv_attention_split_kernel<DP, NT, FULL, BF16>;
     cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(kern), S::kBytes);
     if (err != cudaSuccess) return err;
     const int sms = sm_count(&err);
@@ -664,7 +676,28 @@ cudaError_t run_kv_split(int dtype, const KvAttentionArgs &a, const KvView &c, i
     long long grid = static_cast<long long>(sms) * S::kCtas;
     grid = grid > kMostCtas ? kMostCtas : grid;
     return launch_chained(kern, static_cast<unsigned>(most < grid ? most : grid), kAttnThreads, S::kBytes, s, a, c,
-                          dtype != 0, group);
+                          group);
+}
+
+template <int DP, int NT, bool BF16>
+cudaError_t run_kv_split(const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {
+    return c.dim == DP ? run_kv_split<DP, NT, true, BF16>(a, c, group, s) : run_kv_split<DP, NT, false, BF16>(a, c, group, s);
+}
+
+template <bool BF16>
+cudaError_t pick_kv_split(const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {
+    const long long rows = static_cast<long long>(a.max_q) * group;
+    if (c.dim <= 64)
+        return rows <= 8    ? run_kv_split<64, 1, BF16>(a, c, group, s)
+               : rows <= 16 ? run_kv_split<64, 2, BF16>(a, c, group, s)
+               : rows <= 24 ? run_kv_split<64, 3, BF16>(a, c, group, s)
+                            : run_kv_split<64, 4, BF16>(a, c, group, s);
+    if (c.dim <= 128)
+        return rows <= 8    ? run_kv_split<128, 1, BF16>(a, c, group, s)
+               : rows <= 16 ? run_kv_split<128, 2, BF16>(a, c, group, s)
+               : rows <= 24 ? run_kv_split<128, 3, BF16>(a, c, group, s)
+                            : run_kv_split<128, 4, BF16>(a, c, group, s);
+    return rows <= 8 ? run_kv_split<256, 1, BF16>(a, c, group, s) : run_kv_split<256, 2, BF16>(a, c, group, s);
 }
 
 }  // namespace qrk

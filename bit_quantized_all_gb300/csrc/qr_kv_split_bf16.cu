@@ -1,0 +1,10 @@
+// qr_kv_split_bf16.cu -- the split attention kernel's instantiations for bf16.
+#include "qr_kv_split.cuh"
+
+namespace qrk {
+
+cudaError_t launch_kv_split_bf16(const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {
+    return pick_kv_split<true>(a, c, group, s);
+}
+
+}  // namespace qrk

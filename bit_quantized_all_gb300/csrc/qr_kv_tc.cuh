@@ -18,7 +18,9 @@
 // O stays in tensor memory.  It is rescaled only when a row's maximum has
 // grown by more than 2^kSlack, or the power of two under which the values'
 // scales are kept by more than 2^kScaleSlack; weights are then below 2^15, and
-// fp16 keeps them exact to 2^-11 down to 2^-21 of a weight of 1.
+// fp16 keeps them exact to 2^-12 down to 2^-21 of a weight of 1.  For fp16
+// output what that rounding left is a second P (8 prompt chunks of up to 1024
+// queries over up to 8192 keys: 409 us for bf16, 440 us for fp16).
 //
 // What bounds it: the tensor cores (2048 cycles a tile for both halves) and,
 // close behind, instruction issue (softmax and conversion).
@@ -142,8 +144,9 @@ struct TcSmem {
     int fail;
 };
 
-__device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
-    if (!bf16) return pack_f16(lo, hi);
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
+    if (!BF16) return pack_f16(lo, hi);
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&b);
 }
@@ -151,13 +154,16 @@ __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
 // The 128 threads of one half's softmax.
 __device__ __forceinline__ void bar_half(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 
-template <int DP, bool FULL>
+template <int DP, bool FULL, bool BF16>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    kv_attention_tc_kernel(KvAttentionArgs a, KvView c, bool bf16, int group, unsigned *timeouts) {
+    kv_attention_tc_kernel(KvAttentionArgs a, KvView c, int group, unsigned *timeouts) {
     chain_entry();
     using S = TcSmem<DP>;
     extern __shared__ uint8_t raw[];
     S &sm = *reinterpret_cast<S *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
+    // weights as one fp16 number, or for fp16 output as two: kTerms * 8 of S's
+    // columns for each 16 keys
+    constexpr int kTerms = BF16 ? 1 : 2;
     const int dim = FULL ? DP : c.dim;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -346,8 +352,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const uint32_t v = smem_addr(sm.v[was]);
 #pragma unroll
                             for (int n = 0; n < kTcKeys / 16; ++n)
-                                tc_mma_ts(leader, tmem + kColO + h * 128, tmem + kColS + h * 128 + n * 8,
-                                          smem_desc(v + n * 2048, 16384, 1024), kDescO, i > 1 || n > 0);
+#pragma unroll
+                                for (int lo = 0; lo < kTerms; ++lo)
+                                    tc_mma_ts(leader, tmem + kColO + h * 128, tmem + kColS + h * 128 + (n * kTerms + lo) * 8,
+                                              smem_desc(v + n * 2048, 16384, 1024), kDescO, i > 1 || n > 0 || lo > 0);
                             if (h == halves - 1) tc_commit(leader, &sm.v_empty[was]);
                             if (i == tiles) tc_commit(leader, &sm.o_full[h]);
                         }
@@ -438,7 +446,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int i = 0; i < DP / 8; ++i) {
                     float f[8];
                     const uint4 w = *reinterpret_cast<const uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(ht, i & 7));
-                    if (bf16) widen8<1>(w, f); else widen8<0>(w, f);
+                    widen8<BF16>(w, f);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
                 }
@@ -454,7 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     float f[8];
                     uint4 *const at = reinterpret_cast<uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(ht, i & 7));
                     const uint4 w = *at;
-                    if (bf16) widen8<1>(w, f); else widen8<0>(w, f);
+                    widen8<BF16>(w, f);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) f[k] = f[k] * down1 * down2;
                     *at = make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
@@ -592,19 +600,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 // (past the last group the first ones again, unused:
-                                // P of 16 keys takes 8 columns, all of them read before)
+                                // P of 16 keys takes no more than their 16 columns, all read before)
                                 const int g8 = g0 + u;
                                 uint32_t(&now)[16] = x[u], (&next)[16] = x[u ^ 1];
                                 tc_wait_ld(next);
                                 const float4 ahead4 = meta.group[(g8 + 2) & 7];
                                 exponents(next, next4);
-                                uint32_t p[8];
+                                uint32_t p[kTerms][8];
                                 float2 part[2];
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) {
                                     const float2 y = make_float2(__uint_as_float(now[2 * k]), __uint_as_float(now[2 * k + 1]));
                                     next[2 * k] = __float_as_uint(exp2_fast(__uint_as_float(next[2 * k])));
-                                    p[k] = pack_f16(y.x, y.y);
+                                    p[0][k] = pack_f16(y.x, y.y);
+                                    if constexpr (!BF16) p[kTerms - 1][k] = rest_f16(y, p[0][k]);
                                     next[2 * k + 1] = __float_as_uint(exp2_fast(__uint_as_float(next[2 * k + 1])));
                                     part[k & 1] = k < 2 ? y : add2(part[k & 1], y);
                                 }
@@ -613,7 +622,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 now4 = next4;
                                 next4 = ahead4;
                                 tc_ld16(scol + ((g8 + 2) & 7) * 16, now);
-                                tc_st8(scol + g8 * 8, p);
+#pragma unroll
+                                for (int lo = 0; lo < kTerms; ++lo) tc_st8(scol + (g8 * kTerms + lo) * 8, p[lo]);
                             }
                         }
                         tc_wait_ld(x[1]);
@@ -628,7 +638,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             // (a group beyond the row's power of two is not seen by it)
                             const float w = scale_exp(vs) > ve + kScaleSlack ? 0.0f : vs * up;
                             const bool ok = tile.x >> g8 & 1;
-                            uint32_t p[8];
+                            uint32_t p[kTerms][8];
                             tc_wait_ld(x[0]);
 #pragma unroll
                             for (int k = 0; k < 16; k += 2) {
@@ -640,9 +650,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     y[u] = exp2_fast(sees ? score + base : -INFINITY);
                                     l += y[u];
                                 }
-                                p[k / 2] = pack_f16(y[0] * w, y[1] * w);
+                                const float2 z = make_float2(y[0] * w, y[1] * w);
+                                p[0][k / 2] = pack_f16(z.x, z.y);
+                                if constexpr (!BF16) p[kTerms - 1][k / 2] = rest_f16(z, p[0][k / 2]);
                             }
-                            tc_st8(scol + g8 * 8, p);
+#pragma unroll
+                            for (int lo = 0; lo < kTerms; ++lo) tc_st8(scol + (g8 * kTerms + lo) * 8, p[lo]);
                             if (g8 < 7) tc_ld16(scol + (g8 + 1) * 16, x[0]);
                         }
                     }
@@ -678,9 +691,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int k = 0; k < 32; k += 8) {
                         const int i = cc * 4 + k / 8;
                         *reinterpret_cast<uint4 *>(sm.q[half] + (i >> 3) * 16384 + swizzled(ht, i & 7)) =
-                            make_uint4(pack_out(bf16, y[k] * inv, y[k + 1] * inv), pack_out(bf16, y[k + 2] * inv, y[k + 3] * inv),
-                                       pack_out(bf16, y[k + 4] * inv, y[k + 5] * inv),
-                                       pack_out(bf16, y[k + 6] * inv, y[k + 7] * inv));
+                            make_uint4(pack_out<BF16>(y[k] * inv, y[k + 1] * inv), pack_out<BF16>(y[k + 2] * inv, y[k + 3] * inv),
+                                       pack_out<BF16>(y[k + 4] * inv, y[k + 5] * inv),
+                                       pack_out<BF16>(y[k + 6] * inv, y[k + 7] * inv));
                     }
                 }
             };
@@ -788,9 +801,9 @@ out:
     if (warp == 12) tc_free(tmem, kColumns);
 }
 
-template <int DP, bool FULL>
-cudaError_t run_kv_tc(int dtype, const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {
-    auto kern = kv_attention_tc_kernel<DP, FULL>;
+template <int DP, bool FULL, bool BF16>
+cudaError_t run_kv_tc(const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {
+    auto kern = kv_attention_tc_kernel<DP, FULL, BF16>;
     const int bytes = sizeof(TcSmem<DP>) + 1024;
     cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(kern), bytes);
     if (err != cudaSuccess) return err;
@@ -799,7 +812,7 @@ cudaError_t run_kv_tc(int dtype, const KvAttentionArgs &a, const KvView &c, int 
     unsigned *timeouts = wait_timeout_counter(&err);
     if (!timeouts) return err;
     return launch_chained(kern, static_cast<unsigned>(sms < kTcMostCtas ? sms : kTcMostCtas), kTcThreads, bytes, s, a, c,
-                          dtype != 0, group, timeouts);
+                          group, timeouts);
 }
 
 }  // namespace qrk
