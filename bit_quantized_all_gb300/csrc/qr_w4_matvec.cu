@@ -38,7 +38,7 @@ __device__ __forceinline__ void mma_typed(float (&d)[4], const uint32_t (&a)[4],
 
 template <int NT>
 struct MatvecSmem {
-    static constexpr int kPanel = NT <= 2 ? 16 : 32 / NT;  // chunks of x held at a time
+    static constexpr int kPanel = 16;  // chunks of x held at a time
     static constexpr int kPitch = kPanel * 128 + 32;       // bytes of a token's row: no bank conflicts
     static constexpr int kBuffer = 8 * NT * kPitch;
     static constexpr int kBytes = 2 * kBuffer;

@@ -333,30 +333,63 @@ static cudaError_t run_w4_tc(const W4MatvecArgs &a, cudaStream_t s) {
     unsigned *timeouts = wait_timeout_counter(&err);
     if (!timeouts) return err;
     const long long row_ctas = (a.l.row_tiles + 7) / 8, token_ctas = (a.tokens + N - 1) / N;
-    // the number of slices whose waves of CTAs, each its chunks and about twelve
-    // more to start and end, are shortest
-    int splits = 1;
-    long long best = -1;
+    // The number of slices whose waves of CTAs, each its chunks and about twelve
+    // more to start and end, are shortest; or whole waves of one number, and a
+    // second launch, which costs about eight, for the rest of the rows in as many
+    // slices as make that short (64 tokens through 20481 x 5123: two slices in
+    // three waves 68.5 us, one wave whole and nine row tiles in eight slices 52.7;
+    // 32 through 10240 x 8192: 39.2 and 31.1).
+    struct Slices {
+        int splits;
+        long long cost;
+    };
+    auto slices_of = [&](long long rows) {
+        Slices x = {1, -1};
+        for (int n = 1; n <= 8; n *= 2) {
+            const long long waves = (rows * token_ctas * n + sms - 1) / sms, cost = waves * ((a.l.chunks + n - 1) / n + 12);
+            if (x.cost < 0 || cost < x.cost) x = {n, cost};
+        }
+        return x;
+    };
+    Slices first = slices_of(row_ctas), rest = {1, 0};
+    long long first_rows = row_ctas;
     for (int n = 1; n <= 8; n *= 2) {
-        const long long waves = (row_ctas * token_ctas * n + sms - 1) / sms, cost = waves * ((a.l.chunks + n - 1) / n + 12);
-        if (best < 0 || cost < best) best = cost, splits = n;
+        const long long a_wave = sms / (n * token_ctas), waves = a_wave ? row_ctas / a_wave : 0, rows = waves * a_wave;
+        if (rows == 0 || rows == row_ctas) continue;
+        const Slices x = slices_of(row_ctas - rows);
+        const long long cost = waves * ((a.l.chunks + n - 1) / n + 12);
+        if (cost + x.cost + 8 < first.cost + rest.cost) first = {n, cost}, rest = {x.splits, x.cost + 8}, first_rows = rows;
     }
-    const int slice = (a.l.chunks + splits - 1) / splits;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = splits;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(row_ctas * splits), static_cast<unsigned>(token_ctas));
-    cfg.blockDim = kWtThreads;
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    err = cudaLaunchKernelEx(&cfg, kern, a, slice, timeouts);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    auto launch = [&](const W4MatvecArgs &part, int splits, long long rows) {
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = splits;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(rows * splits), static_cast<unsigned>(token_ctas));
+        cfg.blockDim = kWtThreads;
+        cfg.dynamicSmemBytes = bytes;
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, part, (a.l.chunks + splits - 1) / splits, timeouts);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    };
+    W4MatvecArgs part = a;
+    if (first_rows < row_ctas) part.rows = static_cast<int>(first_rows * kWtRows);
+    err = launch(part, first.splits, first_rows);
+    if (err != cudaSuccess || first_rows == row_ctas) return err;
+    // the rest: everything that a row tile indexes begins first_rows later
+    const long long tiles = first_rows * (kWtRows / 16), codes = tiles * a.l.chunks * 512;
+    part.rows = static_cast<int>(a.rows - first_rows * kWtRows);
+    part.y = a.y + first_rows * kWtRows;
+    part.packed = a.packed + codes;
+    part.l.row_tiles = static_cast<int>(a.l.row_tiles - tiles);
+    part.l.scales_at = a.l.scales_at + tiles * a.l.groups * 32 - codes;
+    part.l.zeros_at = a.l.zeros_at + tiles * a.l.groups * 16 - codes;
+    return launch(part, rest.splits, row_ctas - first_rows);
 }
 
 template <int DT, int N>

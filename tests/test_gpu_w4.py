@@ -66,6 +66,18 @@ def test_odd_sizes(rows, cols, group, tokens):
     _check(_x(rng, tokens, cols, tokens % 2), _pack(*w, cols, group), ref.w4_dense(*w, cols, group), tokens % 2)
 
 
+@pytest.mark.parametrize("dtype,group,zeros", [(0, 128, True), (1, 32, False), (0, 64, True)])
+def test_rows_of_a_second_launch(dtype, group, zeros):
+    # 153 tiles of 128 rows: on 152 SMs one wave and a launch of its own for
+    # the last, of odd height
+    rng = np.random.default_rng(group)
+    rows, cols, tokens = 19511, 1000, 40
+    w = _weights(rng, rows, cols, group, zeros)
+    y = torch.full((tokens, rows + 3), 7.0, dtype=DT[dtype], device="cuda")
+    _check(_x(rng, tokens, cols, dtype), _pack(*w, cols, group), ref.w4_dense(*w, cols, group), dtype, y[:, :rows])
+    assert (y[:, rows:] == 7).all()
+
+
 @pytest.mark.parametrize("tokens", [1, 12, 40])
 @pytest.mark.parametrize("pad,shift", [(0, 0), (8, 0), (3, 0), (8, 1), (0, 4)])
 def test_strides_and_alignment(tokens, pad, shift):
