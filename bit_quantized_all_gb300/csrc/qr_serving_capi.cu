@@ -191,9 +191,13 @@ QR_EXPORT qr_status_t qr_kv_attention(qr_dtype_t dtype, int requests, int64_t to
         for (int j = 0; j < i; ++j)
             if (outs[i].n && overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return QR_ERR_INVALID_ARG;
     }
+    // no request has more queries than there are tokens: the workspace is sized
+    // by these, so the kernel is picked by no larger number
+    const int most_q = max_q < tokens ? max_q : static_cast<int>(tokens);
     return from_cuda(qrk::launch_kv_attention(
         dtype, {q, out, lse, q_offsets, kv_lens, block_table, q_token_stride, q_head_stride, out_token_stride,
-                out_head_stride, tokens, requests, q_heads, table_width, causal != 0, window < kFar ? window : kFar, max_q, scale, workspace},
+                out_head_stride, tokens, requests, q_heads, table_width, causal != 0, window < kFar ? window : kFar, most_q,
+                scale, workspace},
         *cache, reinterpret_cast<cudaStream_t>(stream)));
 }
 

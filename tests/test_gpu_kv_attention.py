@@ -237,6 +237,18 @@ def test_results_do_not_depend_on_max_q():
     assert want[0].shape == c.q.shape
 
 
+@pytest.mark.parametrize("nq", [1, 4])
+def test_max_q_beyond_the_tokens_stays_in_the_workspace(nq):
+    c = Case([20000], [nq], 1, 8, seed=22)
+    need = qr.qr_kv_attention_workspace_bytes(1, nq, 8, 1, 128)
+    buf = torch.full((need + (8 << 20),), 77, dtype=torch.uint8, device="cuda")
+    buf[:need] = 0
+    want, want_lse = c.check()
+    out, lse = c.check(max_q=1 << 20, workspace=buf[:need])
+    assert (buf[need:] == 77).all()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 def test_same_bits_twice_and_on_another_stream():
     c = Case([4000, 37, 1], [1, 1, 1], 2, 8, seed=22)
     out, lse = c.check()
