@@ -281,37 +281,52 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
 
         // the queries as fp16 fragments, each row scaled by a power of two to
         // a largest magnitude in [2^12, 2^13): exact for fp16 and bf16 inputs
-        // down to 2^-26 of it, and the inverse goes into the score's factor
-        for (int rr = warp; rr < kRows; rr += kAttnWarps) {
-            const int row = row0 + rr;
+        // down to 2^-26 of it, and the inverse goes into the score's factor.
+        // A lane holds four dimensions (and four more, 128 on) of each of the
+        // warp's rows; all rows are loaded before the first is waited for.
+        constexpr int kQRows = kRows / kAttnWarps, kQFours = DP <= 128 ? 1 : DP / 128;
+        uint2 raw[kQRows][kQFours];
+#pragma unroll
+        for (int n = 0; n < kQRows; ++n) {
+            const int rr = warp + n * kAttnWarps, row = row0 + rr;
             const uint16_t *q = static_cast<const uint16_t *>(a.q) + (x.q0 + row / group) * a.q_token +
                                 (static_cast<long long>(h) * group + row % group) * a.q_head;
-            float f[DP / 32], amax = 0.0f;
 #pragma unroll
-            for (int i = 0; i < DP / 32; ++i) {
-                const int d = lane + 32 * i;
-                f[i] = rr < rows_here && d < dim ? widen1<BF16>(q[d]) : 0.0f;
-                amax = fmaxf(amax, fabsf(f[i]));
+            for (int i = 0; i < kQFours; ++i) {
+                const int d = lane * 4 + i * 128;
+                raw[n][i] = rr < rows_here && d < dim ? *reinterpret_cast<const uint2 *>(q + d) : make_uint2(0, 0);
             }
+        }
+#pragma unroll
+        for (int n = 0; n < kQRows; ++n) {
+            const int rr = warp + n * kAttnWarps;
+            float f[kQFours][4], amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kQFours; ++i)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t word = w < 2 ? raw[n][i].x : raw[n][i].y;
+                    f[i][w] = widen1<BF16>(static_cast<uint16_t>(word >> (w & 1) * 16));
+                    amax = fmaxf(amax, fabsf(f[i][w]));
+                }
 #pragma unroll
             for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
-            int e = 0;
-            if (amax > 0.0f && amax < INFINITY) {
-                frexpf(amax, &e);
-                e -= 13;
-            }
+            // (a largest magnitude below 2^-126 is scaled as 2^-126 is)
+            const int e = amax > 0.0f && amax < INFINITY ? max(static_cast<int>(__float_as_uint(amax) >> 23), 1) - 139 : 0;
             // 2^-e in two factors, as e may pass the range of one; a negative
             // scale's sign goes into the query, so that the factor is not negative
             const float down1 = pow2i(-(e / 2)) * (a.scale < 0.0f ? -1.0f : 1.0f), down2 = pow2i(-(e - e / 2));
-            if (lane == 0) row_scale[rr] = ldexpf(fabsf(a.scale) * 1.4426950408889634f, e);
-            __half *frag = reinterpret_cast<__half *>(q_frag);
+            if (lane == 0) row_scale[rr] = fabsf(a.scale) * 1.4426950408889634f * pow2i(e / 2) * pow2i(e - e / 2);
 #pragma unroll
-            for (int i = 0; i < DP / 32; ++i) {
+            for (int i = 0; i < kQFours; ++i) {
                 // dimension d = 64 c + 16 t + 4 j + w is element w of lane
                 // (row % 8, t) in step 4 c + j
-                const int d = lane + 32 * i;
-                const int ks = (d >> 6) * 4 + ((d >> 2) & 3), ft = (d >> 4) & 3, w = d & 3;
-                frag[(((rr >> 3) * kSteps + ks) * 32 + (rr & 7) * 4 + ft) * 4 + w] = __float2half_rn(f[i] * down1 * down2);
+                const int d = lane * 4 + i * 128;
+                const int ks = (d >> 6) * 4 + ((d >> 2) & 3), ft = (d >> 4) & 3;
+                uint2 y;
+                y.x = pack_f16(f[i][0] * down1 * down2, f[i][1] * down1 * down2);
+                y.y = pack_f16(f[i][2] * down1 * down2, f[i][3] * down1 * down2);
+                if (d < DP) reinterpret_cast<uint2 *>(q_frag)[((rr >> 3) * kSteps + ks) * 32 + (rr & 7) * 4 + ft] = y;
             }
         }
         __syncthreads();
