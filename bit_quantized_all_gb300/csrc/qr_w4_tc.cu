@@ -14,7 +14,8 @@
 //
 // What bounds it: the warps' latencies, of which two a scheduler hide each
 // other's in the conversion and in the sums, above the codes from HBM (4 KB a
-// chunk, 178 cycles of an SM's share).
+// chunk, 178 cycles of an SM's share): some 700 cycles a chunk (64 tokens
+// through 20481 x 5123 52.7 us, 1.1 TB/s of weights, 255 TFLOP/s).
 #include <cooperative_groups.h>
 
 #include "qr_launch.h"

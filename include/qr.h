@@ -76,8 +76,10 @@
  *     after it with programmatic serialization must wait likewise before
  *     it reads this call's outputs.  (The flag-joined two-shot and the
  *     self-tests are launched plainly.)
- *   - Failure of a device-side wait: the staged kernels and the flag-joined
- *     two-shot bound every wait (one second).  A wait that runs out (which
+ *   - Failure of a device-side wait: the staged kernels, the flag-joined
+ *     two-shot and the kernels that wait for their tensor-core products
+ *     (qr_kv_attention above 32 query rows, qr_w4_matvec above 16 tokens)
+ *     bound every wait (one second).  A wait that runs out (which
  *     a correct launch never does) makes the kernel stop early and count
  *     one timeout; the call has already returned QR_OK, because it returns
  *     when the work is enqueued, and its outputs are then incomplete.  To
@@ -614,7 +616,7 @@ qr_status_t qr_fp4_allreduce(qr_dtype_t dtype, int R, const void *const *x,
  * The cache.  A block holds block_size consecutive tokens of one request for
  * every key/value head; keys and values are int8 codes, one fp32 scale for
  * each (block, head), and value = code * scale.  The arithmetic is the
- * symmetric codec's at INT8 with the scale kept in fp32:
+ * symmetric codec's at INT8 with the scale kept in fp32, never negative:
  *   A = max|x| over the tokens of the block that one call writes,
  *   s = max(s_old, A / 128)   (s_old = 0 when the call writes the block's
  *                              first token; exact), r = fp32_RN(1/s), 0 if s = 0,
@@ -623,6 +625,7 @@ qr_status_t qr_fp4_allreduce(qr_dtype_t dtype, int R, const void *const *x,
  *   round_half_even(clip(fp32_RN(fp32_RN(code*s_old) * r), -128, 127)).
  * Inputs must be finite; a non-finite key or value leaves the codes and the
  * scale of its own (block, head) unspecified and touches nothing else.
+ * Attention takes any codes, and scales that are finite and not negative.
  *
  * Codes are [blocks][heads][block_size][head_dim] with each head's tokens
  * contiguous; the strides between blocks and heads are the caller's (so the
@@ -656,9 +659,9 @@ typedef struct {
  *                           needed beyond num_free, table entries that were
  *                           needed beyond table_width.
  * counts[2] and counts[3] are 0 in a step that fitted; tokens past the
- * 2^31 - 1st are counted (to that number) and get neither block nor slot.  free_blocks may be
- * NULL when num_free is 0; slots when max_tokens is 0.  int32 arrays 4-byte,
- * slots 8-byte aligned.  requests <= 65536. */
+ * 2^31 - 1st are counted (to that number) and get neither block nor slot.
+ * free_blocks may be NULL when num_free is 0; slots when max_tokens is 0.
+ * int32 arrays 4-byte, slots 8-byte aligned.  requests <= 65536. */
 qr_status_t qr_kv_plan(int requests, const int32_t *cached_lens, const int32_t *new_lens,
                        int block_size, const int32_t *free_blocks, int num_free,
                        int32_t *block_table, int table_width, int32_t *q_offsets,
@@ -693,11 +696,13 @@ qr_status_t qr_kv_append(qr_dtype_t dtype, int64_t tokens, const void *k, const 
  * [tokens][q_heads][head_dim], token and head strides in values (multiples
  * of 8; 16-byte aligned); lse (may be NULL) is fp32 [tokens][q_heads].
  * Tokens past q_offsets[requests] are left alone.  max_q is the caller's
- * bound on the n_r (it picks the kernel; results do not depend on it).
- * Products are exact in fp32 accumulation: codes as fp16 integers, queries
- * as fp16 after an exact power-of-two scaling of each row (values more than
- * 2^-28 below their row's largest lose bits); softmax weights are rounded to
- * fp16 for the second product; statistics and sums are fp32.
+ * bound on the n_r (it picks the kernel; every query is
+ * answered whatever it says).  Products are accumulated in fp32: codes as
+ * fp16 integers, queries as fp16 after an exact power-of-two scaling of each
+ * row (values below 2^-26 of their row's largest lose bits); softmax weights
+ * enter the second product rounded to fp16 for bf16 outputs, and as two fp16
+ * numbers for fp16 outputs; statistics and sums are fp32.  A query that is
+ * not finite makes its own row NaN.
  * The workspace (qr_kv_attention_workspace_bytes, 16-byte aligned) must be
  * zeroed once before its first use; every call leaves it ready for the next
  * one on the same stream. */
