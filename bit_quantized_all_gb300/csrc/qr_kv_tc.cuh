@@ -20,13 +20,13 @@
 // scales are kept by more than 2^kScaleSlack; weights are then below 2^15, and
 // fp16 keeps them exact to 2^-12 down to 2^-21 of a weight of 1.  For fp16
 // output what that rounding left is a second P (8 prompt chunks of up to 1024
-// queries over up to 8192 keys: 409 us for bf16, 440 us for fp16).
+// queries over up to 8192 keys: 364 us for bf16, 409 us for fp16).
 //
 // What bounds it: latency.  A tile of both halves takes some 4000 cycles, of
 // which the products take 2048 and the softmax's and conversion's instructions
 // about as many; a half's chain of scores, maximum, weights and their store
 // leaves gaps that the other half does not fill (8 prompt chunks of up to 1024
-// queries over up to 8192 keys, 40 heads on 8, 128 dimensions: 409 us, 704
+// queries over up to 8192 keys, 40 heads on 8, 128 dimensions: 364 us, 792
 // TFLOP/s).
 #pragma once
 
@@ -37,9 +37,10 @@ namespace qrk {
 
 constexpr int kTcRows = 256, kTcHalf = 128, kTcKeys = 128;
 constexpr int kTcThreads = 416;  // warps 0-7 softmax, 8-11 conversion, 12 products
-// An item's queries, output and empty pipeline take about as long as this many
-// tiles; the shares count them, as tiles before the first one.
-constexpr int kItemSteps = 3;
+// An item's queries, output, masked tiles and empty pipeline take about as long
+// as this many tiles; the shares count them, as tiles before the first one (8
+// prompt chunks over up to 8192 keys: 3 407 us, 4 364, 5 365, 8 378).
+constexpr int kItemSteps = 4;
 constexpr int kTcMostCtas = 160;
 constexpr float kSlack = 6.0f;
 constexpr int kScaleSlack = 2;
@@ -119,12 +120,19 @@ struct TcWalk {
         head = static_cast<int>((step - at) / steps);
         item_first = at + static_cast<long long>(head) * steps;
         const int s0 = static_cast<int>(step - item_first), s1 = static_cast<int>(min(item_first + steps, last) - item_first);
+        // its first part is the one with its first tile: a share that ends
+        // before that leaves the item alone
+        const int lead = min(kItemSteps, steps - 1);
+        if (s1 <= lead) {
+            step = last;
+            return false;
+        }
         begin = b + max(0, s0 - kItemSteps) * kTcKeys;
         end = min(b + max(0, s1 - kItemSteps) * kTcKeys, e);
         row0 = j * kTcRows;
         rows = min(kTcRows, x.nq * group - row0);
         p0 = x.kv - x.nq;
-        part_first_cta = static_cast<int>(item_first / share);
+        part_first_cta = static_cast<int>((item_first + lead) / share);
         parts = static_cast<int>((item_first + steps - 1) / share) - part_first_cta + 1;
         step = item_first + s1;
         return true;
