@@ -29,11 +29,11 @@
 // bits was 1.6 times that of a product in 32 bits, with it the same).
 //
 // What bounds it: the codes from HBM when there is enough of them (128 single
-// tokens over up to 8192 keys, 8 heads: 188 us, 5.8 TB/s, 0.86 of the copy
+// tokens over up to 8192 keys, 8 heads: 187 us, 5.8 TB/s, 0.87 of the copy
 // rate), the conversion's and the products' issue when an item has more than
-// eight rows (20 rows over 131075 keys: 85 us, 3.1 TB/s), and below some 20 us
+// eight rows (20 rows over 131075 keys: 82 us, 3.3 TB/s), and below some 20 us
 // the chain of dependent round trips: lengths, table, codes, parts, join (16
-// single tokens over up to 2048 keys, one head: 13.6 us).
+// single tokens over up to 2048 keys, one head: 11.7 us).
 #pragma once
 
 #include <type_traits>
@@ -653,23 +653,33 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
                 __syncthreads();
                 const bool last = level == 1 || groups == 1;
                 float *const to = partial + slot_of(at_cta) * S::kSlot;
-                for (int i = tid; i < rows_here * kQuads; i += kAttnThreads) {
-                    const int rr = i / kQuads, d = i % kQuads * 4, row = row0 + rr;
-                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                // two pieces a thread at a time, eight parts of each on their way
+                for (int i0 = tid; i0 < rows_here * kQuads; i0 += 2 * kAttnThreads) {
+                    const int piece[2] = {i0, min(i0 + kAttnThreads, rows_here * kQuads - 1)};
+                    float4 v[2];
+                    v[0] = v[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
                     for (int k = 0; k < count; ++k) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(
-                            partial + slot_of(at_cta + k * stride) * S::kSlot + rr * DP + d));
-                        const float f = weight[rr * kMostParts + k];
-                        v.x = __fmaf_rn(y.x, f, v.x), v.y = __fmaf_rn(y.y, f, v.y);
-                        v.z = __fmaf_rn(y.z, f, v.z), v.w = __fmaf_rn(y.w, f, v.w);
+                        const float *const part = partial + slot_of(at_cta + k * stride) * S::kSlot;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + piece[u] * 4));
+                            const float f = weight[piece[u] / kQuads * kMostParts + k];
+                            v[u].x = __fmaf_rn(y.x, f, v[u].x), v[u].y = __fmaf_rn(y.y, f, v[u].y);
+                            v[u].z = __fmaf_rn(y.z, f, v[u].z), v[u].w = __fmaf_rn(y.w, f, v[u].w);
+                        }
                     }
-                    const float2 ts = total[rr];
-                    if (last) {
-                        attn_write<BF16>(a, dim, x.q0 + row / group, h * group + row % group, d, v, ts.x, ts.y);
-                    } else {
-                        __stcg(reinterpret_cast<float4 *>(to + rr * DP + d), v);
-                        if (d == 0) __stcg(reinterpret_cast<float2 *>(to + kRows * DP + 2 * rr), ts);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int rr = piece[u] / kQuads, d = piece[u] % kQuads * 4, row = row0 + rr;
+                        if (i0 + u * kAttnThreads >= rows_here * kQuads) break;
+                        const float2 ts = total[rr];
+                        if (last) {
+                            attn_write<BF16>(a, dim, x.q0 + row / group, h * group + row % group, d, v[u], ts.x, ts.y);
+                        } else {
+                            __stcg(reinterpret_cast<float4 *>(to + rr * DP + d), v[u]);
+                            if (d == 0) __stcg(reinterpret_cast<float2 *>(to + kRows * DP + 2 * rr), ts);
+                        }
                     }
                 }
                 if (last) break;
@@ -706,7 +716,7 @@ cudaError_t run_kv_split(const KvAttentionArgs &a, const KvView &c, int group, c
     return c.dim == DP ? run_kv_split<DP, NT, true, BF16>(a, c, group, s) : run_kv_split<DP, NT, false, BF16>(a, c, group, s);
 }
 
-// As few column tiles as hold the rows: 20 rows over 131075 keys take 89 us as
+// As few column tiles as hold the rows: 20 rows over 131075 keys took 89 us as
 // three and 111 as four.  Above 128 dimensions the accumulators leave room for
 // two, and more rows are more items.
 template <bool BF16>
