@@ -231,9 +231,11 @@ cudaError_t launch_kv_append(int dtype, long long tokens, const void *k, const v
     a.dim = cache.head_dim;
     a.inv = static_cast<uint32_t>(((1ull << 32) + a.dim / 8 - 1) / (a.dim / 8));
     for (a.shift = 0; (1 << a.shift) < cache.block_size;) ++a.shift;
-    // teams for runs of a whole block; a window of eight tokens, more when the
-    // call would otherwise make over eight CTAs a SM (most of them, in a
-    // prompt, with no run that begins in them)
+    // teams for runs of a whole block (8 x 1024 tokens into blocks of 128 of 256
+    // dimensions 25 us, a warp each 59; 32 x 1024 into blocks of 32 of 128 37 and
+    // 43); a window of eight tokens, more when the call would otherwise make over
+    // eight CTAs a SM, most of them, in a prompt, with no run that begins in them
+    // (the latter prompt with eight 142 us; 256 single tokens 4.2 us, with 256 38)
     cudaError_t err = cudaSuccess;
     const int sms = sm_count(&err);
     if (sms <= 0) return err;

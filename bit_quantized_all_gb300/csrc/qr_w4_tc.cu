@@ -423,6 +423,8 @@ cudaError_t launch_w4_tc(int dtype, const W4MatvecArgs &given, bool zeros, void 
         a.x_stride = a.l.chunks * 64;
         a.cols = a.l.chunks * 64;
     }
+    // up to 32 tokens half the columns: 32 tokens through 8192 x 8192 22 us, as
+    // half of a tile of 64 26 us
     if (a.tokens <= 32) return dtype ? pick_group<1, 32>(a, zeros, s) : pick_group<0, 32>(a, zeros, s);
     return dtype ? pick_group<1, 64>(a, zeros, s) : pick_group<0, 64>(a, zeros, s);
 }
