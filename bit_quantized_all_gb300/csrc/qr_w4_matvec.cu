@@ -42,15 +42,22 @@ __device__ __forceinline__ void mma_typed(float (&d)[4], const uint32_t (&a)[4],
 
 template <int NT>
 struct MatvecSmem {
-    static constexpr int kPanel = 16;  // chunks of x held at a time
+    static constexpr int kPanel = 16;                      // chunks of x held at a time
+    static_assert(kPanel % kMvDepth == 0, "panels change between rounds of chunks");
     static constexpr int kPitch = kPanel * 128 + 32;       // bytes of a token's row: no bank conflicts
     static constexpr int kBuffer = 8 * NT * kPitch;
     static constexpr int kBytes = 2 * kBuffer;
 };
 
+// CTAs per SM: with a row tile a warp four (one token through 20480 x 5120 20.0
+// us, with three 23.4), or three where zero points of groups of 32 would spill
+// (8 tokens through 8192 x 8192 17.0 us, with four 19.3).
+template <int RT, int NG, bool ZEROS>
+constexpr int kMvCtas = RT == 2 ? 2 : NG == 2 && ZEROS ? 3 : 4;
+
 // NG: groups of a 64-column chunk (2 for groups of 32, else 1).
 template <int DT, int RT, int NT, int NG, bool ZEROS>
-__global__ void __launch_bounds__(kMvThreads, RT == 1 ? 3 : 2) w4_matvec_kernel(W4MatvecArgs a, int slice, bool vector) {
+__global__ void __launch_bounds__(kMvThreads, kMvCtas<RT, NG, ZEROS>) w4_matvec_kernel(W4MatvecArgs a, int slice, bool vector) {
     chain_entry();
     using S = MatvecSmem<NT>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -223,13 +230,13 @@ static cudaError_t run_matvec(const W4MatvecArgs &a, cudaStream_t s) {
     const long long row_ctas = (a.l.row_tiles + RT * kMvWarps - 1) / (RT * kMvWarps);
     const long long token_ctas = (a.tokens + 8 * NT - 1) / (8 * NT);
     // the number of slices whose waves of CTAs, each its chunks and about three
-    // more to start and end, are shortest (8192 x 8192, one token: 6 slices 14.3
-    // us, 4 18.0, 8, which no longer fit at once, 16.8; clusters of 5 and 7 leave
-    // SMs of a processing cluster idle)
+    // more to start and end, are shortest (8192 x 8192, one token, with three CTAs
+    // an SM: 6 slices 14.3 us, 4 18.0, 8, which did not fit at once, 16.8; clusters
+    // of 5 and 7 leave SMs of a processing cluster idle)
     int splits = 1;
     long long best = -1;
     for (int n : {1, 2, 3, 4, 6, 8}) {
-        const long long slots = (RT == 1 ? 3ll : 2ll) * sms, waves = (row_ctas * token_ctas * n + slots - 1) / slots;
+        const long long slots = static_cast<long long>(kMvCtas<RT, NG, ZEROS>) * sms, waves = (row_ctas * token_ctas * n + slots - 1) / slots;
         const long long cost = waves * ((a.l.chunks + n - 1) / n + 3);
         if (best < 0 || (n <= a.l.chunks && cost < best)) best = cost, splits = n;
     }
