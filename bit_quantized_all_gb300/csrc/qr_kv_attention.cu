@@ -22,8 +22,8 @@ cudaError_t launch_kv_attention(int dtype, const KvAttentionArgs &a, const qr_kv
     const KvView c = kv_view(cache);
     const int group = a.q_heads / c.heads;
     // Above 32 rows an item the products are tcgen05's: 32 rows over one context
-    // of 131075 keys take 84 us split and 101 so, in 64 requests of up to 2048
-    // keys 70 and 63; 40 rows 120 and 100, and 149 and 62.
+    // of 131075 keys take 80 us split and 107 so, in 64 requests of up to 2048
+    // keys 83 and 69; 40 rows 120 and 108, and 135 and 69.
     if (c.dim <= 128 && static_cast<long long>(a.max_q) * group > 32) return launch_kv_tc(dtype, a, c, group, s);
     return dtype ? launch_kv_split_bf16(a, c, group, s) : launch_kv_split_f16(a, c, group, s);
 }

@@ -22,18 +22,22 @@
 // Scores are scaled by the block's scale in fp32.  The values' scale goes into
 // the softmax weight before its rounding to fp16, relative to a power of two
 // kept per row (the largest among the blocks that the row sees), so that the
-// accumulators are the matrix instruction's own.  For bf16 output the weight is
-// that one fp16 number, whose error (2^-12 of it) is far below the output's;
-// for fp16 output what its rounding left goes through a second product (128
-// requests of up to 8192 keys: 186 -> 190 us; without it the error against 64
-// bits was 1.6 times that of a product in 32 bits, with it the same).
+// accumulators are the matrix instruction's own.  What that rounding left goes
+// through a second product: a weight as one fp16 number is off by up to 2^-12,
+// which showed in outputs of both types (0.001 of a bf16 output's norm away
+// from a product in 32 bits, with both terms 0.0001; the error of fp16 outputs
+// against 64 bits 1.6 times a 32-bit product's, with both the same).  It costs
+// nothing where HBM bounds (128 requests of up to 8192 keys 187 and 186 us) and
+// 12% where the products do (20 rows over 131075 keys 82 and 92 us).
 //
 // What bounds it: the codes from HBM when there is enough of them (128 single
-// tokens over up to 8192 keys, 8 heads: 187 us, 5.8 TB/s, 0.87 of the copy
-// rate), the conversion's and the products' issue when an item has more than
-// eight rows (20 rows over 131075 keys: 82 us, 3.3 TB/s), and below some 20 us
-// the chain of dependent round trips: lengths, table, codes, parts, join (16
-// single tokens over up to 2048 keys, one head: 11.7 us).
+// tokens over up to 8192 keys, 8 heads: 186 us, 5.8 TB/s, 0.87 of the copy
+// rate); with more than eight rows an item latency, as two or three CTAs an SM
+// are all that the accumulators' registers leave, and each warp waits for its
+// own chain of copies, conversion, products and softmax (20 rows over 131075
+// keys: 92 us, 2.9 TB/s); and below some 20 us the chain of dependent round
+// trips: lengths, table, codes, parts, join (16 single tokens over up to 2048
+// keys, one head: 11.8 us).
 #pragma once
 
 #include <type_traits>
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
             const bool mask = !valid[0] || !valid[1] || key0 + kTile > seen_end || key0 < seen_begin;
             const int vexp[2] = {scale_exp(vs_cur[0]), scale_exp(vs_cur[1])};
             uint32_t p[NT][2][2];     // B fragments of the two 16-key groups
-            uint32_t lo_p[NT][2][2];  // what their rounding left (fp16 output)
+            uint32_t lo_p[NT][2][2];  // what their rounding left
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
                 // (a score is rounded before the maximum is taken from it: of
@@ -501,8 +505,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
                     for (int u = 0; u < 2; ++u) {
                         const uint32_t hi = pack_f16(y[2 * u], y[2 * u + 1]);
                         p[q][kt][u] = transpose8(hi);
-                        if constexpr (!BF16)
-                            lo_p[q][kt][u] = transpose8(rest_f16(make_float2(y[2 * u], y[2 * u + 1]), hi));
+                        lo_p[q][kt][u] = transpose8(rest_f16(make_float2(y[2 * u], y[2 * u + 1]), hi));
                     }
                 }
             }
@@ -539,10 +542,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
 #pragma unroll
                             for (int q = 0; q < NT; ++q)
                                 mma_f16_acc(o[q][pc * 8 + wd * 2 + u], va, p[q][kt][0], p[q][kt][1]);
-                            if constexpr (!BF16)
 #pragma unroll
-                                for (int q = 0; q < NT; ++q)
-                                    mma_f16_acc(o[q][pc * 8 + wd * 2 + u], va, lo_p[q][kt][0], lo_p[q][kt][1]);
+                            for (int q = 0; q < NT; ++q)
+                                mma_f16_acc(o[q][pc * 8 + wd * 2 + u], va, lo_p[q][kt][0], lo_p[q][kt][1]);
                         }
                     }
                 }
@@ -716,8 +718,8 @@ cudaError_t run_kv_split(const KvAttentionArgs &a, const KvView &c, int group, c
     return c.dim == DP ? run_kv_split<DP, NT, true, BF16>(a, c, group, s) : run_kv_split<DP, NT, false, BF16>(a, c, group, s);
 }
 
-// As few column tiles as hold the rows: 20 rows over 131075 keys took 89 us as
-// three and 111 as four.  Above 128 dimensions the accumulators leave room for
+// As few column tiles as hold the rows: 20 rows over 131075 keys take 91 us as
+// three and 116 as four.  Above 128 dimensions the accumulators leave room for
 // two, and more rows are more items.
 template <bool BF16>
 cudaError_t pick_kv_split(const KvAttentionArgs &a, const KvView &c, int group, cudaStream_t s) {

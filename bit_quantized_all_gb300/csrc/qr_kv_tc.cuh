@@ -18,16 +18,16 @@
 // O stays in tensor memory.  It is rescaled only when a row's maximum has
 // grown by more than 2^kSlack, or the power of two under which the values'
 // scales are kept by more than 2^kScaleSlack; weights are then below 2^15, and
-// fp16 keeps them exact to 2^-12 down to 2^-21 of a weight of 1.  For fp16
-// output what that rounding left is a second P (8 prompt chunks of up to 1024
-// queries over up to 8192 keys: 364 us for bf16, 409 us for fp16).
+// fp16 keeps them exact to 2^-12 down to 2^-21 of a weight of 1.  What that
+// rounding left is a second P, as in qr_kv_split.cuh (8 prompt chunks of up to
+// 1024 queries over up to 8192 keys: 409 us, with one P 364, and outputs 0.001
+// of their norm away from a product in 32 bits instead of 0.0001).
 //
-// What bounds it: latency.  A tile of both halves takes some 4000 cycles, of
-// which the products take 2048 and the softmax's and conversion's instructions
-// about as many; a half's chain of scores, maximum, weights and their store
-// leaves gaps that the other half does not fill (8 prompt chunks of up to 1024
-// queries over up to 8192 keys, 40 heads on 8, 128 dimensions: 364 us, 792
-// TFLOP/s).
+// What bounds it: latency.  A tile of both halves takes some 4500 cycles, of
+// which the products take 3072 and the softmax's and conversion's instructions
+// as many; a half's chain of scores, maximum, weights and their store leaves
+// gaps that the other half does not fill (8 prompt chunks of up to 1024 queries
+// over up to 8192 keys, 40 heads on 8, 128 dimensions: 409 us, 704 TFLOP/s).
 #pragma once
 
 #include "qr_kv_split.cuh"
@@ -39,7 +39,7 @@ constexpr int kTcRows = 256, kTcHalf = 128, kTcKeys = 128;
 constexpr int kTcThreads = 416;  // warps 0-7 softmax, 8-11 conversion, 12 products
 // An item's queries, output, masked tiles and empty pipeline take about as long
 // as this many tiles; the shares count them, as tiles before the first one (8
-// prompt chunks over up to 8192 keys: 3 407 us, 4 364, 5 365, 8 378).
+// prompt chunks over up to 8192 keys: 3 436 us, 4 409, 5 414, 8 431).
 constexpr int kItemSteps = 4;
 constexpr int kTcMostCtas = 160;
 constexpr float kSlack = 6.0f;
@@ -173,9 +173,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     using S = TcSmem<DP>;
     extern __shared__ uint8_t raw[];
     S &sm = *reinterpret_cast<S *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
-    // weights as one fp16 number, or for fp16 output as two: kTerms * 8 of S's
-    // columns for each 16 keys
-    constexpr int kTerms = BF16 ? 1 : 2;
+    // weights as two fp16 numbers: kTerms * 8 of S's columns for each 16 keys
+    constexpr int kTerms = 2;
     const int dim = FULL ? DP : c.dim;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -625,7 +624,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     const float2 y = make_float2(__uint_as_float(now[2 * k]), __uint_as_float(now[2 * k + 1]));
                                     next[2 * k] = __float_as_uint(exp2_fast(__uint_as_float(next[2 * k])));
                                     p[0][k] = pack_f16(y.x, y.y);
-                                    if constexpr (!BF16) p[kTerms - 1][k] = rest_f16(y, p[0][k]);
+                                    p[1][k] = rest_f16(y, p[0][k]);
                                     next[2 * k + 1] = __float_as_uint(exp2_fast(__uint_as_float(next[2 * k + 1])));
                                     part[k & 1] = k < 2 ? y : add2(part[k & 1], y);
                                 }
@@ -664,7 +663,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 }
                                 const float2 z = make_float2(y[0] * w, y[1] * w);
                                 p[0][k / 2] = pack_f16(z.x, z.y);
-                                if constexpr (!BF16) p[kTerms - 1][k / 2] = rest_f16(z, p[0][k / 2]);
+                                p[1][k / 2] = rest_f16(z, p[0][k / 2]);
                             }
 #pragma unroll
                             for (int lo = 0; lo < kTerms; ++lo) tc_st8(scol + (g8 * kTerms + lo) * 8, p[lo]);

@@ -700,8 +700,8 @@ qr_status_t qr_kv_append(qr_dtype_t dtype, int64_t tokens, const void *k, const 
  * answered whatever it says).  Products are accumulated in fp32: codes as
  * fp16 integers, queries as fp16 after an exact power-of-two scaling of each
  * row (values below 2^-26 of their row's largest lose bits); softmax weights
- * enter the second product rounded to fp16 for bf16 outputs, and as two fp16
- * numbers for fp16 outputs; statistics and sums are fp32.  A query that is
+ * enter the second product as two fp16 numbers, to 2^-22 of themselves;
+ * statistics and sums are fp32.  A query that is
  * not finite makes its own row NaN.
  * The workspace (qr_kv_attention_workspace_bytes, 16-byte aligned) must be
  * zeroed once before its first use; every call leaves it ready for the next
