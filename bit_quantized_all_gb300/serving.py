@@ -10,7 +10,10 @@ and ``qr_w4_matvec`` multiplies by 4-bit weights with group scales.
 
 As the rest of the binding, these functions check the tensors, pick the
 caller's current stream and call the C ABI; they raise if ``libqr.so`` is
-missing, and there is no CPU path.
+missing, and there is no CPU path.  A call given ``stream`` (a
+``torch.cuda.Stream`` or a raw handle) runs as it would with that stream
+current: outputs and workspaces that it makes for itself are allocated and
+zeroed there, and belong to that stream.
 """
 from __future__ import annotations
 
@@ -69,10 +72,22 @@ def _lib():
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _current(device: torch.device, stream) -> int:
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(device.index)
-    return _stream(device, stream)
+def _current(device: torch.device) -> int:
+    return _raw_stream(device.index) if _raw_stream is not None else _stream(device, None)
+
+
+def _as_current(device: torch.device, stream):
+    """A context in which ``stream`` is the current one.  What a call allocates
+    on another stream than its own could still be in use by work queued there,
+    be zeroed after the call has read it, and be handed on while the call
+    runs."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(device, stream)
+        # (0 and 1 are the runtime's names of the default stream)
+        stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _int_tensor(t, what: str, dtype, shape=None) -> None:
@@ -154,6 +169,9 @@ def qr_kv_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     (int32 [requests, width], in place).  ``plan`` reuses an earlier result's
     buffers."""
     _int_tensor(cached_lens, "cached_lens", torch.int32)
+    if stream is not None:
+        with _as_current(cached_lens.device, stream):
+            return qr_kv_plan(cached_lens, new_lens, block_table, free_blocks, block_size, max_tokens, plan)
     requests = cached_lens.numel()
     _int_tensor(new_lens, "new_lens", torch.int32, cached_lens.shape)
     _int_tensor(block_table, "block_table", torch.int32)
@@ -179,7 +197,7 @@ def qr_kv_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     status = (_L or _lib()).qr_kv_plan(
         requests, cached_lens.data_ptr(), new_lens.data_ptr(), block_size, free_blocks.data_ptr(), free_blocks.numel(),
         block_table.data_ptr(), block_table.shape[1], q_offsets.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(),
-        max_tokens, counts.data_ptr(), _current(dev, stream))
+        max_tokens, counts.data_ptr(), _current(dev))
     if status:
         _check(status, "qr_kv_plan")
     return plan
@@ -204,6 +222,9 @@ def _rows(t: torch.Tensor, what: str, heads: int | None, dim: int) -> None:
 def qr_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> KVCache:
     """Quantizes fp16/bf16 keys and values ([tokens, heads, head_dim]) into
     the cache at ``slots`` (int64 [tokens], as qr_kv_plan gives them)."""
+    if stream is not None:
+        with _as_current(cache.device, stream):
+            return qr_kv_append(cache, k, v, slots)
     _rows(k, "k", cache.heads, cache.head_dim)
     _rows(v, "v", cache.heads, cache.head_dim)
     tokens = k.shape[0]
@@ -217,7 +238,7 @@ def qr_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.
         kt, kh, _ = k.stride()
         vt, vh, _ = v.stride()
         status = (_L or _lib()).qr_kv_append(dt, tokens, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(),
-                                             cache._ref, _current(dev, stream))
+                                             cache._ref, _current(dev))
         if status:
             _check(status, "qr_kv_append")
     return cache
@@ -250,6 +271,10 @@ def qr_kv_attention(q: torch.Tensor, cache: KVCache, q_offsets: torch.Tensor, kv
     defaults to head_dim ** -0.5, ``max_q`` (a bound on the queries of one
     request, which picks the kernel) to the number of tokens.  Returns ``out``, or
     ``(out, lse)``.  Without ``workspace`` one is allocated and zeroed."""
+    if stream is not None:
+        with _as_current(cache.device, stream):
+            return qr_kv_attention(q, cache, q_offsets, kv_lens, block_table, scale, causal, window, max_q, out,
+                                   return_lse, workspace)
     _rows(q, "q", None, cache.head_dim)
     tokens, q_heads = q.shape[0], q.shape[1]
     dt = _dtype_code(q, "q")
@@ -281,7 +306,7 @@ def qr_kv_attention(q: torch.Tensor, cache: KVCache, q_offsets: torch.Tensor, kv
             dt, requests, tokens, q_heads, q.data_ptr(), qt, qh, q_offsets.data_ptr(), kv_lens.data_ptr(),
             block_table.data_ptr(), block_table.shape[1], cache._ref, cache.head_dim ** -0.5 if scale is None else scale,
             1 if causal else 0, window, tokens if max_q is None else max_q, out.data_ptr(), ot, oh,
-            lse.data_ptr() if return_lse else None, workspace.data_ptr(), workspace.numel(), _current(dev, stream))
+            lse.data_ptr() if return_lse else None, workspace.data_ptr(), workspace.numel(), _current(dev))
         if status:
             _check(status, "qr_kv_attention")
     return (out, lse) if return_lse else out
@@ -320,6 +345,9 @@ def qr_w4_pack(codes: torch.Tensor, scales: torch.Tensor, cols: int, group: int,
     the low nibble), fp16 scales and optional uint8 zero points (both
     [rows, ceil(cols/group)]): w = (code - zero) * scale, zero 8 if None."""
     _cuda_contig(codes, "codes")
+    if stream is not None:
+        with _as_current(codes.device, stream):
+            return qr_w4_pack(codes, scales, cols, group, zeros)
     if codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[1] != (cols + 1) // 2:
         raise ValueError(f"codes must be torch.uint8 [rows, {(cols + 1) // 2}]")
     if group not in W4_GROUPS:
@@ -331,7 +359,7 @@ def qr_w4_pack(codes: torch.Tensor, scales: torch.Tensor, cols: int, group: int,
     dev = _same_device([codes, scales] + ([] if zeros is None else [zeros]), "qr_w4_pack")
     w = _new_w4(rows, cols, group, zeros is not None, dev)
     _check(_lib().qr_w4_pack(rows, cols, group, codes.data_ptr(), scales.data_ptr(),
-                             None if zeros is None else zeros.data_ptr(), w.packed.data_ptr(), _stream(dev, stream)),
+                             None if zeros is None else zeros.data_ptr(), w.packed.data_ptr(), _current(dev)),
            "qr_w4_pack")
     return w
 
@@ -355,10 +383,13 @@ def qr_w4_quantize(w: torch.Tensor, group: int = 32, stream=None) -> W4Weight:
     """Quantizes fp16/bf16 weights [rows, cols] with the INT4 codec's
     arithmetic on groups of 32, 64 or 128 columns."""
     _matrix(w, "w")
+    if stream is not None:
+        with _as_current(w.device, stream):
+            return qr_w4_quantize(w, group)
     dt = _dtype_code(w, "w")
     out = _new_w4(w.shape[0], w.shape[1], group, False, w.device)
     _check(_lib().qr_w4_quantize(dt, w.shape[0], w.shape[1], group, w.data_ptr(), w.stride(0), out.packed.data_ptr(),
-                                 _stream(w.device, stream)), "qr_w4_quantize")
+                                 _current(w.device)), "qr_w4_quantize")
     return out
 
 
@@ -371,6 +402,9 @@ def qr_w4_matvec(x: torch.Tensor, weight: W4Weight, y: torch.Tensor | None = Non
     """y = x @ w.T for fp16/bf16 x [tokens, cols] and 4-bit weights.  More than
     16 tokens whose rows are not 16-byte aligned are copied into ``workspace``
     (uint8, qr_w4_matvec_workspace_bytes) first; without one it is allocated."""
+    if stream is not None:
+        with _as_current(weight.packed.device, stream):
+            return qr_w4_matvec(x, weight, y, workspace)
     _matrix(x, "x", weight.cols)
     dt = _dtype_code(x, "x")
     tokens = x.shape[0]
@@ -394,7 +428,7 @@ def qr_w4_matvec(x: torch.Tensor, weight: W4Weight, y: torch.Tensor | None = Non
         status = (_L or _lib()).qr_w4_matvec(
             dt, tokens, at, stride, weight.rows, cols, weight.group, weight.has_zeros, weight.packed.data_ptr(),
             y.data_ptr(), y.stride(0), None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel(), _current(dev, stream))
+            0 if workspace is None else workspace.numel(), _current(dev))
         if status:
             _check(status, "qr_w4_matvec")
     return y
