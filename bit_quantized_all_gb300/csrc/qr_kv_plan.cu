@@ -16,16 +16,17 @@
 #include <climits>
 
 #include "qr_device.cuh"
+#include "qr_kv_plan_range.h"
 #include "qr_launch.h"
 #include "qr_serving.h"
 
 namespace qrk {
 
-constexpr int kPlanThreads = 256;
 constexpr int kEach = 8;                         // requests per thread and chunk
 constexpr int kChunk = kPlanThreads * kEach;
-constexpr long long kMostTokens = INT_MAX;       // tokens past it are counted, and get neither block nor slot
-constexpr int kWide = 4;                         // tokens per thread and step
+constexpr long long kMostTokens = kPlanMostTokens;
+constexpr int kWide = kPlanWide;
+static_assert(kMostTokens == INT_MAX, "token numbers are kept as int");
 
 // The two sums a request adds: its new tokens and the blocks it takes.
 struct PlanSum {
@@ -108,8 +109,10 @@ __global__ void __launch_bounds__(kPlanThreads, 3) kv_plan_kernel(KvPlanArgs a, 
             at.blocks += blocks_of(static_cast<uint32_t>(cached[k]) + fresh[k], shift) - blocks_of(cached[k], shift);
         }
         __syncthreads();
-        const int from = static_cast<int>(min(max(lo, chunk_lo), kMostTokens)), to = static_cast<int>(min(hi, all.tokens));
-        for (long long t0 = from + kWide * tid; t0 < to; t0 += kWide * kPlanThreads) {
+        // in 64 bits: a chunk may begin past the last token that an int holds
+        const PlanTokens range_here = plan_tokens(lo, hi, chunk_lo, all.tokens);
+        const long long to = range_here.to;
+        for (long long t0 = plan_first(range_here, tid); t0 < to; t0 += kWide * kPlanThreads) {
             // kWide tokens in a row: the first one's request is the last whose
             // first token is not after it (those past the last request, and
             // those without new tokens, are passed over), the others' follow
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kPlanThreads, 3) kv_plan_kernel(KvPlanArgs a, 
                 k = i % kEach, j = i / kEach;
                 request[u] = c0 + i;
                 const uint32_t c = s_cached[k][j], have = blocks_of(c, shift);
-                pos[u] = c + (static_cast<int>(t0) + u - s_token[k][j]);
+                pos[u] = c + (static_cast<uint32_t>(t0) + u - static_cast<uint32_t>(s_token[k][j]));
                 const uint32_t b = pos[u] >> shift, f = s_block[k][j] + (b - have);
                 const bool held = b < have;
                 id[u] = -1;
