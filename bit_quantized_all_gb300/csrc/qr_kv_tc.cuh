@@ -45,6 +45,11 @@ constexpr int kTcMostCtas = 160;
 constexpr float kSlack = 6.0f;
 constexpr int kScaleSlack = 2;
 constexpr int kTcWeightExp = 7;  // weight 1 of the largest scale is 2^7
+// Where a tile's weights are taken together with the values' scales in one
+// exponent, the smallest scale is at most so many powers of two below the row's
+// power, and that at most so large: a weight of 2^-60 of the row's largest, and
+// its part of the sum, are then still normal numbers.
+constexpr int kScaleSpan = 64, kMostScaleExp = 64;
 
 // Tensor memory columns: S of both halves (P in its place), O of both halves.
 constexpr uint32_t kColS = 0, kColO = 256, kColumns = 512;
@@ -55,7 +60,8 @@ constexpr uint32_t kColS = 0, kColO = 256, kColumns = 512;
 struct alignas(16) TcMeta {
     float4 group[8];  // key scale; log2 of, one over, and the value scale
     int4 tile;        // valid groups; the largest scale_exp among them; whether
-                      // every group is valid and no value scale is zero or near it
+                      // every group is valid and no value scale is zero or near
+                      // it; the smallest scale_exp if so
 };
 
 // Floats of one half's part: accumulators, then (max, sum) pairs.
@@ -324,10 +330,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t valid = __ballot_sync(~0u, ct < 8 && !bad);
                     int e = ct < 8 && !bad ? scale_exp(vs_now) : kLeastExp;
                     const uint32_t sized = __ballot_sync(~0u, e > kLeastExp && e < 120);
+                    int least = e;
 #pragma unroll
-                    for (int d = 1; d < 8; d <<= 1) e = max(e, __shfl_xor_sync(~0u, e, d));
+                    for (int d = 1; d < 8; d <<= 1) {
+                        e = max(e, __shfl_xor_sync(~0u, e, d));
+                        least = min(least, __shfl_xor_sync(~0u, least, d));
+                    }
                     if (ct < 8) meta.group[ct] = make_float4(ks_now, log2_fast(vs_now), 1.0f / vs_now, vs_now);
-                    if (ct == 0) meta.tile = make_int4(static_cast<int>(valid), e, (valid & sized) == 0xffu, 0);
+                    if (ct == 0) meta.tile = make_int4(static_cast<int>(valid), e, (valid & sized) == 0xffu, least);
                 }
                 smem_to_tensor_fence();
                 mbar_arrive(&sm.k_full[s]);
@@ -584,8 +594,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // Weight: 2^(s f - m) w with w the values' scale under the
                     // row's power of two, taken in one exponent; a group's sum
                     // is then divided by w.  Not for scores so large that the
-                    // fused product's unrounded part would matter.
-                    if (!mask && !__any_sync(~0u, !(fabsf(m) < 65536.0f))) {
+                    // fused product's unrounded part would matter, nor for value
+                    // scales so far apart that the exponent would leave fp32's range.
+                    const bool apart = ve - tile.w > kScaleSpan || ve > kMostScaleExp;
+                    if (!mask && !__any_sync(~0u, !(fabsf(m) < 65536.0f) || apart)) {
                         const float lift = base + static_cast<float>(kTcWeightExp - ve);
                         float sums = 0.0f;
                         auto exponents = [&](uint32_t (&y)[16], const float4 &scales) {

@@ -699,9 +699,12 @@ qr_status_t qr_kv_append(qr_dtype_t dtype, int64_t tokens, const void *k, const 
  * bound on the n_r (it picks the kernel; every query is
  * answered whatever it says).  Products are accumulated in fp32: codes as
  * fp16 integers, queries as fp16 after an exact power-of-two scaling of each
- * row (values below 2^-26 of their row's largest lose bits); softmax weights
- * enter the second product as two fp16 numbers, to 2^-22 of themselves;
- * statistics and sums are fp32.  A query that is
+ * row (values below 2^-26 of their row's largest lose bits).  Softmax weights,
+ * exp(S_i - max S), enter the second product times their value's scale as two
+ * fp16 numbers: off by up to 2^-22 of themselves, and by up to 2^-31 of the
+ * largest v_scale among the blocks that the row sees, so that values whose
+ * scale is far below that lose bits; the sum of the weights does not.
+ * Statistics and sums are fp32.  A query that is
  * not finite makes its own row NaN.
  * The workspace (qr_kv_attention_workspace_bytes, 16-byte aligned) must be
  * zeroed once before its first use; every call leaves it ready for the next
