@@ -327,7 +327,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<DP, NT>::kCtas)
             // 2^-e in two factors, as e may pass the range of one; a negative
             // scale's sign goes into the query, so that the factor is not negative
             const float down1 = pow2i(-(e / 2)) * (a.scale < 0.0f ? -1.0f : 1.0f), down2 = pow2i(-(e - e / 2));
-            if (lane == 0) row_scale[rr] = fabsf(a.scale) * 1.4426950408889634f * pow2i(e / 2) * pow2i(e - e / 2);
+            // (of an infinite query all scores could be -inf, as if it saw
+            // nothing: its factor is NaN; one that is NaN has NaN products)
+            if (lane == 0)
+                row_scale[rr] = amax < INFINITY ? fabsf(a.scale) * 1.4426950408889634f * pow2i(e / 2) * pow2i(e - e / 2)
+                                                : __uint_as_float(0x7fffffffu);
 #pragma unroll
             for (int i = 0; i < kQFours; ++i) {
                 // dimension d = 64 c + 16 t + 4 j + w is element w of lane

@@ -477,7 +477,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     e -= 13;
                 }
                 const float down1 = pow2i(-(e / 2)) * (a.scale < 0.0f ? -1.0f : 1.0f), down2 = pow2i(-(e - e / 2));
-                row_scale = ldexpf(fabsf(a.scale) * 1.4426950408889634f, e);
+                // (NaN for an infinite query, as in qr_kv_split.cuh)
+                row_scale = amax < INFINITY ? ldexpf(fabsf(a.scale) * 1.4426950408889634f, e) : __uint_as_float(0x7fffffffu);
 #pragma unroll 2
                 for (int i = 0; i < DP / 8; ++i) {
                     float f[8];
@@ -597,7 +598,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // fused product's unrounded part would matter, nor for value
                     // scales so far apart that the exponent would leave fp32's range.
                     const bool apart = ve - tile.w > kScaleSpan || ve > kMostScaleExp;
-                    if (!mask && !__any_sync(~0u, !(fabsf(m) < 65536.0f) || apart)) {
+                    // (a row that is NaN does not count: it would change the others' bits)
+                    if (!mask && !__any_sync(~0u, fabsf(m) >= 65536.0f || apart)) {
                         const float lift = base + static_cast<float>(kTcWeightExp - ve);
                         float sums = 0.0f;
                         auto exponents = [&](uint32_t (&y)[16], const float4 &scales) {

@@ -704,8 +704,8 @@ qr_status_t qr_kv_append(qr_dtype_t dtype, int64_t tokens, const void *k, const 
  * fp16 numbers: off by up to 2^-22 of themselves, and by up to 2^-31 of the
  * largest v_scale among the blocks that the row sees, so that values whose
  * scale is far below that lose bits; the sum of the weights does not.
- * Statistics and sums are fp32.  A query that is
- * not finite makes its own row NaN.
+ * Statistics and sums are fp32.  A query that is not finite makes its own row
+ * NaN, if it sees a key, and no other.
  * The workspace (qr_kv_attention_workspace_bytes, 16-byte aligned) must be
  * zeroed once before its first use; every call leaves it ready for the next
  * one on the same stream. */
