@@ -20,9 +20,16 @@ struct KvAppendArgs {
     uint32_t inv;
 };
 
-// Four codes as the bytes of a word.  |x r| is at most 128 (1 + 2^-23), so only
-// the upper end can be left; adding 1.5 * 2^23 rounds half to even and leaves
-// the integer in the low bits.
+// 1 / s, or 0 where that is not a number of fp32: s is 0, or at most 2^-128, which
+// only bf16 magnitudes up to 2^-121 make it (codes of 0 are off by no more).
+__device__ __forceinline__ float inverse_scale(float s) {
+    const float r = __frcp_rn(s);
+    return r < INFINITY ? r : 0.0f;
+}
+
+// Four codes as the bytes of a word.  |x| is at most 128 s and r 1 / s rounded,
+// or 0, so |x r| is at most 128 (1 + 2^-23) and only the upper end can be left;
+// adding 1.5 * 2^23 rounds half to even and leaves the integer in the low bits.
 __device__ __forceinline__ uint32_t quantize4(const float *x, float r) {
     uint32_t u[4];
 #pragma unroll
@@ -41,7 +48,7 @@ __device__ __forceinline__ uint32_t quantize4(const float *x, float r) {
 // What bounds it: the bytes of a prompt (32 x 1024 tokens of 8 heads x 128:
 // 37 us, 5.4 TB/s of reads and writes, 0.81 of the copy rate); for single
 // tokens the launch and three dependent round trips, slot, block, codes (16
-// tokens 2.9 us, 256 tokens of 8 heads 3.8 us).
+// tokens 2.9 us, 256 tokens of 8 heads 4.2 us).
 constexpr int kPieces = 8;
 constexpr int kMarks = 2 * kAppendThreads;  // the window, and a block's length past it
 
@@ -162,7 +169,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(KvAppendAr
         for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
         amax = join(amax);
         const float s = fmaxf(old, __fmul_rn(amax, 0.0078125f));
-        const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+        const float r = inverse_scale(s);
         if (me == 0) *sp = s;
         if (o > 0 && s > old) {
             for (int i = me; i < o * a.dim / 16; i += lanes) {

@@ -619,7 +619,8 @@ qr_status_t qr_fp4_allreduce(qr_dtype_t dtype, int R, const void *const *x,
  * symmetric codec's at INT8 with the scale kept in fp32, never negative:
  *   A = max|x| over the tokens of the block that one call writes,
  *   s = max(s_old, A / 128)   (s_old = 0 when the call writes the block's
- *                              first token; exact), r = fp32_RN(1/s), 0 if s = 0,
+ *                              first token; exact), r = fp32_RN(1/s), 0 if s = 0
+ *                              or 1/s is beyond fp32 (A up to 2^-121),
  *   code = round_half_even(clip(fp32_RN(x*r), -128, 127)),
  *   and when s > s_old the codes already in the block become
  *   round_half_even(clip(fp32_RN(fp32_RN(code*s_old) * r), -128, 127)).
