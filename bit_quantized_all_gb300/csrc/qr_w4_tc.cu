@@ -423,10 +423,21 @@ cudaError_t launch_w4_tc(int dtype, const W4MatvecArgs &given, bool zeros, void 
         a.x_stride = a.l.chunks * 64;
         a.cols = a.l.chunks * 64;
     }
-    // up to 32 tokens half the columns: 32 tokens through 8192 x 8192 22 us, as
-    // half of a tile of 64 26 us
-    if (a.tokens <= 32) return dtype ? pick_group<1, 32>(a, zeros, s) : pick_group<0, 32>(a, zeros, s);
-    return dtype ? pick_group<1, 64>(a, zeros, s) : pick_group<0, 64>(a, zeros, s);
+    // a grid's second dimension, the tokens' tiles, ends at 65535: more tokens
+    // are more launches
+    constexpr long long kMost = 65535ll * 64;
+    for (long long done = 0; done < given.tokens; done += kMost) {
+        W4MatvecArgs part = a;
+        part.tokens = given.tokens - done < kMost ? given.tokens - done : kMost;
+        part.x += done * a.x_stride;
+        part.y += done * a.y_stride;
+        // up to 32 tokens half the columns: 32 tokens through 8192 x 8192 22 us, as
+        // half of a tile of 64 26 us
+        const cudaError_t err = part.tokens <= 32 ? (dtype ? pick_group<1, 32>(part, zeros, s) : pick_group<0, 32>(part, zeros, s))
+                                                  : (dtype ? pick_group<1, 64>(part, zeros, s) : pick_group<0, 64>(part, zeros, s));
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace qrk
