@@ -6,6 +6,10 @@ bits and a slice of the output projection in 4 bits.  A step plans its tokens'
 places once, and then every rank appends its keys and values, attends, and
 multiplies by its slice; the partial outputs are summed by ``qr_allreduce``.
 On one GPU the ranks are R sets of buffers, run in turn on one stream.
+
+A step reads its plan's counts back before it writes anything, so it waits once
+for the GPU and cannot be captured in a graph (the calls it makes can); requests
+only grow, and their blocks are not given back.
 """
 from __future__ import annotations
 
@@ -29,7 +33,7 @@ class TPAttentionLayer:
         self.free_blocks = torch.arange(blocks, dtype=torch.int32, device=device)
         self.cached = torch.zeros(requests, dtype=torch.int32, device=device)
         self.workspace, self.workspace_tokens = None, 0
-        self.counts = None  # of a step whose blocks are still on the free list
+        self.counts = None  # of a step whose blocks are still on the free list (on the host)
 
     def step(self, q: list[torch.Tensor], k: list[torch.Tensor], v: list[torch.Tensor], new_lens: torch.Tensor,
              max_q: int) -> torch.Tensor:
@@ -37,11 +41,20 @@ class TPAttentionLayer:
         tokens of each request (int32, on the device), from every rank's
         queries, keys and values ([tokens, heads, head_dim]); ``max_q`` bounds
         the new tokens of one request.  Blocks that the step before took and
-        that are still on the free list are dropped first (release_taken)."""
+        that are still on the free list are dropped first (release_taken).
+        Raises RuntimeError where the tokens do not fit the free blocks or the
+        table, ValueError where ``new_lens`` are not the queries' tokens; the
+        layer is then as it was, but for table entries past its requests' ends."""
         if self.counts is not None:
             self.release_taken()
         tokens = q[0].shape[0]
         plan = qr_kv_plan(self.cached, new_lens, self.block_table, self.free_blocks, self.block_size, tokens)
+        counts = plan.counts.cpu()
+        _, new, short, beyond = counts.tolist()
+        if short or beyond:
+            raise RuntimeError(f"the step needs {short} blocks and {beyond} table entries more than there are")
+        if new != tokens:
+            raise ValueError(f"new_lens bring {new} tokens, the queries are {tokens}")
         if tokens > self.workspace_tokens:
             self.workspace = qr_kv_attention_workspace(q[0], self.caches[0], new_lens.numel())
             self.workspace_tokens = tokens
@@ -53,12 +66,14 @@ class TPAttentionLayer:
             partial.append(qr_w4_matvec(out.view(tokens, -1), self.weights[rank]))
         y = qr_allreduce(self.bits, partial)
         self.cached = plan.kv_lens
-        self.counts = plan.counts
+        self.counts = counts
         return y
 
     def release_taken(self) -> None:
-        """Drops the blocks that the last step took from the free list.  It
-        reads their number back from the device, so it comes between steps."""
+        """Drops the blocks that the last step took from the free list; the
+        next step does it otherwise."""
+        if self.counts is None:
+            return
         taken, _, short, beyond = self.counts.tolist()
         if short or beyond:
             raise RuntimeError(f"the last step needed {short} blocks and {beyond} table entries more than there are")
