@@ -31,13 +31,13 @@
 // 12% where the products do (20 rows over 131075 keys 82 and 92 us).
 //
 // What bounds it: the codes from HBM when there is enough of them (128 single
-// tokens over up to 8192 keys, 8 heads: 186 us, 5.8 TB/s, 0.87 of the copy
+// tokens over up to 8192 keys, 8 heads: 188 us, 5.8 TB/s, 0.86 of the copy
 // rate); with more than eight rows an item latency, as two or three CTAs an SM
 // are all that the accumulators' registers leave, and each warp waits for its
 // own chain of copies, conversion, products and softmax (20 rows over 131075
-// keys: 92 us, 2.9 TB/s); and below some 20 us the chain of dependent round
+// keys: 93 us, 2.9 TB/s); and below some 20 us the chain of dependent round
 // trips: lengths, table, codes, parts, join (16 single tokens over up to 2048
-// keys, one head: 11.8 us).
+// keys, one head: 12.0 us).
 #pragma once
 
 #include <type_traits>

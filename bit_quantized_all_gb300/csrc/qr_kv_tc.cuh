@@ -27,7 +27,7 @@
 // which the products take 3072 and the softmax's and conversion's instructions
 // as many; a half's chain of scores, maximum, weights and their store leaves
 // gaps that the other half does not fill (8 prompt chunks of up to 1024 queries
-// over up to 8192 keys, 40 heads on 8, 128 dimensions: 409 us, 704 TFLOP/s).
+// over up to 8192 keys, 40 heads on 8, 128 dimensions: 410 us, 702 TFLOP/s).
 #pragma once
 
 #include "qr_kv_split.cuh"
@@ -39,7 +39,9 @@ constexpr int kTcRows = 256, kTcHalf = 128, kTcKeys = 128;
 constexpr int kTcThreads = 416;  // warps 0-7 softmax, 8-11 conversion, 12 products
 // An item's queries, output, masked tiles and empty pipeline take about as long
 // as this many tiles; the shares count them, as tiles before the first one (8
-// prompt chunks over up to 8192 keys: 3 436 us, 4 409, 5 414, 8 431).
+// prompt chunks over up to 8192 keys: 3 436 us, 4 409, 5 414, 8 431; 32 chunks
+// of 200 over up to 700 163, 163, 169, 170; 4 of 64 over 20000 120, 119, 121,
+// 121; a prompt of 2048 86, 88, 88, 92).
 constexpr int kItemSteps = 4;
 constexpr int kTcMostCtas = 160;
 constexpr float kSlack = 6.0f;

@@ -13,9 +13,10 @@
 // slices of the same rows and add their sums, in slice order, through
 // distributed shared memory: no workspace, no second launch.
 //
-// What bounds it: instruction issue in the conversion and the scaled sums (16
-// tokens through 8192 x 8192 with zero points 16.9 us, 2.1 TB/s of weights);
-// for one token through 8192 x 1024, 4.9 us, the launch and its round trips.
+// What bounds it: latency.  No unit is full (16 tokens through 8192 x 8192 with
+// zero points 16.9 us, 2.1 TB/s of weights: issue 44%, tensor pipe 22%, DRAM
+// 22%): a CTA has some 16 chunks between its first loads and its cluster's join.
+// For one token through 8192 x 1024, 4.8 us, the launch and its round trips.
 #include <cooperative_groups.h>
 
 #include "qr_launch.h"
@@ -270,9 +271,11 @@ template <int DT>
 static cudaError_t pick_tokens(const W4MatvecArgs &a, bool zeros, void *workspace, cudaStream_t s) {
     if (a.tokens <= 8) return pick_group<DT, 1, 1>(a, zeros, s);
     if (a.tokens <= kW4FewTokens) {
-        // two row tiles a warp read x half as often, one makes twice the CTAs:
-        // 16 tokens through 8192 x 8192 17.0 and 19.7 us, 12 through 300 x 9000
-        // 10.0 and 6.9
+        // two row tiles a warp read x half as often, one makes twice the CTAs.
+        // 16 tokens through 8192 columns, with two and with one: 64 row tiles
+        // 9.7 and 7.9 us, 96 10.2 and 9.8, 128 11.7 and 11.4, 152 13.1 and 12.8,
+        // 256 14.8 and 14.3, 512 15.7 and 22.0 (9 tokens 15.3 and 21.2): near 152
+        // either will do, below one is better, far above two
         if (a.l.row_tiles >= 152) return pick_group<DT, 2, 2>(a, zeros, s);
         return pick_group<DT, 1, 2>(a, zeros, s);
     }

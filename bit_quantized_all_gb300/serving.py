@@ -255,7 +255,7 @@ def qr_kv_attention_workspace(q: torch.Tensor, cache: KVCache, requests: int,
                               max_q: int | None = None) -> torch.Tensor:
     """A zeroed workspace for attention of queries shaped like ``q`` by up to
     ``requests`` requests; one serves every later call of at most these sizes
-    on one stream."""
+    on one stream, with any ``max_q`` (which need not be given)."""
     need = qr_kv_attention_workspace_bytes(requests, q.shape[0], q.shape[1], cache.heads, cache.head_dim)
     if need == 0:
         raise ValueError(f"unsupported attention shape: requests={requests} q={tuple(q.shape)} heads={cache.heads}")
@@ -269,8 +269,10 @@ def qr_kv_attention(q: torch.Tensor, cache: KVCache, q_offsets: torch.Tensor, kv
     """Attention of ragged fp16/bf16 queries ([tokens, q_heads, head_dim],
     request r's at ``q_offsets[r]:q_offsets[r+1]``) over the cache; ``scale``
     defaults to head_dim ** -0.5, ``max_q`` (a bound on the queries of one
-    request, which picks the kernel) to the number of tokens.  Returns ``out``, or
-    ``(out, lse)``.  Without ``workspace`` one is allocated and zeroed."""
+    request, which picks the kernel) to the number of tokens: a decode batch
+    that does not give it runs the kernel for prompts, right and slower.
+    Returns ``out``, or ``(out, lse)``.  Without ``workspace`` each call
+    allocates and zeroes one (up to 42 MB)."""
     if stream is not None:
         with _as_current(cache.device, stream):
             return qr_kv_attention(q, cache, q_offsets, kv_lens, block_table, scale, causal, window, max_q, out,

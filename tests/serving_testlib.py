@@ -13,6 +13,8 @@ attention  scores are fp32 sums of exact products: |dS| <= d :=
            + u_out |out| + the smallest subnormal of the type; weights below
            fp16's normal range lose at most 2^-25 of the row's largest each,
            i.e. 2^-25 * sum_i |v_i| / l with l >= 1 when scaled by the largest.
+           (The weights are held as two fp16 numbers, to 2^-22; test_gpu_kv_weights
+           has the bound for that, and inputs on which it tells.)
            |d lse| <= d + 2^-20 + 2^-22 |lse|.
 matvec     products are exact in fp32; a sum of K of them in any order of
            tensor-core steps errs by at most (K / 8 + 64) * 2^-23 * sum |x w|.
