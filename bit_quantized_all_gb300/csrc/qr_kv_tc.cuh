@@ -24,8 +24,8 @@
 // of their norm away from a product in 32 bits instead of 0.0001).
 //
 // What bounds it: latency.  A tile of both halves takes some 4500 cycles, of
-// which the products take 3072 and the softmax's and conversion's instructions
-// as many; a half's chain of scores, maximum, weights and their store leaves
+// which the products take two thirds and the softmax's and conversion's issue
+// about as many; a half's chain of scores, maximum, weights and their store leaves
 // gaps that the other half does not fill (8 prompt chunks of up to 1024 queries
 // over up to 8192 keys, 40 heads on 8, 128 dimensions: 410 us, 702 TFLOP/s).
 #pragma once
