@@ -771,3 +771,6 @@ def qr_fp4_allreduce(xs, y: torch.Tensor | None = None, stream=None, ctas: int =
 from .serving import (KVCache, KVPlan, W4Weight, qr_kv_append, qr_kv_attention,  # noqa: E402
                       qr_kv_attention_workspace, qr_kv_attention_workspace_bytes, qr_kv_plan, qr_w4_bytes,
                       qr_w4_matvec, qr_w4_matvec_workspace_bytes, qr_w4_pack, qr_w4_quantize)
+from .layer import (Q8Rows, Rope, W8Weight, qr_q8_quantize, qr_rms_norm, qr_rms_norm_q8, qr_rope,  # noqa: E402
+                    qr_w8_bytes, qr_w8_matmul, qr_w8_matmul_workspace, qr_w8_matmul_workspace_bytes, qr_w8_pack,
+                    qr_w8_quantize, rope_frequencies)

@@ -76,4 +76,68 @@ cudaError_t launch_w4_matvec(int dtype, long long tokens, const void *x, long lo
                              int group, bool has_zeros, const void *packed, void *y, long long y_stride,
                              void *workspace, cudaStream_t s);
 
+// ---- norm, positions and the 8-bit product (qr_layer_capi.cu)
+
+// The packed layout of 8-bit weights: tiles of 16 rows x 64 columns, row-major,
+// 1024 bytes of code + 128 each (128 past the rows and columns), then the
+// rows' fp32 scales (0 past the rows).
+struct W8Layout {
+    int row_tiles, chunks;
+    size_t scales_at, bytes;
+};
+
+inline W8Layout w8_layout(int rows, int cols) {
+    W8Layout l;
+    l.row_tiles = rows / 16 + (rows % 16 != 0);
+    l.chunks = cols / 64 + (cols % 64 != 0);
+    l.scales_at = size_t(l.row_tiles) * size_t(l.chunks) * 1024;
+    l.bytes = l.scales_at + size_t(l.row_tiles) * 64;
+    return l;
+}
+
+// Up to so many tokens the 8-bit product needs no workspace.
+constexpr int kW8FewTokens = 16;
+
+struct NormArgs {
+    const void *x, *residual, *weight;
+    void *residual_out, *y;  // y: 16-bit values, or int8 codes where scales is set
+    float *scales;
+    long long x_row, residual_row, residual_out_row, y_row;  // strides in values
+    long long tokens;
+    int cols;
+    float eps;
+};
+
+struct RopeArgs {
+    const uint16_t *in[2];  // queries, keys
+    uint16_t *out[2];
+    long long in_token[2], in_head[2], out_token[2], out_head[2];  // strides in values
+    int heads[2];
+    const unsigned long long *turns;
+    const int32_t *positions, *q_offsets, *kv_lens;
+    float factor;
+    long long tokens;
+    int requests, head_dim, rot;
+};
+
+struct W8Args {
+    const int8_t *x;
+    const float *x_scales;
+    const uint8_t *packed;
+    uint16_t *y;
+    long long x_stride, y_stride, tokens;
+    int rows, cols;
+    W8Layout l;
+};
+
+// weight: 0 none (rows in 8 bits without a norm), 1 in x's type, 2 in fp32
+cudaError_t launch_norm(int dtype, int weight, const NormArgs &a, cudaStream_t s);
+cudaError_t launch_rope(int dtype, bool interleaved, const RopeArgs &a, cudaStream_t s);
+cudaError_t launch_w8_pack(int rows, int cols, const int8_t *codes, long long stride, const float *scales, void *packed,
+                           cudaStream_t s);
+cudaError_t launch_w8_quantize(int dtype, int rows, int cols, const void *w, long long stride, void *packed,
+                               cudaStream_t s);
+size_t w8_workspace(long long tokens, int cols);
+cudaError_t launch_w8_matmul(int dtype, const W8Args &a, void *workspace, cudaStream_t s);
+
 }  // namespace qrk

@@ -12,44 +12,15 @@
 #include <climits>
 
 #include "qr_serving.h"
-
-#define QR_EXPORT extern "C" __attribute__((visibility("default")))
+#include "qr_serving_checks.h"
 
 namespace {
 
-constexpr int64_t kMostValues = int64_t(1) << 46;  // bound on any offset in values, far from overflow
-
-bool dtype_ok(qr_dtype_t d) { return d == QR_FP16 || d == QR_BF16; }
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-qr_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? QR_OK : QR_ERR_CUDA; }
+using namespace qrk;
 
 bool block_size_ok(int b) { return b == 16 || b == 32 || b == 64 || b == 128 || b == 256; }
 bool head_dim_ok(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
 bool group_ok(int g) { return g == 32 || g == 64 || g == 128; }
-
-// A [tokens][heads][dim] operand with strides in values: bytes from its
-// first value past its last one, 0 if a stride is out of range.
-size_t extent(int64_t tokens, int heads, int dim, int64_t token_stride, int64_t head_stride) {
-    if (heads > 1 && (head_stride < dim || head_stride > kMostValues / heads)) return 0;
-    if (tokens > 1 && (token_stride < dim || token_stride > kMostValues / tokens)) return 0;
-    const int64_t values = (tokens - 1) * (tokens > 1 ? token_stride : 0) + (heads - 1) * (heads > 1 ? head_stride : 0) + dim;
-    return size_t(values) * 2;
-}
-
-// rows (one per token and head) must not share values with one another
-bool rows_apart(int64_t tokens, int heads, int dim, int64_t token_stride, int64_t head_stride) {
-    if (tokens <= 1 || heads <= 1) return true;
-    return token_stride >= (heads - 1) * head_stride + dim || head_stride >= (tokens - 1) * token_stride + dim;
-}
-
-struct Half {
-    const void *codes;
-    size_t bytes;
-};
 
 // Checks of the cache that need no call-specific operand; QR_OK or the error.
 qr_status_t check_cache(const qr_kv_cache_t *c) {

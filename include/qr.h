@@ -78,7 +78,8 @@
  *     self-tests are launched plainly.)
  *   - Failure of a device-side wait: the staged kernels, the flag-joined
  *     two-shot and the kernels that wait for their tensor-core products
- *     (qr_kv_attention above 32 query rows, qr_w4_matvec above 16 tokens)
+ *     (qr_kv_attention above 32 query rows, qr_w4_matvec and qr_w8_matmul
+ *     above 16 tokens)
  *     bound every wait (one second).  A wait that runs out (which
  *     a correct launch never does) makes the kernel stop early and count
  *     one timeout; the call has already returned QR_OK, because it returns
@@ -750,6 +751,99 @@ qr_status_t qr_w4_matvec(qr_dtype_t dtype, int64_t tokens, const void *x, int64_
                          int rows, int cols, int group, int has_zeros, const void *packed,
                          void *y, int64_t y_row_stride, void *workspace, size_t workspace_bytes,
                          qr_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * What stands between the all-reduced message and the attention of the next
+ * layer: norm, projection and positions.  fp16/bf16 values; row, token and
+ * head strides in values; 2-byte alignment unless stated.
+ *
+ * Rows in 8 bits.  A row v of fp32 values becomes int8 codes and one fp32
+ * scale:  A = max|v|,  f = fp32_RN(127 / A), 0 where that is not finite,
+ *   code = round_half_even(fp32_RN(v * f)),  scale = fp32_RN(A / 127),
+ * so that codes are -127..127 and v is near code * scale.  Rows of codes are
+ * 16-byte aligned (pointer, and stride where there are several rows); of a
+ * row only its `cols` bytes are read or written.  A row that holds a value
+ * that is not finite has a scale that is not finite or NaN, unspecified
+ * codes, and touches no other row.
+ * ------------------------------------------------------------------------- */
+
+/* Rows of x (row stride >= cols) in 8 bits: codes [tokens][cols] at
+ * codes_row_stride, scales [tokens].  No output may overlap x or the other. */
+qr_status_t qr_q8_quantize(qr_dtype_t dtype, int64_t tokens, int cols, const void *x,
+                           int64_t x_row_stride, int8_t *codes, int64_t codes_row_stride,
+                           float *scales, qr_stream_t stream);
+
+/* Root-mean-square norm of each row, with the residual's addition:
+ *   h = x + residual (fp32; x where residual is NULL),
+ *   residual_out = h rounded (may be NULL; must be where residual is),
+ *   rs = 1 / sqrt(mean(h^2) + eps)   (eps finite and above 0),
+ *   y = h * rs * weight, in fp32 from the sum h that is not rounded, rounded
+ *   once.  weight [cols]: x's type, or fp32 (weight_fp32 != 0).
+ * Squares are summed in fp32: a row whose sum is beyond fp32 gives rs = 0.
+ * residual_out and y may each equal x or residual exactly (same pointer and
+ * stride); any other overlap of an output is refused. */
+qr_status_t qr_rms_norm(qr_dtype_t dtype, int64_t tokens, int cols, const void *x,
+                        int64_t x_row_stride, const void *residual, int64_t residual_row_stride,
+                        void *residual_out, int64_t residual_out_row_stride, const void *weight,
+                        int weight_fp32, float eps, void *y, int64_t y_row_stride,
+                        qr_stream_t stream);
+
+/* The norm with its output in 8 bits: rows v = fp32_RN(h * weight) in 8 bits,
+ * the norm's factor in the scale:  scale = fp32_RN(A / 127) * rs.  The codes
+ * do not depend on rs, so that no order of the sum of squares changes them. */
+qr_status_t qr_rms_norm_q8(qr_dtype_t dtype, int64_t tokens, int cols, const void *x,
+                           int64_t x_row_stride, const void *residual,
+                           int64_t residual_row_stride, void *residual_out,
+                           int64_t residual_out_row_stride, const void *weight, int weight_fp32,
+                           float eps, int8_t *codes, int64_t codes_row_stride, float *scales,
+                           qr_stream_t stream);
+
+/* 8-bit weights [rows][cols] with an fp32 scale for each row (output
+ * channel): qr_w8_pack lays int8 codes (-128..127, row-major at
+ * codes_row_stride >= cols, any alignment) and scales [rows] out for
+ * qr_w8_matmul; qr_w8_quantize does so from fp16/bf16 weights, a row in 8 bits
+ * as above (finite weights).  The packed buffer (qr_w8_bytes, 16-byte
+ * aligned) is read by qr_w8_matmul only. */
+size_t qr_w8_bytes(int rows, int cols); /* 0 if unsupported */
+qr_status_t qr_w8_pack(int rows, int cols, const int8_t *codes, int64_t codes_row_stride,
+                       const float *scales, void *packed, qr_stream_t stream);
+qr_status_t qr_w8_quantize(qr_dtype_t dtype, int rows, int cols, const void *w,
+                           int64_t w_row_stride, void *packed, qr_stream_t stream);
+
+/* y[t][n] = (sum_k x[t][k] w[n][k]) * x_scale[t] * w_scale[n], rounded once to
+ * `dtype`: x rows in 8 bits (any codes -128..127) and 8-bit weights.  The
+ * products are integers summed in fp32: no sum is rounded as long as
+ * sum_k |x w| stays below 2^24.  Above 16 tokens the workspace
+ * (qr_w8_matmul_workspace_bytes, 16-byte aligned) is written and read; up to
+ * 16 it may be NULL.  y: any row stride >= rows, 2-byte aligned. */
+size_t qr_w8_matmul_workspace_bytes(int64_t tokens, int cols); /* 0 if unsupported */
+qr_status_t qr_w8_matmul(qr_dtype_t dtype, int64_t tokens, const int8_t *x, int64_t x_row_stride,
+                         const float *x_scales, int rows, int cols, const void *packed, void *y,
+                         int64_t y_row_stride, void *workspace, size_t workspace_bytes,
+                         qr_stream_t stream);
+
+/* Rotary positions of queries and keys ([tokens][heads][head_dim]; k may be
+ * NULL with k_heads = 0).  Pair j < rot_dim / 2 of a head, (a, b), the values
+ * (j, j + rot_dim / 2), or with `interleaved` (2j, 2j + 1), becomes
+ *   (a c - b s, b c + a s),  c = factor * cos(angle),  s = factor * sin(angle),
+ *   angle = 2 pi * position * turns[j] / 2^64,
+ * in fp32, rounded once; turns[j] (device) is the pair's frequency in turns a
+ * position times 2^64, so that the product, which wraps at whole turns, keeps
+ * every bit at any position.  Values from rot_dim on are copied.  head_dim
+ * and rot_dim even, 2 <= rot_dim <= head_dim <= 1024.
+ * Positions are positions[token] (device int32, any sign) or, where that is
+ * NULL, those of a step's plan: token t of request r (q_offsets[r] <= t <
+ * q_offsets[r + 1]) stands at kv_lens[r] - (q_offsets[r + 1] - t), and tokens
+ * past q_offsets[requests] are left alone.  q_out and k_out may equal q and k
+ * exactly (in place; same strides); any other overlap of an output is
+ * refused. */
+qr_status_t qr_rope(qr_dtype_t dtype, int64_t tokens, int head_dim, int rot_dim, int interleaved,
+                    const uint64_t *turns, float factor, const int32_t *positions, int requests,
+                    const int32_t *q_offsets, const int32_t *kv_lens, const void *q,
+                    int64_t q_token_stride, int64_t q_head_stride, int q_heads, void *q_out,
+                    int64_t q_out_token_stride, int64_t q_out_head_stride, const void *k,
+                    int64_t k_token_stride, int64_t k_head_stride, int k_heads, void *k_out,
+                    int64_t k_out_token_stride, int64_t k_out_head_stride, qr_stream_t stream);
 
 /* A static string naming a status code (never NULL). */
 const char *qr_status_string(qr_status_t status);
