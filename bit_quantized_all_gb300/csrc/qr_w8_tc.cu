@@ -5,32 +5,34 @@
 // exact fp16 numbers, their products exact in fp32.  A first kernel writes x's
 // codes as fp16 into the workspace, in the order and with the swizzle that the
 // products read from shared memory, so that a chunk of 64 columns of a CTA's
-// tokens is one bulk copy.  Then y^T = W x^T, a CTA taking 128 weight rows by N
-// tokens over one slice of the columns: eight warps, a row tile each, turn packed
-// codes into fp16 and store them as the A operand in tensor memory; one warp
-// brings x; one warp issues the products; then the eight warps scale and store.
-// The CTAs of a cluster add their slices' sums, in order, through distributed
-// shared memory.
+// tokens is one bulk copy.  Then y^T = W x^T in tiles of 128 weight rows by N
+// tokens: eight warps, a row tile of 16 each, turn packed codes into fp16 and store
+// them as the A operand in tensor memory, one warp brings x, one issues the
+// products, and four scale and store a finished tile while the next one runs.
+//
+// The chunks of all tiles, one tile after the other, are divided evenly among
+// the CTAs, one an SM.  A tile that one CTA has whole is stored by it; the parts
+// of the others go to the workspace as fp32 sums, and a last kernel adds them in
+// order, so that the result has the same bits every time.
 //
 // A lane's 16 codes of a tile's row are consecutive columns; as fragments of the
 // store to tensor memory they stand at the columns 16 j + 4 t + 0..3, so x is
 // written into the workspace with its columns exchanged alike.
-#include <cooperative_groups.h>
-
 #include "qr_launch.h"
 #include "qr_tcgen05.cuh"
 #include "qr_w8.cuh"
 
 namespace qrk {
 
-namespace cg = cooperative_groups;
-
 constexpr int kWeThreads = 256;
 
 // x's codes as fp16: a block of N tokens x 64 columns is N * 128 bytes, swizzled.
 // A thread takes 32 codes, half of a token's part of a chunk: pieces j, j + 2, ...
 __global__ void __launch_bounds__(kWeThreads) w8_expand_kernel(W8Args a, uint8_t *to, int n_shift) {
-    chain_entry();
+    // the product may start once everything before this kernel is complete: until
+    // its own wait it reads the weights only
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int n = 1 << n_shift, chunks = a.l.chunks;
     // eight tokens of two chunks a warp
     const long long token = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 1 & 7);
@@ -53,37 +55,76 @@ __global__ void __launch_bounds__(kWeThreads) w8_expand_kernel(W8Args a, uint8_t
     }
 }
 
-constexpr int kWtThreads = 320;  // warps 0-7 codes and results, 8 products, 9 x
+constexpr int kWtThreads = 448;  // warps 0-7 codes, 8 products, 9 x, 10-13 results
 constexpr int kWtRows = 128;
 constexpr int kWtStep = 4, kWtA = 2;  // chunks of a step, and buffers of codes in tensor memory, a step each
 constexpr uint32_t kWtColD = kWtA * 32 * kWtStep, kWtColumns = 512;
+constexpr int kWtMostCtas = 152;  // the workspace has two parts for each
 
 template <int N>
 struct WtSmem {
     static constexpr int kBlock = N * 128;
     static constexpr int kX = N >= 256 ? 6 : N >= 128 ? 12 : 16;  // chunks of x
-    static constexpr int kPitch = kWtRows + 4;
-    static_assert(N * kPitch * 4 <= kX * kBlock, "the sums fit where x was");
-    uint8_t x[kX * kBlock];  // then the sums
-    uint64_t a_full[kWtA], a_done[kWtA], x_full[kX], x_done[kX], d_full;
-    float x_scale[N];
+    static constexpr int kD = N >= 256 ? 1 : 2;                   // accumulators
+    uint8_t x[kX * kBlock];
+    uint8_t out[4][32 * 80];  // by warp: 32 tokens of 32 rows
+    float x_scale[4][N];      // by warp
+    uint64_t a_full[kWtA], a_done[kWtA], x_full[kX], x_done[kX], d_full[kD], d_done[kD];
     uint32_t tmem;
     int fail;
 };
 
+// The division of the chunks: all = tiles * chunks of them over `ctas`.
+struct W8Shares {
+    long long all;
+    int chunks, row_ctas, ctas;
+
+    __host__ __device__ __forceinline__ long long begin(long long cta) const { return all * cta / ctas; }
+    // the CTA that has chunk `u`
+    __device__ __forceinline__ int owner(long long u) const { return static_cast<int>(((u + 1) * ctas - 1) / all); }
+};
+
+// Walks a CTA's chunks, a step of up to kWtStep chunks of one tile at a time.
+struct W8Walk {
+    long long left;
+    int chunk, chunks, row_tile, row_ctas;
+    long long token_tile;
+
+    __device__ __forceinline__ W8Walk(const W8Shares &s, int cta) {
+        const long long u = s.begin(cta), tile = u / s.chunks;
+        left = s.begin(cta + 1) - u;
+        chunk = static_cast<int>(u - tile * s.chunks);
+        chunks = s.chunks;
+        row_ctas = s.row_ctas;
+        token_tile = tile / row_ctas;
+        row_tile = static_cast<int>(tile - token_tile * row_ctas);
+    }
+    __device__ __forceinline__ int step() const {
+        return static_cast<int>(min(static_cast<long long>(min(kWtStep, chunks - chunk)), left));
+    }
+    // Chunks of this tile that are the CTA's, from here on.
+    __device__ __forceinline__ int segment() const {
+        return static_cast<int>(min(static_cast<long long>(chunks - chunk), left));
+    }
+    __device__ __forceinline__ void advance(int n) {
+        left -= n;
+        chunk += n;
+        if (chunk == chunks) {
+            chunk = 0;
+            if (++row_tile == row_ctas) row_tile = 0, ++token_tile;
+        }
+    }
+};
+
 template <int DT, int N>
-__global__ void __launch_bounds__(kWtThreads, 1) w8_tc_kernel(W8Args a, const uint8_t *x16, int slice, unsigned *timeouts) {
+__global__ void __launch_bounds__(kWtThreads, 1)
+    w8_tc_kernel(W8Args a, W8Shares shares, const uint8_t *x16, float *parts, unsigned *timeouts) {
     using S = WtSmem<N>;
     extern __shared__ uint8_t raw[];
     S &sm = *reinterpret_cast<S *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
-    cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int splits = static_cast<int>(cluster.num_blocks()), split = static_cast<int>(cluster.block_rank());
-    const int first = split * slice, count = max(0, min(slice, a.l.chunks - first));
-    const long long token0 = static_cast<long long>(blockIdx.y) * N;
-    const int tokens = static_cast<int>(min(static_cast<long long>(N), a.tokens - token0));
-    const int tile0 = blockIdx.x / splits * (kWtRows / 16);
     int *const fail = &sm.fail;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
         for (int i = 0; i < kWtA; ++i) {
             mbar_init(&sm.a_full[i], 8);
@@ -93,43 +134,48 @@ __global__ void __launch_bounds__(kWtThreads, 1) w8_tc_kernel(W8Args a, const ui
             mbar_init(&sm.x_full[i], 1);
             mbar_init(&sm.x_done[i], 1);
         }
-        mbar_init(&sm.d_full, 1);
+        for (int i = 0; i < S::kD; ++i) {
+            mbar_init(&sm.d_full[i], 1);
+            mbar_init(&sm.d_done[i], 4);
+        }
         mbar_init_fence();
         sm.fail = 0;
     }
     if (warp == 8) tc_alloc(&sm.tmem, kWtColumns);
-    chain_entry();
-    for (int i = tid; i < tokens; i += kWtThreads) sm.x_scale[i] = a.x_scales[token0 + i];
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    const int steps = (count + kWtStep - 1) / kWtStep;
     const int quarter = warp & 3;  // of tensor memory's lanes, that this warp reaches
+    W8Walk at(shares, blockIdx.x);
 
     if (warp < 8) {
         // ---- codes: a row tile of 16, two steps of them on their way in registers
-        const long long tile = min(tile0 + 2 * quarter + (warp >> 2), a.l.row_tiles - 1);
-        const uint4 *const src = reinterpret_cast<const uint4 *>(a.packed) + (tile * a.l.chunks + first) * 64 + lane;
+        W8Walk ahead = at;
+        const int mine = 2 * quarter + (warp >> 2);
         uint4 w[2][kWtStep][2];
-        auto fetch = [&](int b, int p) {
+        auto fetch = [&](int b) {
+            if (ahead.left <= 0) return;
+            const int n = ahead.step();
+            const long long tile = min(ahead.row_tile * (kWtRows / 16) + mine, a.l.row_tiles - 1);
+            const uint4 *const src = reinterpret_cast<const uint4 *>(a.packed) + (tile * a.l.chunks + ahead.chunk) * 64 + lane;
 #pragma unroll
             for (int u = 0; u < kWtStep; ++u)
-                if (kWtStep * p + u < count) {
-                    w[b][u][0] = __ldg(src + (kWtStep * p + u) * 64);
-                    w[b][u][1] = __ldg(src + (kWtStep * p + u) * 64 + 32);
+                if (u < n) {
+                    w[b][u][0] = __ldg(src + u * 64);
+                    w[b][u][1] = __ldg(src + u * 64 + 32);
                 }
+            ahead.advance(n);
         };
-        fetch(0, 0);
-        fetch(1, 1);
+        fetch(0);
+        fetch(1);
         const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32 + (warp >> 2) * 16) << 16);
         bool ok = true;
-        for (int p0 = 0; p0 < steps && ok; p0 += 2) {
+        for (int round = 0; at.left > 0 && ok; ++round) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int p = p0 + b;
-                if (p >= steps) break;
-                if (p >= kWtA) ok = tc_wait_warp(&sm.a_done[b], (p / kWtA - 1) & 1, fail, timeouts);
+                if (at.left <= 0) break;
+                if (round > 0) ok = tc_wait_warp(&sm.a_done[b], (round - 1) & 1, fail, timeouts);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -142,13 +188,14 @@ __global__ void __launch_bounds__(kWtThreads, 1) w8_tc_kernel(W8Args a, const ui
                         weights_f16(up[j], v[4 * j], v[4 * j + 1]);
                         weights_f16(low[j], v[4 * j + 2], v[4 * j + 3]);
                     }
-                    tc_st_fragments(to + b * (32 * kWtStep) + u * 32, v);  // (past the last chunk: unused)
+                    tc_st_fragments(to + b * (32 * kWtStep) + u * 32, v);  // (past the step's last chunk: unused)
                 }
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.a_full[b]);
-                fetch(b, p + 2);
+                at.advance(at.step());
+                fetch(b);
             }
         }
     } else if (warp == 8) {
@@ -156,150 +203,230 @@ __global__ void __launch_bounds__(kWtThreads, 1) w8_tc_kernel(W8Args a, const ui
         const bool leader = elect_lane();
         constexpr uint32_t kDesc = mma_desc(N, false);
         bool ok = true;
-        for (int p = 0; p < steps && ok; ++p) {
-            const int s = p % kWtA, chunks = min(kWtStep, count - kWtStep * p);
-            ok = tc_wait_warp(&sm.a_full[s], (p / kWtA) & 1, fail, timeouts);
-            for (int u = 0; u < chunks && ok; ++u) {
-                const int i = kWtStep * p + u, xs = i % S::kX;
-                ok = tc_wait_warp(&sm.x_full[xs], (i / S::kX) & 1, fail, timeouts);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t x = smem_addr(sm.x) + xs * S::kBlock, codes = tmem + s * (32 * kWtStep) + u * 32;
+        unsigned p = 0, i = 0;
+        for (unsigned g = 0; at.left > 0 && ok; ++g) {
+            const unsigned d = g % S::kD;
+            int n = at.segment();
+            if (g >= S::kD) ok = tc_wait_warp(&sm.d_done[d], (g / S::kD - 1) & 1, fail, timeouts);
+            bool add = false;
+            while (n > 0 && ok) {
+                const int s = p % kWtA, chunks = at.step();
+                ok = tc_wait_warp(&sm.a_full[s], (p / kWtA) & 1, fail, timeouts);
+                for (int u = 0; u < chunks && ok; ++u, ++i) {
+                    const int xs = i % S::kX;
+                    ok = tc_wait_warp(&sm.x_full[xs], (i / S::kX) & 1, fail, timeouts);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t x = smem_addr(sm.x) + xs * S::kBlock, codes = tmem + s * (32 * kWtStep) + u * 32;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    tc_mma_ts(leader, tmem + kWtColD, codes + j * 8, smem_desc(x + j * 32, 16, 1024), kDesc, i + j > 0);
-                tc_commit(leader, &sm.x_done[xs]);
+                    for (int j = 0; j < 4; ++j)
+                        tc_mma_ts(leader, tmem + kWtColD + d * N, codes + j * 8, smem_desc(x + j * 32, 16, 1024), kDesc,
+                                  add || j > 0);
+                    add = true;
+                    tc_commit(leader, &sm.x_done[xs]);
+                }
+                if (!ok) break;
+                tc_commit(leader, &sm.a_done[s]);
+                ++p;
+                n -= chunks;
+                at.advance(chunks);
             }
-            if (ok) tc_commit(leader, &sm.a_done[s]);
+            tc_commit(leader, &sm.d_full[d]);
+            // (after a wait that ran out: nothing is under way when tensor memory is freed)
+            if (!ok) mbar_wait(&sm.d_full[d], (g / S::kD) & 1);
         }
-        tc_commit(leader, &sm.d_full);
-    } else if (lane == 0) {
+    } else if (warp == 9) {
         // ---- x: a chunk's block is one copy
-        const uint8_t *const src = x16 + (blockIdx.y * static_cast<long long>(a.l.chunks) + first) * S::kBlock;
-        bool ok = true;
-        int i = 0;
-        for (; i < count; ++i) {
-            const int xs = i % S::kX;
-            if (i >= S::kX) ok = tc_wait(&sm.x_done[xs], (i / S::kX - 1) & 1, fail, timeouts);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&sm.x_full[xs], S::kBlock);
-            bulk_copy_g2s(sm.x + xs * S::kBlock, src + static_cast<long long>(i) * S::kBlock, S::kBlock, &sm.x_full[xs]);
+        if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            unsigned i = 0;
+            for (; at.left > 0; ++i) {
+                const int xs = i % S::kX;
+                if (i >= S::kX && !tc_wait(&sm.x_done[xs], (i / S::kX - 1) & 1, fail, timeouts)) break;
+                mbar_arrive_expect_tx(&sm.x_full[xs], S::kBlock);
+                bulk_copy_g2s(sm.x + xs * S::kBlock, x16 + (at.token_tile * at.chunks + at.chunk) * S::kBlock, S::kBlock,
+                              &sm.x_full[xs]);
+                at.advance(1);
+            }
+            // none of the copies is on its way when the CTA leaves
+            for (unsigned k = i < S::kX ? 0 : i - S::kX; k < i; ++k) mbar_wait(&sm.x_full[k % S::kX], (k / S::kX) & 1);
         }
-        // none of the copies is on its way when the CTA leaves
-        for (int k = max(0, i - S::kX); k < i; ++k) mbar_wait(&sm.x_full[k % S::kX], (k / S::kX) & 1);
+        __syncwarp();
+    } else {
+        // ---- results: a thread per row
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int mine = warp - 10;
+        uint8_t *const stage = sm.out[mine];
+        float *const x_scale = sm.x_scale[mine];
+        const bool vector = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.y_stride % 8 == 0;
+        long long held = -1;  // the tokens whose scales are in shared memory
+        bool ok = true;
+        for (unsigned g = 0; at.left > 0; ++g) {
+            const unsigned d = g % S::kD;
+            const int n = at.segment();
+            const bool whole = n == at.chunks;
+            const long long token0 = at.token_tile * N, row0 = static_cast<long long>(at.row_tile) * kWtRows + quarter * 32;
+            const int tokens = static_cast<int>(min(static_cast<long long>(N), a.tokens - token0));
+            if (whole && held != at.token_tile) {
+                held = at.token_tile;
+                __syncwarp();
+                for (int m = lane; m < N; m += 32) x_scale[m] = m < tokens ? a.x_scales[token0 + m] : 0.0f;
+                __syncwarp();
+            }
+            const float scale = row0 + lane < a.rows ? reinterpret_cast<const float *>(a.packed + a.l.scales_at)[row0 + lane] : 0.0f;
+            float *const part = parts + (2ll * blockIdx.x + (at.chunk == 0)) * (kWtRows * N) + quarter * 32 + lane;
+            ok = tc_wait_warp(&sm.d_full[d], (g / S::kD) & 1, fail, timeouts);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kWtColD + d * N;
+#pragma unroll 1
+            for (int h = 0; h < N / 32; ++h) {
+                uint32_t v[32];
+                tc_ld32(lanes + h * 32, v);
+                tc_wait_ld(v);
+                if (h == N / 32 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.d_done[d]);
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) part[(h * 32 + e) * kWtRows] = __uint_as_float(v[e]);
+                    continue;
+                }
+                if (h * 32 >= tokens) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    *reinterpret_cast<uint16_t *>(stage + e * 80 + lane * 2) =
+                        narrow1<DT>(__uint_as_float(v[e]) * x_scale[h * 32 + e] * scale);
+                __syncwarp();
+                if (vector && row0 + 32 <= a.rows) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int m = e * 8 + (lane >> 2);
+                        const uint4 o = *reinterpret_cast<const uint4 *>(stage + m * 80 + (lane & 3) * 16);
+                        if (h * 32 + m < tokens)
+                            *reinterpret_cast<uint4 *>(a.y + (token0 + h * 32 + m) * a.y_stride + row0 + (lane & 3) * 8) = o;
+                    }
+                } else if (row0 + lane < a.rows) {
+                    for (int m = 0; m < 32 && h * 32 + m < tokens; ++m)
+                        a.y[(token0 + h * 32 + m) * a.y_stride + row0 + lane] =
+                            *reinterpret_cast<const uint16_t *>(stage + m * 80 + lane * 2);
+                }
+                __syncwarp();
+            }
+            at.advance(n);
+        }
     }
     __syncwarp();
-
-    // the slice's sums as [token][row], then every CTA of the cluster adds the
-    // slices, in order, for its share of them
-    const bool done = tc_wait_warp(&sm.d_full, 0, fail, timeouts);
-    tc_fence_after();
-    __syncthreads();  // (x's buffers are free)
-    float *const sums = reinterpret_cast<float *>(sm.x);
-    if (warp < 8) {
-        constexpr int kMine = N / 2;
-        const int from = (warp >> 2) * kMine;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kWtColD + from;
-#pragma unroll
-        for (int h = 0; h < kMine / 16; ++h) {
-            uint32_t v[16];
-            tc_ld16(lanes + h * 16, v);
-            tc_wait_ld(v);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                sums[(from + h * 16 + e) * S::kPitch + quarter * 32 + lane] = count > 0 && done ? __uint_as_float(v[e]) : 0.0f;
-        }
-    }
     tc_fence_before();
     __syncthreads();
     if (warp == 8) tc_free(tmem, kWtColumns);
-    if (splits > 1) cluster.sync();
-    const long long row0 = tile0 * 16ll;
-    const int mine0 = tokens * kWtRows * split / splits, mine1 = tokens * kWtRows * (split + 1) / splits;
-    const float *const scales = reinterpret_cast<const float *>(a.packed + a.l.scales_at) + row0;
-    for (int i = mine0 + tid; i < mine1; i += kWtThreads) {
-        const int m = i / kWtRows, row = i % kWtRows;
-        float v = 0.0f;
-        if (splits > 1)
-            for (int c = 0; c < splits; ++c) v += cluster.map_shared_rank(sums, c)[m * S::kPitch + row];
-        else
-            v = sums[m * S::kPitch + row];
-        if (row0 + row < a.rows) a.y[(token0 + m) * a.y_stride + row0 + row] = narrow1<DT>(v * sm.x_scale[m] * scales[row]);
+    // (a kernel is complete for the next one only when all of its threads have
+    // waited for the one before, or left)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Adds the parts of the tiles that several CTAs share: block x is the tile in
+// which CTA x's share ends, y a group of 32 tokens of it.
+template <int DT>
+__global__ void __launch_bounds__(256) w8_join_kernel(W8Args a, W8Shares shares, const float *parts, int n) {
+    chain_entry();
+    const long long end = shares.begin(blockIdx.x + 1), tile = (end - 1) / shares.chunks;
+    const long long from = tile * shares.chunks, to = from + shares.chunks;
+    if (end == to || shares.owner(from) != static_cast<int>(blockIdx.x)) return;  // whole, or another's to add
+    const int last = shares.owner(to - 1);
+    const long long token0 = tile / shares.row_ctas * n + blockIdx.y * 32;
+    const long long row = tile % shares.row_ctas * kWtRows + (threadIdx.x & 31) * 4;
+    if (token0 >= a.tokens || row >= a.rows) return;
+    const int col = blockIdx.y * 32 + (threadIdx.x >> 5);  // and every eighth from there
+    float4 sum[4];
+#pragma unroll 2
+    for (int c = blockIdx.x; c <= last; ++c) {
+        const float4 *const p = reinterpret_cast<const float4 *>(parts + (2ll * c + (c == blockIdx.x)) * (kWtRows * n)) +
+                                col * (kWtRows / 4) + (threadIdx.x & 31);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = __ldcg(p + k * 8 * (kWtRows / 4));
+            if (c == blockIdx.x)
+                sum[k] = v;
+            else
+                sum[k].x += v.x, sum[k].y += v.y, sum[k].z += v.z, sum[k].w += v.w;
+        }
     }
-    if (splits > 1) cluster.sync();  // no CTA leaves while another reads its sums
+    const float *const scales = reinterpret_cast<const float *>(a.packed + a.l.scales_at) + row;
+    const float4 scale = *reinterpret_cast<const float4 *>(scales);
+    const bool vector = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0 && a.y_stride % 4 == 0 && row + 4 <= a.rows;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const long long token = token0 + (threadIdx.x >> 5) + 8 * k;
+        if (token >= a.tokens) break;
+        const float s = a.x_scales[token];
+        const float y[4] = {sum[k].x * s * scale.x, sum[k].y * s * scale.y, sum[k].z * s * scale.z, sum[k].w * s * scale.w};
+        uint16_t *const to_y = a.y + token * a.y_stride + row;
+        if (vector)
+            *reinterpret_cast<uint2 *>(to_y) = make_uint2(narrow2<DT>(y[0], y[1]), narrow2<DT>(y[2], y[3]));
+        else
+            for (int e = 0; e < 4 && row + e < a.rows; ++e) to_y[e] = narrow1<DT>(y[e]);
+    }
+}
+
+// Tokens of a tile: the fewest that take them all, 256 at most.
+static int w8_token_shift(long long tokens) { return tokens <= 32 ? 5 : tokens <= 64 ? 6 : tokens <= 128 ? 7 : 8; }
+
+static size_t w8_x16_bytes(long long tokens, int chunks, int shift) {
+    return static_cast<size_t>((tokens + (1 << shift) - 1) >> shift << shift) * chunks * 128;
+}
+
+size_t w8_workspace(long long tokens, int cols) {
+    const int shift = w8_token_shift(tokens);
+    return w8_x16_bytes(tokens, cols / 64 + (cols % 64 != 0), shift) + (size_t(2) * kWtMostCtas * kWtRows * 4 << shift);
 }
 
 template <int DT, int N>
-static cudaError_t run_w8_tc(const W8Args &a, const uint8_t *x16, cudaStream_t s) {
+static cudaError_t run_w8_tc(const W8Args &a, uint8_t *workspace, int shift, cudaStream_t s) {
     auto kern = w8_tc_kernel<DT, N>;
     const int bytes = sizeof(WtSmem<N>) + 1024;
     cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(kern), bytes);
     if (err != cudaSuccess) return err;
-    const int sms = sm_count(&err);
+    int sms = sm_count(&err);
     if (sms <= 0) return err;
+    if (sms > kWtMostCtas) sms = kWtMostCtas;
     unsigned *timeouts = wait_timeout_counter(&err);
     if (!timeouts) return err;
-    const long long row_ctas = (a.l.row_tiles + 7) / 8, token_ctas = (a.tokens + N - 1) / N;
-    int splits = 1;
-    long long best = -1;
-    for (int n = 1; n <= 8; n *= 2) {
-        const long long waves = (row_ctas * token_ctas * n + sms - 1) / sms, cost = waves * ((a.l.chunks + n - 1) / n + 12);
-        if (best < 0 || cost < best) best = cost, splits = n;
-    }
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = splits;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = kWtThreads;
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    // a grid's second dimension, the tokens' tiles, ends at 65535: more tokens are more launches
-    for (long long done = 0; done < token_ctas; done += 65535) {
-        const long long now = token_ctas - done < 65535 ? token_ctas - done : 65535;
-        W8Args part = a;
-        part.tokens = a.tokens - done * N < now * N ? a.tokens - done * N : now * N;
-        part.x_scales += done * N;
-        part.y += done * N * a.y_stride;
-        cfg.gridDim = dim3(static_cast<unsigned>(row_ctas * splits), static_cast<unsigned>(now));
-        err = cudaLaunchKernelEx(&cfg, kern, part, x16 + done * a.l.chunks * WtSmem<N>::kBlock,
-                                 (a.l.chunks + splits - 1) / splits, timeouts);
-        if (err == cudaSuccess) err = cudaGetLastError();
-        if (err != cudaSuccess) return err;
-    }
-    return cudaSuccess;
-}
-
-// Tokens of a CTA: the fewest that take them all, 256 at most.
-static int w8_token_shift(long long tokens) { return tokens <= 32 ? 5 : tokens <= 64 ? 6 : tokens <= 128 ? 7 : 8; }
-
-size_t w8_workspace(long long tokens, int cols) {
-    const long long n = 1ll << w8_token_shift(tokens);
-    return static_cast<size_t>((tokens + n - 1) / n * n) * (static_cast<size_t>(cols) / 64 + (cols % 64 != 0)) * 128;
+    const long long tiles = (a.l.row_tiles + 7) / 8 * ((a.tokens + N - 1) / N);
+    W8Shares shares = {tiles * a.l.chunks, a.l.chunks, (a.l.row_tiles + 7) / 8, sms};
+    // at least eight chunks a CTA, or a tile where that is less
+    const long long few = a.l.chunks < 8 ? tiles : shares.all / 8;
+    if (few < sms) shares.ctas = static_cast<int>(few > 1 ? few : 1);
+    float *const parts = reinterpret_cast<float *>(workspace + w8_x16_bytes(a.tokens, a.l.chunks, shift));
+    err = launch_chained(kern, shares.ctas, kWtThreads, bytes, s, a, shares, static_cast<const uint8_t *>(workspace), parts,
+                         timeouts);
+    if (err != cudaSuccess) return err;
+    bool joined = false;
+    for (int c = 1; c < shares.ctas && !joined; ++c) joined = shares.begin(c) % a.l.chunks != 0;
+    if (!joined) return cudaSuccess;
+    return launch_chained(w8_join_kernel<DT>, dim3(shares.ctas - 1, N / 32), 256, 0, s, a, shares, static_cast<const float *>(parts), N);
 }
 
 template <int DT>
-static cudaError_t pick_tokens(int shift, const W8Args &a, const uint8_t *x16, cudaStream_t s) {
+static cudaError_t pick_tokens(int shift, const W8Args &a, uint8_t *workspace, cudaStream_t s) {
     switch (shift) {
-        case 5: return run_w8_tc<DT, 32>(a, x16, s);
-        case 6: return run_w8_tc<DT, 64>(a, x16, s);
-        case 7: return run_w8_tc<DT, 128>(a, x16, s);
-        default: return run_w8_tc<DT, 256>(a, x16, s);
+        case 5: return run_w8_tc<DT, 32>(a, workspace, shift, s);
+        case 6: return run_w8_tc<DT, 64>(a, workspace, shift, s);
+        case 7: return run_w8_tc<DT, 128>(a, workspace, shift, s);
+        default: return run_w8_tc<DT, 256>(a, workspace, shift, s);
     }
 }
 
 cudaError_t launch_w8_tc(int dtype, const W8Args &a, void *workspace, cudaStream_t s) {
     const int shift = w8_token_shift(a.tokens);
-    uint8_t *const x16 = static_cast<uint8_t *>(workspace);
+    uint8_t *const to = static_cast<uint8_t *>(workspace);
     const int sweep = (a.l.chunks + kWeThreads / 16 - 1) / (kWeThreads / 16);
     const dim3 grid(static_cast<unsigned>((a.tokens + 7) / 8), static_cast<unsigned>(sweep < 65535 ? sweep : 65535));
-    const cudaError_t err = launch_chained(w8_expand_kernel, grid, kWeThreads, 0, s, a, x16, shift);
+    const cudaError_t err = launch_chained(w8_expand_kernel, grid, kWeThreads, 0, s, a, to, shift);
     if (err != cudaSuccess) return err;
-    return dtype ? pick_tokens<1>(shift, a, x16, s) : pick_tokens<0>(shift, a, x16, s);
+    return dtype ? pick_tokens<1>(shift, a, to, s) : pick_tokens<0>(shift, a, to, s);
 }
 
 }  // namespace qrk
