@@ -26,7 +26,7 @@ SOURCES = ["qr_capi.cu", "qr_grid.cu", "qr_encode.cu", "qr_decode.cu", "qr_reduc
            "qr_fc_twoshot.cu", "qr_fp4_twoshot.cu", "qr_codec_peer.cu",
            "qr_serving_capi.cu", "qr_kv_plan.cu", "qr_kv_append.cu", "qr_kv_attention.cu", "qr_kv_split_f16.cu",
            "qr_kv_split_bf16.cu", "qr_kv_tc.cu", "qr_w4.cu", "qr_w4_matvec.cu", "qr_w4_tc.cu",
-           "qr_layer_capi.cu", "qr_norm.cu", "qr_rope.cu", "qr_w8.cu", "qr_w8_few.cu",
+           "qr_layer_capi.cu", "qr_norm_f16.cu", "qr_norm_bf16.cu", "qr_rope.cu", "qr_w8.cu", "qr_w8_few.cu",
            "qr_w8_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

@@ -11,6 +11,10 @@ namespace {
 
 using namespace qrk;
 
+cudaError_t launch_norm(int dtype, int weight, const NormArgs &a, cudaStream_t s) {
+    return dtype ? launch_norm_typed<1>(weight, a, s) : launch_norm_typed<0>(weight, a, s);
+}
+
 cudaStream_t stream_of(qr_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Rows of `width` bytes, `stride` bytes apart.

@@ -1,0 +1,8 @@
+// qr_norm_bf16.cu -- the norm kernels for bf16 values (qr_norm.cuh).
+#include "qr_norm.cuh"
+
+namespace qrk {
+
+template cudaError_t launch_norm_typed<1>(int weight, const NormArgs &a, cudaStream_t s);
+
+}  // namespace qrk

@@ -131,7 +131,8 @@ struct W8Args {
 };
 
 // weight: 0 none (rows in 8 bits without a norm), 1 in x's type, 2 in fp32
-cudaError_t launch_norm(int dtype, int weight, const NormArgs &a, cudaStream_t s);
+template <int DT>  // qr_norm_f16.cu, qr_norm_bf16.cu
+cudaError_t launch_norm_typed(int weight, const NormArgs &a, cudaStream_t s);
 cudaError_t launch_rope(int dtype, bool interleaved, const RopeArgs &a, cudaStream_t s);
 cudaError_t launch_w8_pack(int rows, int cols, const int8_t *codes, long long stride, const float *scales, void *packed,
                            cudaStream_t s);
