@@ -12,57 +12,63 @@
 #include "qr_kv_device.cuh"
 #include "qr_launch.h"
 #include "qr_serving.h"
-#include "qr_w4.cuh"
 
 namespace qrk {
 
-// Eight 16-bit values, any alignment, those before `have`.
-template <bool ALIGNED>
-__device__ __forceinline__ uint4 load8(const uint16_t *p, int have) {
-    if constexpr (ALIGNED) return have > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
-    else return load8_any(p, have);
+// A piece is eight values of a row on a 16-byte boundary, from value i on.  Where
+// rows do not begin on such boundaries (SHIFT), the first and the last piece of a
+// row are partly outside it: they are read whole, as aligned words that hold a
+// value of the row, and what is outside becomes zero when it is used (masking
+// what a load has just asked for would wait for it).
+__device__ __forceinline__ uint4 load_piece(const uint16_t *row, int i, int cols) {
+    return i < cols ? *reinterpret_cast<const uint4 *>(row + i) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ bool edge_piece(int i, int cols) { return i < 0 || (i < cols && i + 8 > cols); }
+// `mask`: of the row's first piece and of its last (one piece may be both).
+__device__ __forceinline__ uint4 inside(uint4 r, int i, int cols, const uint4 *mask) {
+    const uint4 a = i < 0 ? mask[0] : make_uint4(~0u, ~0u, ~0u, ~0u), b = i + 8 > cols ? mask[1] : make_uint4(~0u, ~0u, ~0u, ~0u);
+    return make_uint4(r.x & a.x & b.x, r.y & a.y & b.y, r.z & a.z & b.z, r.w & a.w & b.w);
 }
 
-// ... and back, by the widest stores that the address allows.
-template <bool ALIGNED>
-__device__ __forceinline__ void store8(uint16_t *p, const uint4 o, int have) {
-    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15;
-    if (ALIGNED || (have >= 8 && off == 0)) {
-        if (have > 0) *reinterpret_cast<uint4 *>(p) = o;
-    } else if (have >= 8 && (off & 3) == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(p)[i] = w[i];
-    } else if (have >= 8) {
-        p[0] = static_cast<uint16_t>(w[0]);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(p + 1 + 2 * i) = __funnelshift_r(w[i], w[i + 1], 16);
-        p[7] = static_cast<uint16_t>(w[3] >> 16);
+template <int DT, bool SHIFT>
+__device__ __forceinline__ void store_piece(uint16_t *row, int i, int cols, const float (&v)[8]) {
+    const uint32_t w[4] = {narrow2<DT>(v[0], v[1]), narrow2<DT>(v[2], v[3]), narrow2<DT>(v[4], v[5]), narrow2<DT>(v[6], v[7])};
+    if (!SHIFT || !edge_piece(i, cols)) {
+        *reinterpret_cast<uint4 *>(row + i) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < have) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+        for (int e = 0; e < 8; ++e)
+            if (i + e >= 0 && i + e < cols) row[i + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
     }
 }
 
-// W: weight none (0), in x's type (1), fp32 (2).
-template <int DT, int W, bool ALIGNED>
+// W: weight none (0), in x's type (1), fp32 (2); of a piece, from aligned words
+// or, SHIFT, value by value.
+template <int DT, int W, bool SHIFT>
 struct NormWeight {
     uint4 raw[W == 2 ? 2 : 1];
 
-    __device__ __forceinline__ void load(const void *weight, int i, int have) {
-        if constexpr (W == 1) raw[0] = load8<ALIGNED>(static_cast<const uint16_t *>(weight) + i, have);
-        if constexpr (W == 2) {
-            const float *const p = static_cast<const float *>(weight) + i;
-            if (ALIGNED) {
-                if (have > 0) raw[0] = reinterpret_cast<const uint4 *>(p)[0], raw[1] = reinterpret_cast<const uint4 *>(p)[1];
-            } else {
-                uint32_t v[8];
+    __device__ __forceinline__ void load(const void *weight, int i, int cols) {
+        if (W == 0 || i >= cols) return;
+        if constexpr (SHIFT) {
+            uint32_t v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = e < have ? __float_as_uint(p[e]) : 0u;
+            for (int e = 0; e < 8; ++e) {
+                v[e] = 0;
+                if (i + e >= 0 && i + e < cols)
+                    v[e] = W == 2 ? static_cast<const uint32_t *>(weight)[i + e] : static_cast<const uint16_t *>(weight)[i + e];
+            }
+            if constexpr (W == 2) {
                 raw[0] = make_uint4(v[0], v[1], v[2], v[3]);
                 raw[1] = make_uint4(v[4], v[5], v[6], v[7]);
+            } else {
+                raw[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
             }
+        } else if constexpr (W == 1) {
+            raw[0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(weight) + i);
+        } else {
+            const uint4 *const p = reinterpret_cast<const uint4 *>(static_cast<const float *>(weight) + i);
+            raw[0] = p[0], raw[1] = p[1];
         }
     }
     __device__ __forceinline__ void get(float (&w)[8]) const {
@@ -75,13 +81,16 @@ struct NormWeight {
     }
 };
 
-// The bytes of four codes of v * f (|v f| is at most 127 (1 + 2^-23), or NaN,
+// A code (in the low byte), and the bytes of four, of v * f (|v f| is at most 127 (1 + 2^-23), or NaN,
 // which gives what it gives): adding 1.5 * 2^23 rounds half to even and leaves
 // the integer in the low bits.
+__device__ __forceinline__ uint32_t row_code(float v, float f) {
+    return __float_as_uint(__fadd_rn(__fmul_rn(v, f), 12582912.0f));
+}
 __device__ __forceinline__ uint32_t row_codes(const float *v, float f) {
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(__fadd_rn(__fmul_rn(v[i], f), 12582912.0f));
+    for (int i = 0; i < 4; ++i) u[i] = row_code(v[i], f);
     return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
 }
 
@@ -118,108 +127,151 @@ __device__ __forceinline__ void row_reduce(float &sum, float &most, float2 *s, i
     }
 }
 
-// A row a CTA, or a warp (WARP); P pieces of eight values a thread, THREADS at
-// most.  HOLD: the weights stay in registers from row to row, and the next row is
-// on its way while this one is reduced.
-template <int DT, int W, bool EIGHT, bool ALIGNED, bool WARP, int P, int THREADS, bool HOLD>
-__global__ void __launch_bounds__(THREADS) norm_kernel(NormArgs a) {
+// A row a CTA, or a warp (WARP); P pieces a thread, THREADS threads at most.
+// AHEAD: the next row is on its way while this one is reduced, and the weights
+// stay in registers from row to row: a CTA's (or warp's) rows are a multiple of
+// eight apart, so that they all lie alike between 16-byte words.
+//
+// Shifted rows in 8 bits: codes begin on boundaries that the pieces do not, so
+// that eight of them are a piece's last and the next lane's first; a warp's last
+// lane has the piece that the next warp's first has too, and stores none.
+template <int DT, int W, bool EIGHT, bool SHIFT, bool WARP, int P, int THREADS, bool AHEAD>
+__global__ void __launch_bounds__(THREADS, WARP || (P == 2 && !EIGHT) ? 2 : 1) norm_kernel(NormArgs a) {
     chain_entry();
+    constexpr int kLanes = SHIFT && EIGHT ? 31 : 32;
     __shared__ float2 s_part[64];
-    const int threads = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
+    __shared__ uint4 s_mask[2];
+    const int lane = threadIdx.x & 31, cols = a.cols;
+    const int threads = WARP ? kLanes : (blockDim.x >> 5) * kLanes, me0 = WARP ? 0 : (threadIdx.x >> 5) * kLanes;
+    const bool own = kLanes == 32 || lane < kLanes;
     const long long stride = WARP ? gridDim.x * (blockDim.x / 32ll) : gridDim.x;
     long long t = WARP ? blockIdx.x * (blockDim.x / 32ll) + (threadIdx.x >> 5) : blockIdx.x;
     const auto *const x = static_cast<const uint16_t *>(a.x), *const res = static_cast<const uint16_t *>(a.residual);
     const bool has_res = W && res != nullptr;
 
-    NormWeight<DT, W, ALIGNED> weight[HOLD ? P : 1];
+    // values between the 16-byte boundary at or before the rows and their first
+    const int off = SHIFT ? static_cast<int>(reinterpret_cast<uintptr_t>(x + t * a.x_row) >> 1 & 7) : 0;
+    auto place = [&](int p) { return (me0 + lane + p * threads) * 8 - off; };
+    // whether the warp has a piece of the row in its p-th place
+    auto any = [&](int p) { return (me0 + p * threads) * 8 - off < cols; };
+    // (weights that are not held are read a group ahead of its stores)
+    constexpr int kGroup = AHEAD ? P : P > 2 ? 2 : 1;
+    NormWeight<DT, W, SHIFT> weight[kGroup];
     uint4 rx[P], rr[P];
     auto load = [&](long long row) {
+        const uint16_t *const xr = x + row * a.x_row, *const sr = res + row * a.residual_row;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int i = (me + p * threads) * 8;
-            rx[p] = load8<ALIGNED>(x + row * a.x_row + i, a.cols - i);
-            if (has_res) rr[p] = load8<ALIGNED>(res + row * a.residual_row + i, a.cols - i);
+            rx[p] = load_piece(xr, place(p), cols);
+            if (has_res) rr[p] = load_piece(sr, place(p), cols);
         }
     };
     auto weights = [&](int p, float (&w)[8]) {
-        if (!HOLD) weight[0].load(a.weight, (me + p * threads) * 8, a.cols - (me + p * threads) * 8);
-        weight[HOLD ? p : 0].get(w);
+        if (!AHEAD && p % kGroup == 0) {
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) weight[k].load(a.weight, place(p + k), cols);
+        }
+        weight[p % kGroup].get(w);
     };
-    if (HOLD) {
+    if constexpr (AHEAD) {
         if (t < a.tokens) load(t);
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-            weight[HOLD ? p : 0].load(a.weight, (me + p * threads) * 8, a.cols - (me + p * threads) * 8);
+        for (int p = 0; p < P; ++p) weight[p].load(a.weight, place(p), cols);
     }
+    // (the rows of a warp of its own lie as that warp's do: a mask each is not worth
+    // its shared memory, it is worked out)
+    if (SHIFT && !WARP && threadIdx.x < 16) {
+        const int last = (cols + off) & 7, e = threadIdx.x & 7;
+        const bool in = threadIdx.x < 8 ? e >= off : e < (last ? last : 8);
+        reinterpret_cast<uint16_t *>(s_mask)[threadIdx.x] = in ? 0xffff : 0;
+    }
+    if (SHIFT && !WARP) __syncthreads();
     for (int turn = 0; t < a.tokens; t += stride, turn ^= 1) {
-        float h[P][8];  // in 8 bits: h times the weight
+        float h[W ? P : 1][8];  // in 8 bits: h times the weight
+        uint4 kept[P];          // x itself where there is no weight
         float sum = 0.0f, most = 0.0f;
-        if (!HOLD) load(t);
+        if (!AHEAD) load(t);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int i = (me + p * threads) * 8;
-            widen8<DT>(rx[p], h[p]);
-            if (has_res) {
-                float r[8];
-                widen8<DT>(rr[p], r);
+            if ((SHIFT || WARP) && !any(p)) break;
+            const int i = place(p);
+            float(&v)[8] = h[W ? p : 0];
+            auto masked = [&](uint4 r) {
+                if (!SHIFT || !edge_piece(i, cols)) return r;
+                if constexpr (!WARP) return inside(r, i, cols, s_mask);
+                uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[p][e] = __fadd_rn(h[p][e], r[e]);
-                if (a.residual_out) {
-                    uint4 o;
-                    o.x = narrow2<DT>(h[p][0], h[p][1]), o.y = narrow2<DT>(h[p][2], h[p][3]);
-                    o.z = narrow2<DT>(h[p][4], h[p][5]), o.w = narrow2<DT>(h[p][6], h[p][7]);
-                    store8<ALIGNED>(static_cast<uint16_t *>(a.residual_out) + t * a.residual_out_row + i, o, a.cols - i);
-                }
-            }
-            if (i >= a.cols) continue;
+                for (int e = 0; e < 8; ++e)
+                    if (i + e < 0 || i + e >= cols) w[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                return make_uint4(w[0], w[1], w[2], w[3]);
+            };
+            kept[p] = masked(rx[p]);
+            widen8<DT>(kept[p], v);
             float w[8];
             if (W && EIGHT) weights(p, w);
+            if (i >= cols) continue;
+            if (has_res) {
+                float r[8];
+                widen8<DT>(masked(rr[p]), r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(v[e], r[e]);
+                if (a.residual_out && own)
+                    store_piece<DT, SHIFT>(static_cast<uint16_t *>(a.residual_out) + t * a.residual_out_row, i, cols, v);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (W) sum = __fmaf_rn(h[p][e], h[p][e], sum);
-                if (W && EIGHT) h[p][e] = __fmul_rn(h[p][e], w[e]);
-                if (EIGHT) most = max_nan(most, fabsf(h[p][e]));
+                if (W && own) sum = __fmaf_rn(v[e], v[e], sum);
+                if (W && EIGHT) v[e] = __fmul_rn(v[e], w[e]);
+                if (EIGHT) most = max_nan(most, fabsf(v[e]));
             }
         }
-        if (HOLD && t + stride < a.tokens) load(t + stride);
+        if (AHEAD && t + stride < a.tokens) load(t + stride);
         row_reduce<WARP, W != 0, EIGHT>(sum, most, s_part, turn);
         const float rs = W ? norm_factor(sum, a) : 1.0f;
         if constexpr (EIGHT) {
             const float f = row_factor(most);
-            if (me == 0) a.scales[t] = __fmul_rn(__fdiv_rn(most, 127.0f), rs);
+            if (me0 + lane == 0) a.scales[t] = __fmul_rn(__fdiv_rn(most, 127.0f), rs);
             uint8_t *const to = static_cast<uint8_t *>(a.y) + t * a.y_row;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                const int i = (me + p * threads) * 8;
-                if (i >= a.cols) break;
-                const uint2 o = make_uint2(row_codes(h[p], f), row_codes(h[p] + 4, f));
-                if (ALIGNED || i + 8 <= a.cols) {
-                    *reinterpret_cast<uint2 *>(to + i) = o;
+                if ((SHIFT || WARP) && !any(p)) break;
+                const int i = place(p);
+                float(&v)[8] = h[W ? p : 0];
+                if (!W) widen8<DT>(kept[p], v);
+                const uint2 o = make_uint2(row_codes(v, f), row_codes(v + 4, f));
+                if constexpr (!SHIFT) {
+                    if (i < cols) *reinterpret_cast<uint2 *>(to + i) = o;
                 } else {
-#pragma unroll
-                    for (int e = 0; e < 7; ++e)
-                        if (i + e < a.cols) to[i + e] = static_cast<uint8_t>((e < 4 ? o.x : o.y) >> (8 * (e & 3)));
+                    unsigned long long mine = o.x | static_cast<unsigned long long>(o.y) << 32;
+                    const unsigned long long next = __shfl_down_sync(~0u, mine, 1);
+                    if (off) mine = mine >> (8 * off) | next << (64 - 8 * off);
+                    const int have = cols - i - off;
+                    if (own && have >= 8) {
+                        *reinterpret_cast<unsigned long long *>(to + i + off) = mine;
+                    } else if (own && have > 0) {
+#pragma unroll 1
+                        for (int e = 0; e < have; ++e) to[i + off + e] = static_cast<uint8_t>(mine >> (8 * e));
+                    }
                 }
             }
         } else {
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                const int i = (me + p * threads) * 8;
-                if (i >= a.cols) break;
-                float w[8];
+                if ((SHIFT || WARP) && !any(p)) break;
+                const int i = place(p);
+                float w[8], (&v)[8] = h[W ? p : 0];
                 weights(p, w);
+                if (i >= cols) continue;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[p][e] = h[p][e] * rs * w[e];
-                uint4 o;
-                o.x = narrow2<DT>(h[p][0], h[p][1]), o.y = narrow2<DT>(h[p][2], h[p][3]);
-                o.z = narrow2<DT>(h[p][4], h[p][5]), o.w = narrow2<DT>(h[p][6], h[p][7]);
-                store8<ALIGNED>(static_cast<uint16_t *>(a.y) + t * a.y_row + i, o, a.cols - i);
+                for (int e = 0; e < 8; ++e) v[e] = v[e] * rs * w[e];
+                store_piece<DT, SHIFT>(static_cast<uint16_t *>(a.y) + t * a.y_row, i, cols, v);
             }
         }
     }
 }
 
-// Rows longer than a CTA's registers: read twice, a value a thread at a time.
+// Rows longer than a CTA's registers, or on unlike boundaries: read twice, a value
+// a thread at a time.
 constexpr int kNormLongThreads = 1024;
 template <int DT, int W, bool EIGHT>
 __global__ void __launch_bounds__(kNormLongThreads) norm_long_kernel(NormArgs a) {
@@ -250,8 +302,8 @@ __global__ void __launch_bounds__(kNormLongThreads) norm_long_kernel(NormArgs a)
             const float h = h_at(i);
             if (W && a.residual_out) static_cast<uint16_t *>(a.residual_out)[t * a.residual_out_row + i] = narrow1<DT>(h);
             if constexpr (EIGHT) {
-                const float v[4] = {W ? __fmul_rn(h, w_at(i)) : h, 0.0f, 0.0f, 0.0f};
-                static_cast<uint8_t *>(a.y)[t * a.y_row + i] = static_cast<uint8_t>(row_codes(v, f));
+                static_cast<uint8_t *>(a.y)[t * a.y_row + i] =
+                    static_cast<uint8_t>(row_code(W ? __fmul_rn(h, w_at(i)) : h, f));
             } else {
                 static_cast<uint16_t *>(a.y)[t * a.y_row + i] = narrow1<DT>(h * rs * w_at(i));
             }
@@ -259,41 +311,57 @@ __global__ void __launch_bounds__(kNormLongThreads) norm_long_kernel(NormArgs a)
     }
 }
 
-template <int DT, int W, bool EIGHT, bool ALIGNED>
+template <int DT, int W, bool EIGHT, bool SHIFT>
 static cudaError_t run_norm(const NormArgs &a, cudaStream_t s) {
     cudaError_t err = cudaSuccess;
     const int sms = sm_count(&err);
     if (sms <= 0) return err;
-    auto launch = [&](auto kern, int threads, int rows) {
-        const int grid = grid_for(reinterpret_cast<const void *>(kern), threads, (a.tokens + rows - 1) / rows, 0, 1, &err);
-        return grid <= 0 ? err : launch_chained(kern, grid, threads, 0, s, a);
+    constexpr int kLanes = SHIFT && EIGHT ? 31 : 32;
+    const int pieces = (a.cols + 7) / 8 + SHIFT;
+    auto threads = [&](int p) { return (pieces + kLanes * p - 1) / (kLanes * p) * 32; };
+    auto launch = [&](auto kern, int n, int rows) {
+        const long long units = (a.tokens + rows - 1) / rows;
+        int grid = grid_for(reinterpret_cast<const void *>(kern), n, units, 0, 1, &err);
+        if (SHIFT && rows == 1 && grid < units) grid &= ~7;  // (a CTA's rows lie alike)
+        return grid <= 0 ? err : launch_chained(kern, grid, n, 0, s, a);
     };
-    if (a.cols > 32768) return launch(norm_long_kernel<DT, W, EIGHT>, kNormLongThreads, 1);
-    const int pieces = (a.cols + 7) / 8;
-    if (a.cols <= 1024 && a.tokens > 8 * sms)
-        return launch(norm_kernel<DT, W, EIGHT, ALIGNED, true, 4, 256, ALIGNED>, 256, 8);
-    if (pieces <= 1024 && a.tokens <= 2 * sms)
-        return launch(norm_kernel<DT, W, EIGHT, ALIGNED, false, 1, 1024, false>, (pieces + 31) / 32 * 32, 1);
-    if (pieces <= 2048)
-        return launch(norm_kernel<DT, W, EIGHT, ALIGNED, false, 4, 512, ALIGNED>, (pieces + 127) / 128 * 32, 1);
-    return launch(norm_kernel<DT, W, EIGHT, ALIGNED, false, 4, 1024, false>, (pieces + 127) / 128 * 32, 1);
+    if (threads(4) <= 32 && a.tokens > 8 * sms) return launch(norm_kernel<DT, W, EIGHT, SHIFT, true, 4, 256, true>, 256, 8);
+    if (threads(1) <= 1024 && a.tokens <= 2 * sms)
+        return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 1, 1024, false>, threads(1), 1);
+    if constexpr (W == 0) {
+        if (threads(4) > 512) return launch(norm_kernel<DT, 0, EIGHT, SHIFT, false, 8, 512, true>, threads(8), 1);
+    }
+    if constexpr (SHIFT) {
+        if (threads(2) <= 512) return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 2, 512, true>, threads(2), 1);
+    }
+    if (threads(4) <= 512) return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 4, 512, true>, threads(4), 1);
+    return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 4, 1024, false>, threads(4), 1);
+}
+
+template <int DT, int W, bool EIGHT>
+static cudaError_t pick_norm(const NormArgs &a, cudaStream_t s) {
+    // 16-byte words: rows that all begin on them, and a weight that does; or rows
+    // that all lie alike between them
+    auto at = [](const void *p) { return reinterpret_cast<uintptr_t>(p) & 15; };
+    auto alike = [&](const void *p, long long row) {
+        return !p || (at(p) == at(a.x) && (a.tokens == 1 || (row - a.x_row) % 8 == 0));
+    };
+    const bool like = alike(a.residual, a.residual_row) && alike(a.residual_out, a.residual_out_row) &&
+                      (EIGHT || alike(a.y, a.y_row));
+    const bool whole = a.cols % 8 == 0 && at(a.x) == 0 && (a.tokens == 1 || a.x_row % 8 == 0) && at(a.weight) == 0;
+    if (like && whole && a.cols <= 32768) return run_norm<DT, W, EIGHT, false>(a, s);
+    if (like && a.cols <= 31 * 1024 - 8) return run_norm<DT, W, EIGHT, true>(a, s);
+    cudaError_t err = cudaSuccess;
+    const int grid = grid_for(reinterpret_cast<const void *>(norm_long_kernel<DT, W, EIGHT>), kNormLongThreads, a.tokens, 0, 1, &err);
+    return grid <= 0 ? err : launch_chained(norm_long_kernel<DT, W, EIGHT>, grid, kNormLongThreads, 0, s, a);
 }
 
 template <int DT>
 cudaError_t launch_norm_typed(int weight, const NormArgs &a, cudaStream_t s) {
     const bool eight = a.scales != nullptr;
-    auto rows16 = [&](const void *p, long long row) {
-        return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (a.tokens == 1 || row % 8 == 0);
-    };
-    const bool vector = a.cols % 8 == 0 && rows16(a.x, a.x_row) && (!a.residual || rows16(a.residual, a.residual_row)) &&
-                        (!a.residual_out || rows16(a.residual_out, a.residual_out_row)) && rows16(a.weight, 0) &&
-                        rows16(a.y, a.y_row);
-    if (weight == 0) return vector ? run_norm<DT, 0, true, true>(a, s) : run_norm<DT, 0, true, false>(a, s);
-    if (weight == 1)
-        return eight ? (vector ? run_norm<DT, 1, true, true>(a, s) : run_norm<DT, 1, true, false>(a, s))
-                     : (vector ? run_norm<DT, 1, false, true>(a, s) : run_norm<DT, 1, false, false>(a, s));
-    return eight ? (vector ? run_norm<DT, 2, true, true>(a, s) : run_norm<DT, 2, true, false>(a, s))
-                 : (vector ? run_norm<DT, 2, false, true>(a, s) : run_norm<DT, 2, false, false>(a, s));
+    if (weight == 0) return pick_norm<DT, 0, true>(a, s);
+    if (weight == 1) return eight ? pick_norm<DT, 1, true>(a, s) : pick_norm<DT, 1, false>(a, s);
+    return eight ? pick_norm<DT, 2, true>(a, s) : pick_norm<DT, 2, false>(a, s);
 }
 
 }  // namespace qrk

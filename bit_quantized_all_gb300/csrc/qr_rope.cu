@@ -171,7 +171,7 @@ static cudaError_t run_rope(const RopeArgs &a, bool copies, cudaStream_t s) {
     p.heads = a.heads[0] + a.heads[1];
     const int each = p.heads * p.units;
     p.tokens = 1;
-    while (2 * p.tokens <= kRopeTokens && p.tokens * each < 4 * kRopeThreads && 2 * p.tokens * (a.rot / 2) <= kRopePairs &&
+    while (2 * p.tokens <= kRopeTokens && p.tokens * each < 8 * kRopeThreads && 2 * p.tokens * (a.rot / 2) <= kRopePairs &&
            a.tokens / (2 * p.tokens) >= 8ll * sms)
         p.tokens *= 2;
     // (threads past the last task divide too, up to a round further)

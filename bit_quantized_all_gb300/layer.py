@@ -83,18 +83,20 @@ class Q8Rows:
 
 def _rows8_out(out, tokens: int, cols: int, device, what: str) -> Q8Rows:
     if out is None:
-        # (as Q8Rows.empty, of one allocation and without its checks: some 6 us a call)
-        pitch = (cols + 15) // 16 * 16
-        raw = torch.empty(tokens * (pitch + 4), dtype=torch.int8, device=device)
+        # (as Q8Rows.empty without its checks: some 5 us a call)
         out = Q8Rows.__new__(Q8Rows)
+        pad = -cols % 16
+        codes = torch.empty((tokens, cols + pad), dtype=torch.int8, device=device)
+        out.codes = codes[:, :cols] if pad else codes
+        out.scales = torch.empty(tokens, dtype=torch.float32, device=device)
         out.device, out.tokens, out.cols = device, tokens, cols
-        out.codes = raw.as_strided((tokens, cols), (pitch, 1))
-        out.scales = raw[tokens * pitch:].view(torch.float32)
         return out
     if not isinstance(out, Q8Rows):
         raise TypeError(f"{what}: out must be a Q8Rows")
     if out.tokens != tokens or out.cols != cols:
         raise ValueError(f"{what}: out is [{out.tokens}, {out.cols}], expected [{tokens}, {cols}]")
+    if out.device != device:
+        raise ValueError(f"{what}: every tensor must be on {device}")
     return out
 
 
@@ -108,10 +110,10 @@ def qr_q8_quantize(x: torch.Tensor, out: Q8Rows | None = None, stream=None) -> Q
     tokens, cols = x.shape
     dev = x.device
     out = _rows8_out(out, tokens, cols, dev, "qr_q8_quantize")
-    _on(dev, "qr_q8_quantize", out.codes)
     if tokens and cols:
-        status = (_L or _lib()).qr_q8_quantize(dt, tokens, cols, x.data_ptr(), x.stride(0), out.codes.data_ptr(),
-                                               out.codes.stride(0), out.scales.data_ptr(), _current(dev))
+        codes = out.codes
+        status = (_L or _lib()).qr_q8_quantize(dt, tokens, cols, x.data_ptr(), x.stride(0), codes.data_ptr(),
+                                               codes.stride(0), out.scales.data_ptr(), _current(dev))
         if status:
             _check(status, "qr_q8_quantize")
     elif tokens:
@@ -124,52 +126,58 @@ def qr_q8_quantize(x: torch.Tensor, out: Q8Rows | None = None, stream=None) -> Q
 # ---------------------------------------------------------------------------
 def _norm(what, x, weight, eps, residual, residual_out, out, eight):
     dt = _dtype_code(x, "x")
-    tokens, cols = x.shape
-    dev = x.device
-    _cuda_contig(weight, "weight")
-    if weight.dtype not in (x.dtype, torch.float32):
-        raise TypeError(f"weight must be {x.dtype} or torch.float32, got {weight.dtype}")
-    if weight.shape != (cols,):
-        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected ({cols},)")
-    _on(dev, what, weight)
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    tokens, cols = shape
+    wide = isinstance(weight, torch.Tensor) and weight.dtype is torch.float32
+    _int_tensor(weight, "weight", torch.float32 if wide else dtype, (cols,))
+    if weight.device != dev:
+        _on(dev, what, weight)
+    if not 0.0 < eps < math.inf:
+        raise ValueError(f"eps must be finite and above 0, got {eps}")
     if residual is None:
         if residual_out is not None:
             raise ValueError(f"{what}: residual_out without residual")
+        res = (0, 0, 0, 0)
     else:
-        if residual_out is None:
-            residual_out = residual
-        for t, name in ((residual, "residual"), (residual_out, "residual_out")):
-            _matrix(t, name, cols)
-            if t.dtype != x.dtype or t.shape[0] != tokens:
-                raise ValueError(f"{name} must match x's shape and dtype")
-        _on(dev, what, residual, residual_out)
+        _matrix(residual, "residual", cols)
+        if residual.dtype is not dtype or residual.shape != shape:
+            raise ValueError("residual must match x's shape and dtype")
+        if residual.device != dev:
+            _on(dev, what, residual)
+        at, stride = residual.data_ptr(), residual.stride(0)
+        if residual_out is None or residual_out is residual:
+            res = (at, stride, at, stride)
+        else:
+            _matrix(residual_out, "residual_out", cols)
+            if residual_out.dtype is not dtype or residual_out.shape != shape:
+                raise ValueError("residual_out must match x's shape and dtype")
+            if residual_out.device != dev:
+                _on(dev, what, residual_out)
+            res = (at, stride, residual_out.data_ptr(), residual_out.stride(0))
     if eight:
         out = _rows8_out(out, tokens, cols, dev, what)
-        y, scales = out.codes, out.scales
+        y = out.codes
     else:
         if out is None:
-            out = torch.empty((tokens, cols), dtype=x.dtype, device=dev)
+            out = torch.empty((tokens, cols), dtype=dtype, device=dev)
         else:
             _matrix(out, "out", cols)
-            if out.dtype != x.dtype or out.shape[0] != tokens:
+            if out.dtype is not dtype or out.shape != shape:
                 raise ValueError("out must match x's shape and dtype")
-        y, scales = out, None
-    _on(dev, what, y)
-    if not (eps > 0 and math.isfinite(eps)):
-        raise ValueError(f"eps must be finite and above 0, got {eps}")
+            _on(dev, what, out)
+        y = out
     if tokens and cols:
-        args = (dt, tokens, cols, x.data_ptr(), x.stride(0),
-                0 if residual is None else residual.data_ptr(), 0 if residual is None else residual.stride(0),
-                0 if residual is None else residual_out.data_ptr(), 0 if residual is None else residual_out.stride(0),
-                weight.data_ptr(), weight.dtype is torch.float32, eps, y.data_ptr(), y.stride(0))
+        L = _L or _lib()
         if eight:
-            status = (_L or _lib()).qr_rms_norm_q8(*args, scales.data_ptr(), _current(dev))
+            status = L.qr_rms_norm_q8(dt, tokens, cols, x.data_ptr(), x.stride(0), *res, weight.data_ptr(), wide, eps,
+                                      y.data_ptr(), y.stride(0), out.scales.data_ptr(), _current(dev))
         else:
-            status = (_L or _lib()).qr_rms_norm(*args, _current(dev))
+            status = L.qr_rms_norm(dt, tokens, cols, x.data_ptr(), x.stride(0), *res, weight.data_ptr(), wide, eps,
+                                   y.data_ptr(), y.stride(0), _current(dev))
         if status:
             _check(status, what)
     elif tokens and eight:
-        scales.zero_()
+        out.scales.zero_()
     return out
 
 
@@ -372,6 +380,8 @@ class Rope:
 
 
 def _heads(t: torch.Tensor, what: str) -> None:
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3 and t.stride(2) == 1:
+        return
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{what} must be a tensor [tokens, heads, head_dim]")
     if not t.is_cuda:
@@ -391,31 +401,37 @@ def qr_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope, positions: torc
         with _as_current(q.device, stream):
             return qr_rope(q, k, rope, positions, plan, out)
     dt = _dtype_code(q, "q")
-    tokens, q_heads, dim = q.shape
+    shape, dtype, dev = q.shape, q.dtype, q.device
+    tokens, q_heads, dim = shape
     if k is not None:
         _heads(k, "k")
-        if k.dtype != q.dtype or k.shape[0] != tokens or k.shape[2] != dim:
+        k_shape = k.shape
+        if k.dtype is not dtype or k_shape[0] != tokens or k_shape[2] != dim:
             raise ValueError("k must have q's dtype, tokens and head_dim")
-    dev = q.device
+        if k.device != dev:
+            _on(dev, "qr_rope", k)
     if rope.rot_dim > dim:
         raise ValueError(f"the table rotates {rope.rot_dim} values of a head, which has {dim}")
+    if rope.device != dev:
+        _on(dev, "qr_rope", rope.turns)
     if (positions is None) == (plan is None):
         raise ValueError("either positions or plan")
     if plan is None:
         _int_tensor(positions, "positions", torch.int32, (tokens,))
+        if positions.device != dev:
+            _on(dev, "qr_rope", positions)
         where = (positions.data_ptr(), 0, 0, 0)
-        _on(dev, "qr_rope", positions, rope.turns)
     else:
         requests = plan.kv_lens.numel()
         _int_tensor(plan.kv_lens, "plan.kv_lens", torch.int32)
         _int_tensor(plan.q_offsets, "plan.q_offsets", torch.int32, (requests + 1,))
+        _on(dev, "qr_rope", plan.kv_lens, plan.q_offsets)
         where = (0, requests, plan.q_offsets.data_ptr(), plan.kv_lens.data_ptr())
-        _on(dev, "qr_rope", plan.kv_lens, plan.q_offsets, rope.turns)
     if out is None:
         # (tokens that a plan leaves out: zeros rather than what the memory held)
         new = torch.empty if plan is None else torch.zeros
-        q_out = new((tokens, q_heads, dim), dtype=q.dtype, device=dev)
-        k_out = None if k is None else new(k.shape, dtype=k.dtype, device=dev)
+        q_out = new(shape, dtype=dtype, device=dev)
+        k_out = None if k is None else new(k_shape, dtype=dtype, device=dev)
     else:
         q_out, k_out = out
         if (k is None) != (k_out is None):
@@ -423,16 +439,16 @@ def qr_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope, positions: torc
         for t, x, what in ((q_out, q, "q"), (k_out, k, "k")):
             if t is not None and t is not x:
                 _heads(t, f"out's {what}")
-                if t.dtype != x.dtype or t.shape != x.shape:
+                if t.dtype is not dtype or t.shape != x.shape:
                     raise ValueError(f"out's {what} must match {what}'s shape and dtype")
-    _on(dev, "qr_rope", *(t for t in (k, q_out, k_out) if t is not None))
+                _on(dev, "qr_rope", t)
     if tokens and q_heads:
         qs, qo = q.stride(), q_out.stride()
-        if k is None or not k.shape[1]:
+        if k is None or not k_shape[1]:
             keys = (0, 0, 0, 0, 0, 0, 0)
         else:
             ks, ko = k.stride(), k_out.stride()
-            keys = (k.data_ptr(), ks[0], ks[1], k.shape[1], k_out.data_ptr(), ko[0], ko[1])
+            keys = (k.data_ptr(), ks[0], ks[1], k_shape[1], k_out.data_ptr(), ko[0], ko[1])
         status = (_L or _lib()).qr_rope(dt, tokens, dim, rope.rot_dim, rope.layout == "interleaved", rope.turns.data_ptr(),
                                         rope.factor, *where, q.data_ptr(), qs[0], qs[1], q_heads, q_out.data_ptr(),
                                         qo[0], qo[1], *keys, _current(dev))

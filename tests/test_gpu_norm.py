@@ -114,6 +114,26 @@ def test_strided_rows_leave_their_surroundings(cols, off):
     assert (raw[:, cols:] == 77).all()
 
 
+@pytest.mark.parametrize("tokens", [5, 3000])
+@pytest.mark.parametrize("cols", [33, 640, 1003])
+def test_rows_on_unlike_boundaries(cols, tokens):
+    """Operands that do not lie alike between 16-byte words, one after the other."""
+    rng = np.random.default_rng(cols)
+    plain = [_x(rng, (tokens, cols), 1).cuda() for _ in range(2)]
+    w = _x(rng, (cols,), 1).cuda()
+    odd_w = torch.zeros(cols + 3, dtype=torch.bfloat16, device="cuda")[3:].copy_(w)
+    for which in range(5):
+        wide = torch.full((tokens, cols + 13), 2.0, dtype=torch.bfloat16, device="cuda")
+        odd = wide[:, 5:5 + cols]
+        x, res = (odd.copy_(t) if which == i else t for i, t in enumerate(plain))
+        res_out = odd if which == 2 else torch.empty_like(plain[0])
+        y = odd if which == 3 else None
+        _check(x, odd_w if which == 4 else w, res, False, 1, out=y, residual_out=res_out)
+        assert (wide[:, :5] == 2).all() and (wide[:, 5 + cols:] == 2).all()
+        _check(x, odd_w if which == 4 else w, res, True, 1, residual_out=res_out)
+        assert (wide[:, :5] == 2).all() and (wide[:, 5 + cols:] == 2).all()
+
+
 @pytest.mark.parametrize("cols", [512, 1001, 40000])
 def test_in_place(cols):
     rng = np.random.default_rng(cols)
