@@ -7,10 +7,16 @@
 // lane takes 16 consecutive columns of its rows, one 16-byte load of a packed
 // tile's row, and of its token's row, and they serve four instructions.
 //
-// The eight warps of a CTA take the chunks of its slice of the columns in
-// turn, for RT row tiles, and add their sums in order through shared memory;
-// the CTAs of a cluster take the slices of the same rows and add theirs
-// through distributed shared memory.
+// The warps of a CTA take the chunks of its slice of the columns in turn, for RT
+// row tiles, and add their sums in order through shared memory; where there are few
+// row tiles and long rows, the CTAs of a cluster take the slices of the same rows
+// and add theirs through distributed shared memory.
+//
+// What bounds it: the weights' bytes and, with 16 tokens, x, which every CTA reads
+// and converts for itself (10240 x 8192: 8 tokens 16.2 us, 5.2 TB/s, without
+// loading x 14.5; 16 tokens 20.0 us, without loading x 16.5).  Shares of whole
+// single rows, so that all SMs have the same bytes, were slower at every size (8
+// tokens 18.8 us): their tiles of eight rows use each x for half as many rows.
 #include <cooperative_groups.h>
 
 #include "qr_launch.h"
@@ -20,15 +26,14 @@ namespace qrk {
 
 namespace cg = cooperative_groups;
 
-constexpr int kW8fWarps = 8, kW8fThreads = 32 * kW8fWarps;
-constexpr int kW8fDepth = 4;  // chunks in flight per warp
-
-// NT: tiles of eight tokens; RT: tiles of 16 rows.
-template <int DT, int NT, int RT>
-__global__ void __launch_bounds__(kW8fThreads, 2) w8_few_kernel(W8Args a, int slice) {
+// NT: tiles of eight tokens; RT: tiles of 16 rows; kWarps of a CTA, with kDepth
+// chunks each on their way; CTAS on an SM.
+template <int DT, int NT, int RT, int kWarps, int kDepth, int CTAS>
+__global__ void __launch_bounds__(32 * kWarps, CTAS) w8_few_kernel(W8Args a, int slice) {
     chain_entry();
+    constexpr int kThreads = 32 * kWarps;
     constexpr int kRows = 16 * RT, kTokens = 8 * NT, kValues = kRows * kTokens;
-    __shared__ float s_part[kW8fWarps][kTokens][kRows + 4];
+    __shared__ float s_part[kWarps][kTokens][kRows + 4];
     __shared__ float s_sum[kValues];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -47,7 +52,7 @@ __global__ void __launch_bounds__(kW8fThreads, 2) w8_few_kernel(W8Args a, int sl
     for (int n = 0; n < NT; ++n) xp[n] = a.x + min(n * 8 + g, tokens - 1) * a.x_stride + first * 64ll + t * 16;
     const int cols = a.cols - first * 64 - t * 16;  // of this lane's part of the slice
 
-    uint4 w[kW8fDepth][RT][2], x[kW8fDepth][NT];
+    uint4 w[kDepth][RT][2], x[kDepth][NT];
     auto fetch = [&](int d, int i) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -58,14 +63,14 @@ __global__ void __launch_bounds__(kW8fThreads, 2) w8_few_kernel(W8Args a, int sl
             x[d][n] = n * 8 + g < tokens ? load16_codes(xp[n] + i * 64, cols - i * 64) : make_uint4(0, 0, 0, 0);
     };
 #pragma unroll
-    for (int d = 0; d < kW8fDepth; ++d)
-        if (warp + d * kW8fWarps < count) fetch(d, warp + d * kW8fWarps);
+    for (int d = 0; d < kDepth; ++d)
+        if (warp + d * kWarps < count) fetch(d, warp + d * kWarps);
 
     float acc[RT][NT][4] = {};
-    for (int i0 = warp; i0 < count; i0 += kW8fDepth * kW8fWarps) {
+    for (int i0 = warp; i0 < count; i0 += kDepth * kWarps) {
 #pragma unroll
-        for (int d = 0; d < kW8fDepth; ++d) {
-            const int i = i0 + d * kW8fWarps;
+        for (int d = 0; d < kDepth; ++d) {
+            const int i = i0 + d * kWarps;
             if (i >= count) break;
             uint32_t b[NT][8];
 #pragma unroll
@@ -87,7 +92,7 @@ __global__ void __launch_bounds__(kW8fThreads, 2) w8_few_kernel(W8Args a, int sl
                     for (int n = 0; n < NT; ++n) mma_f16_acc(acc[r][n], f, b[n][2 * j], b[n][2 * j + 1]);
                 }
             }
-            const int next = i + kW8fDepth * kW8fWarps;
+            const int next = i + kDepth * kWarps;
             if (next < count) fetch(d, next);
         }
     }
@@ -104,15 +109,15 @@ __global__ void __launch_bounds__(kW8fThreads, 2) w8_few_kernel(W8Args a, int sl
         if (m < tokens && tile0 * 16ll + row < a.rows)
             a.y[m * a.y_stride + tile0 * 16ll + row] = narrow1<DT>(v * a.x_scales[m] * scales[row]);
     };
-    for (int i = tid; i < kValues; i += kW8fThreads) {
+    for (int i = tid; i < kValues; i += kThreads) {
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kW8fWarps; ++k) v += s_part[k][i / kRows][i % kRows];
+        for (int k = 0; k < kWarps; ++k) v += s_part[k][i / kRows][i % kRows];
         if (splits == 1) store(i, v); else s_sum[i] = v;
     }
     if (splits == 1) return;
     cluster.sync();
-    for (int i = kValues * split / splits + tid; i < kValues * (split + 1) / splits; i += kW8fThreads) {
+    for (int i = kValues * split / splits + tid; i < kValues * (split + 1) / splits; i += kThreads) {
         float v = 0.0f;
         for (int c = 0; c < splits; ++c) v += cluster.map_shared_rank(s_sum, c)[i];
         store(i, v);
@@ -120,14 +125,15 @@ __global__ void __launch_bounds__(kW8fThreads, 2) w8_few_kernel(W8Args a, int sl
     cluster.sync();  // no CTA leaves while another reads its sums
 }
 
-template <int DT, int NT, int RT>
-static cudaError_t run_w8_few(const W8Args &a, cudaStream_t s) {
-    cudaError_t err = cudaSuccess;
-    const int sms = sm_count(&err);
-    if (sms <= 0) return err;
+template <int DT, int NT, int RT, int kWarps, int kDepth, int CTAS>
+static cudaError_t run_w8_few(const W8Args &a, int sms, cudaStream_t s) {
     const long long groups = (a.l.row_tiles + RT - 1) / RT;
+    // a cluster costs some 2.4 us (8 tokens through 8192 x 1024: one slice 3.5 us, two
+    // 5.9), which slices save where they leave fewer rounds of loads to few CTAs
+    // (8 tokens through 1280 x 8192: one slice 7.7 us, four 4.7)
     int splits = 1;
-    while (splits < 8 && groups * splits < 2 * sms && a.l.chunks / (2 * splits) >= kW8fWarps) splits *= 2;
+    if (2 * groups < 3 * sms && a.l.chunks > 2 * kWarps * kDepth)
+        while (splits < 8 && groups * splits < 2 * sms && a.l.chunks / (2 * splits) >= kWarps) splits *= 2;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -136,17 +142,32 @@ static cudaError_t run_w8_few(const W8Args &a, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(groups * splits));
-    cfg.blockDim = kW8fThreads;
+    cfg.blockDim = 32 * kWarps;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, w8_few_kernel<DT, NT, RT>, a, (a.l.chunks + splits - 1) / splits);
+    cfg.numAttrs = splits > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, w8_few_kernel<DT, NT, RT, kWarps, kDepth, CTAS>, a,
+                                             (a.l.chunks + splits - 1) / splits);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <int DT>
+static cudaError_t pick_w8_few(const W8Args &a, cudaStream_t s) {
+    cudaError_t err = cudaSuccess;
+    const int sms = sm_count(&err);
+    if (sms <= 0) return err;
+    if (a.tokens <= 8) {
+        // many row tiles: small CTAs, evenly spread (10240 x 8192: four warps 16.2 us,
+        // eight 17.3); few: more of a tile's columns at once (1280 x 8192: 5.2 and 4.7)
+        return a.l.row_tiles >= 2 * sms ? run_w8_few<DT, 1, 1, 4, 4, 6>(a, sms, s) : run_w8_few<DT, 1, 1, 8, 4, 3>(a, sms, s);
+    }
+    // two row tiles share x; more CTAs rather than more chunks each once there are
+    // enough to fill the SMs (20480 x 5120: 22.3 and 26.4 us; 10240 x 8192: 21.6 and 20.0)
+    return a.l.row_tiles > 6 * sms ? run_w8_few<DT, 2, 2, 4, 2, 5>(a, sms, s) : run_w8_few<DT, 2, 2, 4, 4, 3>(a, sms, s);
+}
+
 cudaError_t launch_w8_few(int dtype, const W8Args &a, cudaStream_t s) {
-    if (a.tokens <= 8) return dtype ? run_w8_few<1, 1, 1>(a, s) : run_w8_few<0, 1, 1>(a, s);
-    return dtype ? run_w8_few<1, 2, 2>(a, s) : run_w8_few<0, 2, 2>(a, s);
+    return dtype ? pick_w8_few<1>(a, s) : pick_w8_few<0>(a, s);
 }
 
 cudaError_t launch_w8_matmul(int dtype, const W8Args &a, void *workspace, cudaStream_t s) {
