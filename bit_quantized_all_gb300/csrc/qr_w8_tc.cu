@@ -55,7 +55,10 @@ __global__ void __launch_bounds__(kWeThreads) w8_expand_kernel(W8Args a, uint8_t
     }
 }
 
-constexpr int kWtThreads = 448;  // warps 0-7 codes, 8 products, 9 x, 10-13 results
+// warps 0-7 codes, 8 products, 9 x, 10-13 results, and up to 128 tokens 14 the
+// packed codes' way in
+template <int N>
+constexpr int kWtThreads = N >= 256 ? 448 : 480;
 constexpr int kWtRows = 128;
 constexpr int kWtStep = 4, kWtA = 2;  // chunks of a step, and buffers of codes in tensor memory, a step each
 constexpr uint32_t kWtColD = kWtA * 32 * kWtStep, kWtColumns = 512;
@@ -64,12 +67,22 @@ constexpr int kWtMostCtas = 152;  // the workspace has two parts for each
 template <int N>
 struct WtSmem {
     static constexpr int kBlock = N * 128;
-    static constexpr int kX = N >= 256 ? 6 : N >= 128 ? 12 : 16;  // chunks of x
-    static constexpr int kD = N >= 256 ? 1 : 2;                   // accumulators
-    uint8_t x[kX * kBlock];
+    // Up to 128 tokens the weights' bytes bound the kernel, and their way in is deep,
+    // through shared memory; with 256 tokens x fills that, and the products leave
+    // time for two steps in registers (64 tokens through 10240 x 8192: XX).
+    static constexpr bool kStaged = N < 256;
+    static constexpr int kW = kStaged ? (N >= 128 ? 2 : N >= 64 ? 3 : 4) : 1;  // steps of packed codes
+    // x: chunks that are handed on together (a wait and a commit take the products'
+    // warp some 150 cycles, four chunks' products of 64 tokens run for 512), and
+    // buffers of them
+    static constexpr int kXc = N >= 256 ? 1 : N >= 128 ? 2 : 4;
+    static constexpr int kX = N >= 256 ? 6 : N >= 128 ? 4 : N >= 64 ? 3 : 4;
+    static constexpr int kD = N >= 256 ? 1 : 2;  // accumulators
+    uint8_t x[kX * kXc * kBlock];
+    uint8_t codes[kStaged ? kW : 1][8][kStaged ? kWtStep * 1024 : 16];  // by warp: its row tile
     uint8_t out[4][32 * 80];  // by warp: 32 tokens of 32 rows
     float x_scale[4][N];      // by warp
-    uint64_t a_full[kWtA], a_done[kWtA], x_full[kX], x_done[kX], d_full[kD], d_done[kD];
+    uint64_t a_full[kWtA], a_done[kWtA], x_full[kX], x_done[kX], d_full[kD], d_done[kD], w_full[kW], w_done[kW];
     uint32_t tmem;
     int fail;
 };
@@ -117,7 +130,7 @@ struct W8Walk {
 };
 
 template <int DT, int N>
-__global__ void __launch_bounds__(kWtThreads, 1)
+__global__ void __launch_bounds__(kWtThreads<N>, 1)
     w8_tc_kernel(W8Args a, W8Shares shares, const uint8_t *x16, float *parts, unsigned *timeouts) {
     using S = WtSmem<N>;
     extern __shared__ uint8_t raw[];
@@ -138,6 +151,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             mbar_init(&sm.d_full[i], 1);
             mbar_init(&sm.d_done[i], 4);
         }
+        for (int i = 0; i < S::kW; ++i) {
+            mbar_init(&sm.w_full[i], 1);
+            mbar_init(&sm.w_done[i], 8);
+        }
         mbar_init_fence();
         sm.fail = 0;
     }
@@ -150,52 +167,77 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     W8Walk at(shares, blockIdx.x);
 
     if (warp < 8) {
-        // ---- codes: a row tile of 16, two steps of them on their way in registers
-        W8Walk ahead = at;
-        const int mine = 2 * quarter + (warp >> 2);
-        uint4 w[2][kWtStep][2];
-        auto fetch = [&](int b) {
-            if (ahead.left <= 0) return;
-            const int n = ahead.step();
-            const long long tile = min(ahead.row_tile * (kWtRows / 16) + mine, a.l.row_tiles - 1);
-            const uint4 *const src = reinterpret_cast<const uint4 *>(a.packed) + (tile * a.l.chunks + ahead.chunk) * 64 + lane;
-#pragma unroll
-            for (int u = 0; u < kWtStep; ++u)
-                if (u < n) {
-                    w[b][u][0] = __ldg(src + u * 64);
-                    w[b][u][1] = __ldg(src + u * 64 + 32);
-                }
-            ahead.advance(n);
-        };
-        fetch(0);
-        fetch(1);
+        // ---- codes: a row tile of 16
         const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32 + (warp >> 2) * 16) << 16);
-        bool ok = true;
-        for (int round = 0; at.left > 0 && ok; ++round) {
+        // a chunk's packed codes to its place as the A operand
+        auto convert = [&](const uint4 &u, const uint4 &l, int b, int k) {
+            const uint32_t up[4] = {u.x, u.y, u.z, u.w}, low[4] = {l.x, l.y, l.z, l.w};
+            uint32_t v[16];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (at.left <= 0) break;
-                if (round > 0) ok = tc_wait_warp(&sm.a_done[b], (round - 1) & 1, fail, timeouts);
+            for (int j = 0; j < 4; ++j) {
+                weights_f16(up[j], v[4 * j], v[4 * j + 1]);
+                weights_f16(low[j], v[4 * j + 2], v[4 * j + 3]);
+            }
+            tc_st_fragments(to + b * (32 * kWtStep) + k * 32, v);  // (past the step's last chunk: unused)
+        };
+        auto hand_on = [&](int b) {
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.a_full[b]);
+        };
+        bool ok = true;
+        if constexpr (S::kStaged) {
+            for (unsigned p = 0; at.left > 0; ++p) {
+                const unsigned b = p % kWtA, ws = p % S::kW;
+                ok = tc_wait_warp(&sm.w_full[ws], (p / S::kW) & 1, fail, timeouts);
+                const uint32_t from = smem_addr(sm.codes[ws][2 * quarter + (warp >> 2)]) + lane * 16;
+                uint4 w[kWtStep][2];
+#pragma unroll
+                for (int u = 0; u < kWtStep; ++u) w[u][0] = lds128(from + u * 1024), w[u][1] = lds128(from + u * 1024 + 512);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.w_done[ws]);
+                if (ok && p >= kWtA) ok = tc_wait_warp(&sm.a_done[b], (p / kWtA - 1) & 1, fail, timeouts);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int u = 0; u < kWtStep; ++u) {
-                    const uint32_t up[4] = {w[b][u][0].x, w[b][u][0].y, w[b][u][0].z, w[b][u][0].w},
-                                   low[4] = {w[b][u][1].x, w[b][u][1].y, w[b][u][1].z, w[b][u][1].w};
-                    uint32_t v[16];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        weights_f16(up[j], v[4 * j], v[4 * j + 1]);
-                        weights_f16(low[j], v[4 * j + 2], v[4 * j + 3]);
-                    }
-                    tc_st_fragments(to + b * (32 * kWtStep) + u * 32, v);  // (past the step's last chunk: unused)
-                }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.a_full[b]);
+                for (int u = 0; u < kWtStep; ++u) convert(w[u][0], w[u][1], b, u);
+                hand_on(b);
                 at.advance(at.step());
-                fetch(b);
+            }
+        } else {
+            // two steps on their way in registers
+            W8Walk ahead = at;
+            const int mine = 2 * quarter + (warp >> 2);
+            uint4 w[2][kWtStep][2];
+            auto fetch = [&](int b) {
+                if (ahead.left <= 0) return;
+                const int n = ahead.step();
+                const long long tile = min(ahead.row_tile * (kWtRows / 16) + mine, a.l.row_tiles - 1);
+                const uint4 *const src = reinterpret_cast<const uint4 *>(a.packed) + (tile * a.l.chunks + ahead.chunk) * 64 + lane;
+#pragma unroll
+                for (int u = 0; u < kWtStep; ++u)
+                    if (u < n) {
+                        w[b][u][0] = __ldg(src + u * 64);
+                        w[b][u][1] = __ldg(src + u * 64 + 32);
+                    }
+                ahead.advance(n);
+            };
+            fetch(0);
+            fetch(1);
+            for (int round = 0; at.left > 0 && ok; ++round) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    if (at.left <= 0) break;
+                    if (round > 0) ok = tc_wait_warp(&sm.a_done[b], (round - 1) & 1, fail, timeouts);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int u = 0; u < kWtStep; ++u) convert(w[b][u][0], w[b][u][1], b, u);
+                    hand_on(b);
+                    at.advance(at.step());
+                    fetch(b);
+                }
             }
         }
     } else if (warp == 8) {
@@ -212,16 +254,20 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             while (n > 0 && ok) {
                 const int s = p % kWtA, chunks = at.step();
                 ok = tc_wait_warp(&sm.a_full[s], (p / kWtA) & 1, fail, timeouts);
-                for (int u = 0; u < chunks && ok; ++u, ++i) {
+                for (int u0 = 0; u0 < chunks && ok; u0 += S::kXc, ++i) {
                     const int xs = i % S::kX;
                     ok = tc_wait_warp(&sm.x_full[xs], (i / S::kX) & 1, fail, timeouts);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t x = smem_addr(sm.x) + xs * S::kBlock, codes = tmem + s * (32 * kWtStep) + u * 32;
+                    const uint32_t x = smem_addr(sm.x) + xs * (S::kXc * S::kBlock), codes = tmem + s * (32 * kWtStep) + u0 * 32;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        tc_mma_ts(leader, tmem + kWtColD + d * N, codes + j * 8, smem_desc(x + j * 32, 16, 1024), kDesc,
-                                  add || j > 0);
+                    for (int k = 0; k < S::kXc; ++k) {
+                        if (u0 + k >= chunks) break;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            tc_mma_ts(leader, tmem + kWtColD + d * N, codes + k * 32 + j * 8,
+                                      smem_desc(x + k * S::kBlock + j * 32, 16, 1024), kDesc, add || k + j > 0);
+                    }
                     add = true;
                     tc_commit(leader, &sm.x_done[xs]);
                 }
@@ -236,22 +282,47 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (!ok) mbar_wait(&sm.d_full[d], (g / S::kD) & 1);
         }
     } else if (warp == 9) {
-        // ---- x: a chunk's block is one copy
+        // ---- x: the blocks of consecutive chunks are one copy
         if (lane == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
             unsigned i = 0;
-            for (; at.left > 0; ++i) {
-                const int xs = i % S::kX;
-                if (i >= S::kX && !tc_wait(&sm.x_done[xs], (i / S::kX - 1) & 1, fail, timeouts)) break;
-                mbar_arrive_expect_tx(&sm.x_full[xs], S::kBlock);
-                bulk_copy_g2s(sm.x + xs * S::kBlock, x16 + (at.token_tile * at.chunks + at.chunk) * S::kBlock, S::kBlock,
-                              &sm.x_full[xs]);
-                at.advance(1);
+            for (bool ok = true; at.left > 0 && ok;) {
+                const int chunks = at.step();
+                for (int u0 = 0; u0 < chunks; u0 += S::kXc, ++i) {
+                    const int xs = i % S::kX;
+                    if (i >= S::kX) ok = tc_wait(&sm.x_done[xs], (i / S::kX - 1) & 1, fail, timeouts);
+                    if (!ok) break;
+                    const uint32_t bytes = min(S::kXc, chunks - u0) * S::kBlock;
+                    mbar_arrive_expect_tx(&sm.x_full[xs], bytes);
+                    bulk_copy_g2s(sm.x + xs * (S::kXc * S::kBlock), x16 + (at.token_tile * at.chunks + at.chunk + u0) * S::kBlock,
+                                  bytes, &sm.x_full[xs]);
+                }
+                at.advance(chunks);
             }
             // none of the copies is on its way when the CTA leaves
             for (unsigned k = i < S::kX ? 0 : i - S::kX; k < i; ++k) mbar_wait(&sm.x_full[k % S::kX], (k / S::kX) & 1);
         }
         __syncwarp();
+    } else if (warp == 14) {
+        // ---- the packed codes' way in: a step of a row tile is one copy
+        if constexpr (S::kStaged) {
+            if (lane == 0) {
+                unsigned p = 0;
+                for (; at.left > 0; ++p) {
+                    const unsigned ws = p % S::kW;
+                    if (p >= S::kW && !tc_wait(&sm.w_done[ws], (p / S::kW - 1) & 1, fail, timeouts)) break;
+                    const int n = at.step();
+                    mbar_arrive_expect_tx(&sm.w_full[ws], 8 * n * 1024);
+                    for (int k = 0; k < 8; ++k) {
+                        const long long tile = min(at.row_tile * (kWtRows / 16) + k, a.l.row_tiles - 1);
+                        bulk_copy_g2s(sm.codes[ws][k], a.packed + (tile * a.l.chunks + at.chunk) * 1024, n * 1024, &sm.w_full[ws]);
+                    }
+                    at.advance(n);
+                }
+                for (unsigned k = p < S::kW ? 0 : p - S::kW; k < p; ++k) mbar_wait(&sm.w_full[k % S::kW], (k / S::kW) & 1);
+            }
+            __syncwarp();
+        }
     } else {
         // ---- results: a thread per row
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -328,40 +399,45 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 }
 
 // Adds the parts of the tiles that several CTAs share: block x is the tile in
-// which CTA x's share ends, y a group of 32 tokens of it.
+// which CTA x's share ends, y a group of 32 tokens of it.  What is not a part (the
+// scales) was there before the product began, and is read before its end.
 template <int DT>
 __global__ void __launch_bounds__(256) w8_join_kernel(W8Args a, W8Shares shares, const float *parts, int n) {
-    chain_entry();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long end = shares.begin(blockIdx.x + 1), tile = (end - 1) / shares.chunks;
     const long long from = tile * shares.chunks, to = from + shares.chunks;
-    if (end == to || shares.owner(from) != static_cast<int>(blockIdx.x)) return;  // whole, or another's to add
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long token0 = tile / shares.row_ctas * n + blockIdx.y * 32 + warp;  // and every eighth from there
+    const long long row = tile % shares.row_ctas * kWtRows + lane * 4;
+    // nothing where the tile is whole, or another block's to add
+    const bool mine = end != to && shares.owner(from) == static_cast<int>(blockIdx.x) && token0 < a.tokens && row < a.rows;
     const int last = shares.owner(to - 1);
-    const long long token0 = tile / shares.row_ctas * n + blockIdx.y * 32;
-    const long long row = tile % shares.row_ctas * kWtRows + (threadIdx.x & 31) * 4;
-    if (token0 >= a.tokens || row >= a.rows) return;
-    const int col = blockIdx.y * 32 + (threadIdx.x >> 5);  // and every eighth from there
+    float4 scale = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float x_scale[4];
+    if (mine) scale = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.packed + a.l.scales_at) + row);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x_scale[k] = mine && token0 + 8 * k < a.tokens ? a.x_scales[token0 + 8 * k] : 0.0f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!mine) return;
+    const float4 *const p = reinterpret_cast<const float4 *>(parts) + (blockIdx.y * 32 + warp) * (kWtRows / 4) + lane;
+    const long long pitch = static_cast<long long>(kWtRows / 4) * n;  // of a part; CTA c's are 2 c and 2 c + 1
     float4 sum[4];
-#pragma unroll 2
-    for (int c = blockIdx.x; c <= last; ++c) {
-        const float4 *const p = reinterpret_cast<const float4 *>(parts + (2ll * c + (c == blockIdx.x)) * (kWtRows * n)) +
-                                col * (kWtRows / 4) + (threadIdx.x & 31);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k] = __ldcg(p + (2ll * blockIdx.x + 1) * pitch + k * 8 * (kWtRows / 4));
+#pragma unroll 4
+    for (int c = blockIdx.x + 1; c <= last; ++c) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float4 v = __ldcg(p + k * 8 * (kWtRows / 4));
-            if (c == blockIdx.x)
-                sum[k] = v;
-            else
-                sum[k].x += v.x, sum[k].y += v.y, sum[k].z += v.z, sum[k].w += v.w;
+            const float4 v = __ldcg(p + 2ll * c * pitch + k * 8 * (kWtRows / 4));
+            sum[k].x += v.x, sum[k].y += v.y, sum[k].z += v.z, sum[k].w += v.w;
         }
     }
-    const float *const scales = reinterpret_cast<const float *>(a.packed + a.l.scales_at) + row;
-    const float4 scale = *reinterpret_cast<const float4 *>(scales);
     const bool vector = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0 && a.y_stride % 4 == 0 && row + 4 <= a.rows;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const long long token = token0 + (threadIdx.x >> 5) + 8 * k;
+        const long long token = token0 + 8 * k;
         if (token >= a.tokens) break;
-        const float s = a.x_scales[token];
+        const float s = x_scale[k];
         const float y[4] = {sum[k].x * s * scale.x, sum[k].y * s * scale.y, sum[k].z * s * scale.z, sum[k].w * s * scale.w};
         uint16_t *const to_y = a.y + token * a.y_stride + row;
         if (vector)
@@ -400,7 +476,7 @@ static cudaError_t run_w8_tc(const W8Args &a, uint8_t *workspace, int shift, cud
     const long long few = a.l.chunks < 8 ? tiles : shares.all / 8;
     if (few < sms) shares.ctas = static_cast<int>(few > 1 ? few : 1);
     float *const parts = reinterpret_cast<float *>(workspace + w8_x16_bytes(a.tokens, a.l.chunks, shift));
-    err = launch_chained(kern, shares.ctas, kWtThreads, bytes, s, a, shares, static_cast<const uint8_t *>(workspace), parts,
+    err = launch_chained(kern, shares.ctas, kWtThreads<N>, bytes, s, a, shares, static_cast<const uint8_t *>(workspace), parts,
                          timeouts);
     if (err != cudaSuccess) return err;
     bool joined = false;
