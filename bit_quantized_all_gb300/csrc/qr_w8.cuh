@@ -19,6 +19,7 @@ __device__ __forceinline__ void weights_f16(uint32_t w, uint32_t &lo, uint32_t &
 __device__ __forceinline__ uint4 load16_codes(const int8_t *p, int have) {
     if (have >= 16) return *reinterpret_cast<const uint4 *>(p);
     uint32_t w[4] = {0, 0, 0, 0};
+    if (have <= 0) return make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 15; ++i)
         if (i < have) w[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i & 3));

@@ -28,23 +28,24 @@ constexpr int kWeThreads = 256;
 
 // x's codes as fp16: a block of N tokens x 64 columns is N * 128 bytes, swizzled.
 // A thread takes 32 codes, half of a token's part of a chunk: pieces j, j + 2, ...
-__global__ void __launch_bounds__(kWeThreads) w8_expand_kernel(W8Args a, uint8_t *to, int n_shift) {
+__global__ void __launch_bounds__(kWeThreads) w8_expand_kernel(W8Args a, uint8_t *to, int n) {
     // the product may start once everything before this kernel is complete: until
     // its own wait it reads the weights only
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int n = 1 << n_shift, chunks = a.l.chunks;
+    const int chunks = a.l.chunks;
     // eight tokens of two chunks a warp
     const long long token = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 1 & 7);
     if (token >= a.tokens) return;
-    const int j = threadIdx.x & 1, row = static_cast<int>(token & (n - 1));
+    const unsigned tile = static_cast<unsigned>(token) / n;  // (tokens are below 2^31)
+    const int j = threadIdx.x & 1, row = static_cast<int>(token - static_cast<long long>(tile) * n);
     const int8_t *const src = a.x + token * a.x_stride + j * 32;
-    uint8_t *const dst = to + ((token >> n_shift) * chunks << (n_shift + 7));
+    uint8_t *const dst = to + static_cast<long long>(tile) * chunks * n * 128;
     for (int c = blockIdx.y * (kWeThreads / 16) + (threadIdx.x >> 4); c < chunks; c += gridDim.y * (kWeThreads / 16)) {
         const int have = a.cols - c * 64 - j * 32;
         const uint4 p = load16_codes(src + c * 64, have), q = load16_codes(src + c * 64 + 16, have - 16);
         const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
-        uint8_t *const block = dst + (static_cast<long long>(c) << (n_shift + 7));
+        uint8_t *const block = dst + static_cast<long long>(c) * n * 128;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint4 o;
@@ -60,13 +61,16 @@ __global__ void __launch_bounds__(kWeThreads) w8_expand_kernel(W8Args a, uint8_t
 template <int N>
 constexpr int kWtThreads = N >= 256 ? 448 : 480;
 constexpr int kWtRows = 128;
-constexpr int kWtStep = 4, kWtA = 2;  // chunks of a step, and buffers of codes in tensor memory, a step each
-constexpr uint32_t kWtColD = kWtA * 32 * kWtStep, kWtColumns = 512;
+constexpr uint32_t kWtColumns = 512;  // of tensor memory: codes, then accumulators
 constexpr int kWtMostCtas = 152;  // the workspace has two parts for each
 
 template <int N>
 struct WtSmem {
     static constexpr int kBlock = N * 128;
+    // chunks of a step, and buffers of codes in tensor memory, a step each: the next
+    // step's codes must be there when a step's products end, XX
+    static constexpr int kStep = 4, kA = N <= 64 ? 3 : 2;
+    static constexpr uint32_t kColD = kA * 32 * kStep;
     // Up to 128 tokens the weights' bytes bound the kernel, and their way in is deep,
     // through shared memory; with 256 tokens x fills that, and the products leave
     // time for two steps in registers (64 tokens through 10240 x 8192: XX).
@@ -79,41 +83,45 @@ struct WtSmem {
     static constexpr int kX = N >= 256 ? 6 : N >= 128 ? 4 : N >= 64 ? 3 : 4;
     static constexpr int kD = N >= 256 ? 1 : 2;  // accumulators
     uint8_t x[kX * kXc * kBlock];
-    uint8_t codes[kStaged ? kW : 1][8][kStaged ? kWtStep * 1024 : 16];  // by warp: its row tile
+    uint8_t codes[kStaged ? kW : 1][8][kStaged ? kStep * 1024 : 16];  // by warp: its row tile
     uint8_t out[4][32 * 80];  // by warp: 32 tokens of 32 rows
     float x_scale[4][N];      // by warp
-    uint64_t a_full[kWtA], a_done[kWtA], x_full[kX], x_done[kX], d_full[kD], d_done[kD], w_full[kW], w_done[kW];
+    uint64_t a_full[kA], a_done[kA], x_full[kX], x_done[kX], d_full[kD], d_done[kD], w_full[kW], w_done[kW];
     uint32_t tmem;
     int fail;
 };
 
 // The division of the chunks: all = tiles * chunks of them over `ctas`.
 struct W8Shares {
-    long long all;
-    int chunks, row_ctas, ctas;
+    long long all, each;  // each = all / ctas
+    int rest;             // all % ctas
+    int chunks, row_ctas, ctas, n;  // n: tokens of a tile, a multiple of 16
 
-    __host__ __device__ __forceinline__ long long begin(long long cta) const { return all * cta / ctas; }
-    // the CTA that has chunk `u`
-    __device__ __forceinline__ int owner(long long u) const { return static_cast<int>(((u + 1) * ctas - 1) / all); }
+    __host__ __device__ __forceinline__ long long begin(int cta) const { return each * cta + rest * cta / ctas; }
+    // (64-bit divisions take hundreds of cycles at a kernel's start)
+    __device__ __forceinline__ long long divide(long long x, int d) const {
+        return all <= 0x7fffffff ? static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(d)) : x / d;
+    }
 };
 
-// Walks a CTA's chunks, a step of up to kWtStep chunks of one tile at a time.
+// Walks a CTA's chunks, a step of up to STEP chunks of one tile at a time.
+template <int STEP>
 struct W8Walk {
     long long left;
     int chunk, chunks, row_tile, row_ctas;
     long long token_tile;
 
     __device__ __forceinline__ W8Walk(const W8Shares &s, int cta) {
-        const long long u = s.begin(cta), tile = u / s.chunks;
+        const long long u = s.begin(cta), tile = s.divide(u, s.chunks);
         left = s.begin(cta + 1) - u;
         chunk = static_cast<int>(u - tile * s.chunks);
         chunks = s.chunks;
         row_ctas = s.row_ctas;
-        token_tile = tile / row_ctas;
+        token_tile = s.divide(tile, row_ctas);
         row_tile = static_cast<int>(tile - token_tile * row_ctas);
     }
     __device__ __forceinline__ int step() const {
-        return static_cast<int>(min(static_cast<long long>(min(kWtStep, chunks - chunk)), left));
+        return static_cast<int>(min(static_cast<long long>(min(STEP, chunks - chunk)), left));
     }
     // Chunks of this tile that are the CTA's, from here on.
     __device__ __forceinline__ int segment() const {
@@ -135,11 +143,12 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
     using S = WtSmem<N>;
     extern __shared__ uint8_t raw[];
     S &sm = *reinterpret_cast<S *>(raw + ((1024 - (smem_addr(raw) & 1023)) & 1023));
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, block = shares.n * 128;
     int *const fail = &sm.fail;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    W8Walk<S::kStep> at(shares, blockIdx.x);
     if (tid == 0) {
-        for (int i = 0; i < kWtA; ++i) {
+        for (int i = 0; i < S::kA; ++i) {
             mbar_init(&sm.a_full[i], 8);
             mbar_init(&sm.a_done[i], 1);
         }
@@ -164,7 +173,6 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     const int quarter = warp & 3;  // of tensor memory's lanes, that this warp reaches
-    W8Walk at(shares, blockIdx.x);
 
     if (warp < 8) {
         // ---- codes: a row tile of 16
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
                 weights_f16(up[j], v[4 * j], v[4 * j + 1]);
                 weights_f16(low[j], v[4 * j + 2], v[4 * j + 3]);
             }
-            tc_st_fragments(to + b * (32 * kWtStep) + k * 32, v);  // (past the step's last chunk: unused)
+            tc_st_fragments(to + b * (32 * S::kStep) + k * 32, v);  // (past the step's last chunk: unused)
         };
         auto hand_on = [&](int b) {
             tc_wait_st();
@@ -189,34 +197,35 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
         bool ok = true;
         if constexpr (S::kStaged) {
             for (unsigned p = 0; at.left > 0; ++p) {
-                const unsigned b = p % kWtA, ws = p % S::kW;
+                const unsigned b = p % S::kA, ws = p % S::kW;
                 ok = tc_wait_warp(&sm.w_full[ws], (p / S::kW) & 1, fail, timeouts);
                 const uint32_t from = smem_addr(sm.codes[ws][2 * quarter + (warp >> 2)]) + lane * 16;
-                uint4 w[kWtStep][2];
+                uint4 w[S::kStep][2];
 #pragma unroll
-                for (int u = 0; u < kWtStep; ++u) w[u][0] = lds128(from + u * 1024), w[u][1] = lds128(from + u * 1024 + 512);
+                for (int u = 0; u < S::kStep; ++u) w[u][0] = lds128(from + u * 1024), w[u][1] = lds128(from + u * 1024 + 512);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.w_done[ws]);
-                if (ok && p >= kWtA) ok = tc_wait_warp(&sm.a_done[b], (p / kWtA - 1) & 1, fail, timeouts);
+                if (ok && p >= S::kA) ok = tc_wait_warp(&sm.a_done[b], (p / S::kA - 1) & 1, fail, timeouts);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int u = 0; u < kWtStep; ++u) convert(w[u][0], w[u][1], b, u);
+                for (int u = 0; u < S::kStep; ++u) convert(w[u][0], w[u][1], b, u);
                 hand_on(b);
                 at.advance(at.step());
             }
         } else {
             // two steps on their way in registers
-            W8Walk ahead = at;
+            static_assert(S::kStaged || S::kA == 2, "a buffer each");
+            W8Walk<S::kStep> ahead = at;
             const int mine = 2 * quarter + (warp >> 2);
-            uint4 w[2][kWtStep][2];
+            uint4 w[2][S::kStep][2];
             auto fetch = [&](int b) {
                 if (ahead.left <= 0) return;
                 const int n = ahead.step();
                 const long long tile = min(ahead.row_tile * (kWtRows / 16) + mine, a.l.row_tiles - 1);
                 const uint4 *const src = reinterpret_cast<const uint4 *>(a.packed) + (tile * a.l.chunks + ahead.chunk) * 64 + lane;
 #pragma unroll
-                for (int u = 0; u < kWtStep; ++u)
+                for (int u = 0; u < S::kStep; ++u)
                     if (u < n) {
                         w[b][u][0] = __ldg(src + u * 64);
                         w[b][u][1] = __ldg(src + u * 64 + 32);
@@ -233,7 +242,7 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int u = 0; u < kWtStep; ++u) convert(w[b][u][0], w[b][u][1], b, u);
+                    for (int u = 0; u < S::kStep; ++u) convert(w[b][u][0], w[b][u][1], b, u);
                     hand_on(b);
                     at.advance(at.step());
                     fetch(b);
@@ -243,7 +252,7 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
     } else if (warp == 8) {
         // ---- products
         const bool leader = elect_lane();
-        constexpr uint32_t kDesc = mma_desc(N, false);
+        const uint32_t desc = mma_desc(shares.n, false);
         bool ok = true;
         unsigned p = 0, i = 0;
         for (unsigned g = 0; at.left > 0 && ok; ++g) {
@@ -252,21 +261,21 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
             if (g >= S::kD) ok = tc_wait_warp(&sm.d_done[d], (g / S::kD - 1) & 1, fail, timeouts);
             bool add = false;
             while (n > 0 && ok) {
-                const int s = p % kWtA, chunks = at.step();
-                ok = tc_wait_warp(&sm.a_full[s], (p / kWtA) & 1, fail, timeouts);
+                const int s = p % S::kA, chunks = at.step();
+                ok = tc_wait_warp(&sm.a_full[s], (p / S::kA) & 1, fail, timeouts);
                 for (int u0 = 0; u0 < chunks && ok; u0 += S::kXc, ++i) {
                     const int xs = i % S::kX;
                     ok = tc_wait_warp(&sm.x_full[xs], (i / S::kX) & 1, fail, timeouts);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t x = smem_addr(sm.x) + xs * (S::kXc * S::kBlock), codes = tmem + s * (32 * kWtStep) + u0 * 32;
+                    const uint32_t x = smem_addr(sm.x) + xs * (S::kXc * S::kBlock), codes = tmem + s * (32 * S::kStep) + u0 * 32;
 #pragma unroll
                     for (int k = 0; k < S::kXc; ++k) {
                         if (u0 + k >= chunks) break;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            tc_mma_ts(leader, tmem + kWtColD + d * N, codes + k * 32 + j * 8,
-                                      smem_desc(x + k * S::kBlock + j * 32, 16, 1024), kDesc, add || k + j > 0);
+                            tc_mma_ts(leader, tmem + S::kColD + d * N, codes + k * 32 + j * 8,
+                                      smem_desc(x + k * block + j * 32, 16, 1024), desc, add || k + j > 0);
                     }
                     add = true;
                     tc_commit(leader, &sm.x_done[xs]);
@@ -292,9 +301,9 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
                     const int xs = i % S::kX;
                     if (i >= S::kX) ok = tc_wait(&sm.x_done[xs], (i / S::kX - 1) & 1, fail, timeouts);
                     if (!ok) break;
-                    const uint32_t bytes = min(S::kXc, chunks - u0) * S::kBlock;
+                    const uint32_t bytes = min(S::kXc, chunks - u0) * block;
                     mbar_arrive_expect_tx(&sm.x_full[xs], bytes);
-                    bulk_copy_g2s(sm.x + xs * (S::kXc * S::kBlock), x16 + (at.token_tile * at.chunks + at.chunk + u0) * S::kBlock,
+                    bulk_copy_g2s(sm.x + xs * (S::kXc * S::kBlock), x16 + (at.token_tile * at.chunks + at.chunk + u0) * block,
                                   bytes, &sm.x_full[xs]);
                 }
                 at.advance(chunks);
@@ -327,8 +336,7 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
         // ---- results: a thread per row
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const int mine = warp - 10;
-        uint8_t *const stage = sm.out[mine];
-        float *const x_scale = sm.x_scale[mine];
+        const uint32_t stage = smem_addr(sm.out[mine]), x_scale = smem_addr(sm.x_scale[mine]);
         const bool vector = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.y_stride % 8 == 0;
         long long held = -1;  // the tokens whose scales are in shared memory
         bool ok = true;
@@ -336,12 +344,12 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
             const unsigned d = g % S::kD;
             const int n = at.segment();
             const bool whole = n == at.chunks;
-            const long long token0 = at.token_tile * N, row0 = static_cast<long long>(at.row_tile) * kWtRows + quarter * 32;
-            const int tokens = static_cast<int>(min(static_cast<long long>(N), a.tokens - token0));
+            const long long token0 = at.token_tile * shares.n, row0 = static_cast<long long>(at.row_tile) * kWtRows + quarter * 32;
+            const int tokens = static_cast<int>(min(static_cast<long long>(shares.n), a.tokens - token0));
             if (whole && held != at.token_tile) {
                 held = at.token_tile;
                 __syncwarp();
-                for (int m = lane; m < N; m += 32) x_scale[m] = m < tokens ? a.x_scales[token0 + m] : 0.0f;
+                for (int m = lane; m < N; m += 32) sm.x_scale[mine][m] = m < tokens ? a.x_scales[token0 + m] : 0.0f;
                 __syncwarp();
             }
             const float scale = row0 + lane < a.rows ? reinterpret_cast<const float *>(a.packed + a.l.scales_at)[row0 + lane] : 0.0f;
@@ -349,13 +357,13 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
             ok = tc_wait_warp(&sm.d_full[d], (g / S::kD) & 1, fail, timeouts);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kWtColD + d * N;
+            const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + S::kColD + d * N;
 #pragma unroll 1
-            for (int h = 0; h < N / 32; ++h) {
+            for (int h = 0; 32 * h < tokens; ++h) {
                 uint32_t v[32];
                 tc_ld32(lanes + h * 32, v);
                 tc_wait_ld(v);
-                if (h == N / 32 - 1) {
+                if (32 * (h + 1) >= tokens) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.d_done[d]);
@@ -365,24 +373,36 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
                     for (int e = 0; e < 32; ++e) part[(h * 32 + e) * kWtRows] = __uint_as_float(v[e]);
                     continue;
                 }
-                if (h * 32 >= tokens) continue;
+                // (the scales first: loads between the stores would wait for them)
+                float xs[32];
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const uint4 q = lds128(x_scale + (h * 32 + e) * 4);
+                    xs[e] = __uint_as_float(q.x), xs[e + 1] = __uint_as_float(q.y);
+                    xs[e + 2] = __uint_as_float(q.z), xs[e + 3] = __uint_as_float(q.w);
+                }
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    *reinterpret_cast<uint16_t *>(stage + e * 80 + lane * 2) =
-                        narrow1<DT>(__uint_as_float(v[e]) * x_scale[h * 32 + e] * scale);
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + e * 80 + lane * 2),
+                                 "h"(narrow1<DT>(__uint_as_float(v[e]) * xs[e] * scale))
+                                 : "memory");
                 __syncwarp();
                 if (vector && row0 + 32 <= a.rows) {
+                    uint4 o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = lds128(stage + (e * 8 + (lane >> 2)) * 80 + (lane & 3) * 16);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int m = e * 8 + (lane >> 2);
-                        const uint4 o = *reinterpret_cast<const uint4 *>(stage + m * 80 + (lane & 3) * 16);
-                        if (h * 32 + m < tokens)
-                            *reinterpret_cast<uint4 *>(a.y + (token0 + h * 32 + m) * a.y_stride + row0 + (lane & 3) * 8) = o;
+                        const int m = h * 32 + e * 8 + (lane >> 2);
+                        if (m < tokens) *reinterpret_cast<uint4 *>(a.y + (token0 + m) * a.y_stride + row0 + (lane & 3) * 8) = o[e];
                     }
                 } else if (row0 + lane < a.rows) {
-                    for (int m = 0; m < 32 && h * 32 + m < tokens; ++m)
-                        a.y[(token0 + h * 32 + m) * a.y_stride + row0 + lane] =
-                            *reinterpret_cast<const uint16_t *>(stage + m * 80 + lane * 2);
+#pragma unroll 8
+                    for (int m = 0; m < 32; ++m) {
+                        uint16_t y;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(y) : "r"(stage + m * 80 + lane * 2) : "memory");
+                        if (h * 32 + m < tokens) a.y[(token0 + h * 32 + m) * a.y_stride + row0 + lane] = y;
+                    }
                 }
                 __syncwarp();
             }
@@ -399,47 +419,54 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
 }
 
 // Adds the parts of the tiles that several CTAs share: block x is the tile in
-// which CTA x's share ends, y a group of 32 tokens of it.  What is not a part (the
+// which CTA x's share ends, y a group of 16 tokens of it.  What is not a part (the
 // scales) was there before the product began, and is read before its end.
 template <int DT>
-__global__ void __launch_bounds__(256) w8_join_kernel(W8Args a, W8Shares shares, const float *parts, int n) {
+__global__ void __launch_bounds__(256, 6) w8_join_kernel(W8Args a, W8Shares shares, const float *parts, int pitch) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long end = shares.begin(blockIdx.x + 1), tile = (end - 1) / shares.chunks;
-    const long long from = tile * shares.chunks, to = from + shares.chunks;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long token0 = tile / shares.row_ctas * n + blockIdx.y * 32 + warp;  // and every eighth from there
-    const long long row = tile % shares.row_ctas * kWtRows + lane * 4;
+    const long long end = shares.begin(blockIdx.x + 1), tile = shares.divide(end - 1, shares.chunks);
+    const long long from = tile * shares.chunks;
+    const long long token_tile = shares.divide(tile, shares.row_ctas);
+    const long long row = (tile - token_tile * shares.row_ctas) * kWtRows + (threadIdx.x & 31) * 4;
+    const int col = blockIdx.y * 16 + (threadIdx.x >> 5);  // and the eighth from there
+    const long long token = token_tile * shares.n + col;
+    const int have = static_cast<int>(min(a.tokens - token, static_cast<long long>(shares.n - col)));  // tokens from here on
     // nothing where the tile is whole, or another block's to add
-    const bool mine = end != to && shares.owner(from) == static_cast<int>(blockIdx.x) && token0 < a.tokens && row < a.rows;
-    const int last = shares.owner(to - 1);
+    const bool mine = end != from + shares.chunks && shares.begin(blockIdx.x) <= from && have > 0 && row < a.rows;
     float4 scale = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float x_scale[4];
-    if (mine) scale = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.packed + a.l.scales_at) + row);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x_scale[k] = mine && token0 + 8 * k < a.tokens ? a.x_scales[token0 + 8 * k] : 0.0f;
+    float x_scale[2] = {0.0f, 0.0f};
+    if (mine) {
+        scale = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.packed + a.l.scales_at) + row);
+        x_scale[0] = a.x_scales[token];
+        if (have > 8) x_scale[1] = a.x_scales[token + 8];
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!mine) return;
-    const float4 *const p = reinterpret_cast<const float4 *>(parts) + (blockIdx.y * 32 + warp) * (kWtRows / 4) + lane;
-    const long long pitch = static_cast<long long>(kWtRows / 4) * n;  // of a part; CTA c's are 2 c and 2 c + 1
-    float4 sum[4];
+    const float4 *const p = reinterpret_cast<const float4 *>(parts) + col * (kWtRows / 4) + (threadIdx.x & 31);
+    const long long next = static_cast<long long>(kWtRows / 4) * pitch;  // of a part; CTA c's are 2 c and 2 c + 1
+    const long long to = from + shares.chunks;
+    float4 sum[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sum[k] = __ldcg(p + (2ll * blockIdx.x + 1) * pitch + k * 8 * (kWtRows / 4));
-#pragma unroll 4
-    for (int c = blockIdx.x + 1; c <= last; ++c) {
+    for (int k = 0; k < 2; ++k) sum[k] = __ldcg(p + (2ll * blockIdx.x + 1) * next + k * 8 * (kWtRows / 4));
+    for (int c = blockIdx.x + 1; shares.begin(c) < to; c += 2) {
+        const bool two = shares.begin(c + 1) < to;
+        float4 v[2][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 v = __ldcg(p + 2ll * c * pitch + k * 8 * (kWtRows / 4));
-            sum[k].x += v.x, sum[k].y += v.y, sum[k].z += v.z, sum[k].w += v.w;
-        }
+        for (int k = 0; k < 2; ++k) v[0][k] = __ldcg(p + 2ll * c * next + k * 8 * (kWtRows / 4));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) v[1][k] = two ? __ldcg(p + 2ll * (c + 1) * next + k * 8 * (kWtRows / 4)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) sum[k].x += v[i][k].x, sum[k].y += v[i][k].y, sum[k].z += v[i][k].z, sum[k].w += v[i][k].w;
     }
     const bool vector = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0 && a.y_stride % 4 == 0 && row + 4 <= a.rows;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const long long token = token0 + 8 * k;
-        if (token >= a.tokens) break;
+    for (int k = 0; k < 2; ++k) {
+        if (8 * k >= have) break;
         const float s = x_scale[k];
         const float y[4] = {sum[k].x * s * scale.x, sum[k].y * s * scale.y, sum[k].z * s * scale.z, sum[k].w * s * scale.w};
-        uint16_t *const to_y = a.y + token * a.y_stride + row;
+        uint16_t *const to_y = a.y + (token + 8 * k) * a.y_stride + row;
         if (vector)
             *reinterpret_cast<uint2 *>(to_y) = make_uint2(narrow2<DT>(y[0], y[1]), narrow2<DT>(y[2], y[3]));
         else
@@ -447,20 +474,28 @@ __global__ void __launch_bounds__(256) w8_join_kernel(W8Args a, W8Shares shares,
     }
 }
 
-// Tokens of a tile: the fewest that take them all, 256 at most.
-static int w8_token_shift(long long tokens) { return tokens <= 32 ? 5 : tokens <= 64 ? 6 : tokens <= 128 ? 7 : 8; }
-
-static size_t w8_x16_bytes(long long tokens, int chunks, int shift) {
-    return static_cast<size_t>((tokens + (1 << shift) - 1) >> shift << shift) * chunks * 128;
+// Tokens of a tile: 256 at most, in equal shares (129 tokens one tile of 144, 300
+// two of 160).
+static int w8_tile_tokens(long long tokens) {
+    const long long tiles = (tokens + 255) / 256;
+    return static_cast<int>(((tokens + tiles - 1) / tiles + 15) / 16 * 16);
 }
 
+static size_t w8_x16_bytes(long long tokens, int chunks, int n) {
+    return static_cast<size_t>((tokens + n - 1) / n * n) * chunks * 128;
+}
+
+// A buffer's size: of the next 32, 64, 128 or whole 256 tokens, so that it grows
+// with them.
+static int w8_most_tokens(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
+
 size_t w8_workspace(long long tokens, int cols) {
-    const int shift = w8_token_shift(tokens);
-    return w8_x16_bytes(tokens, cols / 64 + (cols % 64 != 0), shift) + (size_t(2) * kWtMostCtas * kWtRows * 4 << shift);
+    const int most = w8_most_tokens(tokens < 256 ? static_cast<int>(tokens) : 256);
+    return w8_x16_bytes(tokens, cols / 64 + (cols % 64 != 0), most) + size_t(2) * kWtMostCtas * kWtRows * 4 * most;
 }
 
 template <int DT, int N>
-static cudaError_t run_w8_tc(const W8Args &a, uint8_t *workspace, int shift, cudaStream_t s) {
+static cudaError_t run_w8_tc(const W8Args &a, uint8_t *workspace, int n, cudaStream_t s) {
     auto kern = w8_tc_kernel<DT, N>;
     const int bytes = sizeof(WtSmem<N>) + 1024;
     cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(kern), bytes);
@@ -470,39 +505,50 @@ static cudaError_t run_w8_tc(const W8Args &a, uint8_t *workspace, int shift, cud
     if (sms > kWtMostCtas) sms = kWtMostCtas;
     unsigned *timeouts = wait_timeout_counter(&err);
     if (!timeouts) return err;
-    const long long tiles = (a.l.row_tiles + 7) / 8 * ((a.tokens + N - 1) / N);
-    W8Shares shares = {tiles * a.l.chunks, a.l.chunks, (a.l.row_tiles + 7) / 8, sms};
-    // at least eight chunks a CTA, or a tile where that is less
-    const long long few = a.l.chunks < 8 ? tiles : shares.all / 8;
-    if (few < sms) shares.ctas = static_cast<int>(few > 1 ? few : 1);
-    float *const parts = reinterpret_cast<float *>(workspace + w8_x16_bytes(a.tokens, a.l.chunks, shift));
+    const long long tiles = (a.l.row_tiles + 7) / 8 * ((a.tokens + n - 1) / n);
+    W8Shares shares = {tiles * a.l.chunks, 0, 0, a.l.chunks, (a.l.row_tiles + 7) / 8, 1, n};
+    // Whole tiles, or even shares and a kernel that joins the parts of the tiles that
+    // they divide: what either takes in microseconds.  A chunk is bound by its
+    // products or its hand-overs; joining takes a launch, the parts' way to L2 and
+    // back, and some time for each part of a tile.
+    const double chunk = (n > 160 ? 2 * n : 320) / 1900.0;
+    shares.ctas = static_cast<int>(tiles < sms ? tiles : sms);
+    double best = static_cast<double>((tiles + shares.ctas - 1) / shares.ctas) * a.l.chunks * chunk;
+    for (int c = sms; c >= 8; c = c * 3 / 4) {
+        const double each = static_cast<double>(shares.all) / c;
+        const double cost = each * chunk + 3.0 + (each < a.l.chunks ? a.l.chunks / each : 1.0) * 0.3 + c * n * (4.0 * kWtRows * 4 / 6e6);
+        if (each >= 4 && cost < best) best = cost, shares.ctas = c;
+    }
+    shares.each = shares.all / shares.ctas;
+    shares.rest = static_cast<int>(shares.all % shares.ctas);
+    float *const parts = reinterpret_cast<float *>(workspace + w8_x16_bytes(a.tokens, a.l.chunks, n));
     err = launch_chained(kern, shares.ctas, kWtThreads<N>, bytes, s, a, shares, static_cast<const uint8_t *>(workspace), parts,
                          timeouts);
     if (err != cudaSuccess) return err;
     bool joined = false;
     for (int c = 1; c < shares.ctas && !joined; ++c) joined = shares.begin(c) % a.l.chunks != 0;
     if (!joined) return cudaSuccess;
-    return launch_chained(w8_join_kernel<DT>, dim3(shares.ctas - 1, N / 32), 256, 0, s, a, shares, static_cast<const float *>(parts), N);
+    return launch_chained(w8_join_kernel<DT>, dim3(shares.ctas - 1, (n + 15) / 16), 256, 0, s, a, shares, static_cast<const float *>(parts), N);  // (parts are N tokens apart)
 }
 
 template <int DT>
-static cudaError_t pick_tokens(int shift, const W8Args &a, uint8_t *workspace, cudaStream_t s) {
-    switch (shift) {
-        case 5: return run_w8_tc<DT, 32>(a, workspace, shift, s);
-        case 6: return run_w8_tc<DT, 64>(a, workspace, shift, s);
-        case 7: return run_w8_tc<DT, 128>(a, workspace, shift, s);
-        default: return run_w8_tc<DT, 256>(a, workspace, shift, s);
+static cudaError_t pick_tokens(int n, const W8Args &a, uint8_t *workspace, cudaStream_t s) {
+    switch (w8_most_tokens(n)) {
+        case 32: return run_w8_tc<DT, 32>(a, workspace, n, s);
+        case 64: return run_w8_tc<DT, 64>(a, workspace, n, s);
+        case 128: return run_w8_tc<DT, 128>(a, workspace, n, s);
+        default: return run_w8_tc<DT, 256>(a, workspace, n, s);
     }
 }
 
 cudaError_t launch_w8_tc(int dtype, const W8Args &a, void *workspace, cudaStream_t s) {
-    const int shift = w8_token_shift(a.tokens);
+    const int n = w8_tile_tokens(a.tokens);
     uint8_t *const to = static_cast<uint8_t *>(workspace);
     const int sweep = (a.l.chunks + kWeThreads / 16 - 1) / (kWeThreads / 16);
     const dim3 grid(static_cast<unsigned>((a.tokens + 7) / 8), static_cast<unsigned>(sweep < 65535 ? sweep : 65535));
-    const cudaError_t err = launch_chained(w8_expand_kernel, grid, kWeThreads, 0, s, a, to, shift);
+    const cudaError_t err = launch_chained(w8_expand_kernel, grid, kWeThreads, 0, s, a, to, n);
     if (err != cudaSuccess) return err;
-    return dtype ? pick_tokens<1>(shift, a, to, s) : pick_tokens<0>(shift, a, to, s);
+    return dtype ? pick_tokens<1>(n, a, to, s) : pick_tokens<0>(n, a, to, s);
 }
 
 }  // namespace qrk
