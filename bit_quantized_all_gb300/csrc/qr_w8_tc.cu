@@ -381,27 +381,39 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
                     xs[e] = __uint_as_float(q.x), xs[e + 1] = __uint_as_float(q.y);
                     xs[e + 2] = __uint_as_float(q.z), xs[e + 3] = __uint_as_float(q.w);
                 }
+                uint16_t y[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = narrow1<DT>(__uint_as_float(v[e]) * xs[e] * scale);
+                if (!vector) {
+                    uint16_t *const to = a.y + (token0 + h * 32) * a.y_stride + row0 + lane;
+                    if (row0 + lane < a.rows) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (h * 32 + e < tokens) to[e * a.y_stride] = y[e];
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + e * 80 + lane * 2),
-                                 "h"(narrow1<DT>(__uint_as_float(v[e]) * xs[e] * scale))
-                                 : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + e * 80 + lane * 2), "h"(y[e]) : "memory");
                 __syncwarp();
-                if (vector && row0 + 32 <= a.rows) {
-                    uint4 o[4];
+                uint4 o[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = lds128(stage + (e * 8 + (lane >> 2)) * 80 + (lane & 3) * 16);
+                for (int e = 0; e < 4; ++e) o[e] = lds128(stage + (e * 8 + (lane >> 2)) * 80 + (lane & 3) * 16);
+                const long long row = row0 + (lane & 3) * 8;
+                const int rows = static_cast<int>(min(a.rows - row, 8ll));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int m = h * 32 + e * 8 + (lane >> 2);
-                        if (m < tokens) *reinterpret_cast<uint4 *>(a.y + (token0 + m) * a.y_stride + row0 + (lane & 3) * 8) = o[e];
-                    }
-                } else if (row0 + lane < a.rows) {
-#pragma unroll 8
-                    for (int m = 0; m < 32; ++m) {
-                        uint16_t y;
-                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(y) : "r"(stage + m * 80 + lane * 2) : "memory");
-                        if (h * 32 + m < tokens) a.y[(token0 + h * 32 + m) * a.y_stride + row0 + lane] = y;
+                for (int e = 0; e < 4; ++e) {
+                    const int m = h * 32 + e * 8 + (lane >> 2);
+                    uint16_t *const to = a.y + (token0 + m) * a.y_stride + row;
+                    if (m >= tokens) break;
+                    if (rows == 8) {
+                        *reinterpret_cast<uint4 *>(to) = o[e];
+                    } else {
+                        const uint32_t w[4] = {o[e].x, o[e].y, o[e].z, o[e].w};
+#pragma unroll
+                        for (int k = 0; k < 7; ++k)
+                            if (k < rows) to[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
                     }
                 }
                 __syncwarp();
