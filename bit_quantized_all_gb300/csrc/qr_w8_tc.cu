@@ -56,10 +56,14 @@ __global__ void __launch_bounds__(kWeThreads) w8_expand_kernel(W8Args a, uint8_t
     }
 }
 
-// warps 0-7 codes, 8 products, 9 x, 10-13 results, and up to 128 tokens 14 the
-// packed codes' way in
+// Warps 0-7 codes, 8 products, 9 x, then those of the results, and up to 128 tokens
+// a last one for the packed codes' way in.  Results: eight warps, or four with 256
+// tokens, where more threads would leave the codes' warps too few registers (512
+// tokens through 10240 x 8192: eight 65 us, four 59).
 template <int N>
-constexpr int kWtThreads = N >= 256 ? 448 : 480;
+constexpr int kWtResults = N >= 256 ? 4 : 8;
+template <int N>
+constexpr int kWtThreads = 32 * (10 + kWtResults<N> + (N < 256));
 constexpr int kWtRows = 128;
 constexpr uint32_t kWtColumns = 512;  // of tensor memory: codes, then accumulators
 constexpr int kWtMostCtas = 152;  // the workspace has two parts for each
@@ -84,8 +88,8 @@ struct WtSmem {
     static constexpr int kD = N >= 256 ? 1 : 2;  // accumulators
     uint8_t x[kX * kXc * kBlock];
     uint8_t codes[kStaged ? kW : 1][8][kStaged ? kStep * 1024 : 16];  // by warp: its row tile
-    uint8_t out[4][32 * 80];  // by warp: 32 tokens of 32 rows
-    float x_scale[4][N];      // by warp
+    uint8_t out[kWtResults<N>][16 * 80];  // by warp: 16 tokens of 32 rows
+    float x_scale[kWtResults<N>][N];      // by warp
     uint64_t a_full[kA], a_done[kA], x_full[kX], x_done[kX], d_full[kD], d_done[kD], w_full[kW], w_done[kW];
     uint32_t tmem;
     int fail;
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
         }
         for (int i = 0; i < S::kD; ++i) {
             mbar_init(&sm.d_full[i], 1);
-            mbar_init(&sm.d_done[i], 4);
+            mbar_init(&sm.d_done[i], kWtResults<N>);
         }
         for (int i = 0; i < S::kW; ++i) {
             mbar_init(&sm.w_full[i], 1);
@@ -312,7 +316,7 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
             for (unsigned k = i < S::kX ? 0 : i - S::kX; k < i; ++k) mbar_wait(&sm.x_full[k % S::kX], (k / S::kX) & 1);
         }
         __syncwarp();
-    } else if (warp == 14) {
+    } else if (warp == 10 + kWtResults<N>) {
         // ---- the packed codes' way in: a step of a row tile is one copy
         if constexpr (S::kStaged) {
             if (lane == 0) {
@@ -333,11 +337,13 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
             __syncwarp();
         }
     } else {
-        // ---- results: a thread per row
+        // ---- results: a thread per row, 16 tokens at a time, kStride apart
         asm volatile("griddepcontrol.wait;" ::: "memory");
+        constexpr int kStride = kWtResults<N> * 4;
         const int mine = warp - 10;
         const uint32_t stage = smem_addr(sm.out[mine]), x_scale = smem_addr(sm.x_scale[mine]);
-        const bool vector = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.y_stride % 8 == 0;
+        const uintptr_t odd = reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(a.y_stride * 2);
+        const int wide = (odd & 15) == 0 ? 16 : (odd & 7) == 0 ? 8 : 2;  // bytes of a store
         long long held = -1;  // the tokens whose scales are in shared memory
         bool ok = true;
         for (unsigned g = 0; at.left > 0; ++g) {
@@ -358,62 +364,73 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + S::kColD + d * N;
+            const int first = (mine >> 2) * 16;
+            if (first >= tokens && lane == 0) mbar_arrive(&sm.d_done[d]);
 #pragma unroll 1
-            for (int h = 0; 32 * h < tokens; ++h) {
-                uint32_t v[32];
-                tc_ld32(lanes + h * 32, v);
+            for (int m0 = first; m0 < tokens; m0 += kStride) {
+                uint32_t v[16];
+                tc_ld16(lanes + m0, v);
                 tc_wait_ld(v);
-                if (32 * (h + 1) >= tokens) {
+                if (m0 + kStride >= tokens) {  // (the accumulator is read)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.d_done[d]);
                 }
                 if (!whole) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) part[(h * 32 + e) * kWtRows] = __uint_as_float(v[e]);
+                    for (int e = 0; e < 16; ++e) part[(m0 + e) * kWtRows] = __uint_as_float(v[e]);
                     continue;
                 }
                 // (the scales first: loads between the stores would wait for them)
-                float xs[32];
+                float xs[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const uint4 q = lds128(x_scale + (h * 32 + e) * 4);
+                for (int e = 0; e < 16; e += 4) {
+                    const uint4 q = lds128(x_scale + (m0 + e) * 4);
                     xs[e] = __uint_as_float(q.x), xs[e + 1] = __uint_as_float(q.y);
                     xs[e + 2] = __uint_as_float(q.z), xs[e + 3] = __uint_as_float(q.w);
                 }
-                uint16_t y[32];
+                uint16_t y[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = narrow1<DT>(__uint_as_float(v[e]) * xs[e] * scale);
-                if (!vector) {
-                    uint16_t *const to = a.y + (token0 + h * 32) * a.y_stride + row0 + lane;
+                for (int e = 0; e < 16; ++e) y[e] = narrow1<DT>(__uint_as_float(v[e]) * xs[e] * scale);
+                if (wide == 2) {
+                    uint16_t *const to = a.y + (token0 + m0) * a.y_stride + row0 + lane;
                     if (row0 + lane < a.rows) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (h * 32 + e < tokens) to[e * a.y_stride] = y[e];
+                        for (int e = 0; e < 16; ++e)
+                            if (m0 + e < tokens) to[e * a.y_stride] = y[e];
                     }
                     continue;
                 }
+                // through shared memory, [token][row], to pieces of a token's rows
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
+                for (int e = 0; e < 16; ++e)
                     asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + e * 80 + lane * 2), "h"(y[e]) : "memory");
                 __syncwarp();
-                uint4 o[4];
+                const int each = wide == 16 ? 8 : 4;  // rows of a piece
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = lds128(stage + (e * 8 + (lane >> 2)) * 80 + (lane & 3) * 16);
-                const long long row = row0 + (lane & 3) * 8;
-                const int rows = static_cast<int>(min(a.rows - row, 8ll));
+                for (int i = 0; i < 4; ++i) {
+                    const int piece = i * 32 + lane, m = wide == 16 ? piece >> 2 : piece >> 3, k = (wide == 16 ? piece & 3 : piece & 7) * each;
+                    if (m >= 16) break;
+                    uint16_t *const to = a.y + (token0 + m0 + m) * a.y_stride + row0 + k;
+                    const int rows = static_cast<int>(min(a.rows - row0 - k, static_cast<long long>(each)));
+                    if (m0 + m >= tokens || rows <= 0) continue;
+                    const uint2 lo = lds64(stage + m * 80 + k * 2);
+                    if (wide == 16) {
+                        const uint2 hi = lds64(stage + m * 80 + k * 2 + 8);
+                        if (rows == 8) {
+                            *reinterpret_cast<uint4 *>(to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                        } else {
+                            const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int m = h * 32 + e * 8 + (lane >> 2);
-                    uint16_t *const to = a.y + (token0 + m) * a.y_stride + row;
-                    if (m >= tokens) break;
-                    if (rows == 8) {
-                        *reinterpret_cast<uint4 *>(to) = o[e];
+                            for (int r = 0; r < 7; ++r)
+                                if (r < rows) to[r] = static_cast<uint16_t>(w[r >> 1] >> (16 * (r & 1)));
+                        }
+                    } else if (rows == 4) {
+                        *reinterpret_cast<uint2 *>(to) = lo;
                     } else {
-                        const uint32_t w[4] = {o[e].x, o[e].y, o[e].z, o[e].w};
 #pragma unroll
-                        for (int k = 0; k < 7; ++k)
-                            if (k < rows) to[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+                        for (int r = 0; r < 3; ++r)
+                            if (r < rows) to[r] = static_cast<uint16_t>((r < 2 ? lo.x : lo.y) >> (16 * (r & 1)));
                     }
                 }
                 __syncwarp();
@@ -479,10 +496,14 @@ __global__ void __launch_bounds__(256, 6) w8_join_kernel(W8Args a, W8Shares shar
         const float s = x_scale[k];
         const float y[4] = {sum[k].x * s * scale.x, sum[k].y * s * scale.y, sum[k].z * s * scale.z, sum[k].w * s * scale.w};
         uint16_t *const to_y = a.y + (token + 8 * k) * a.y_stride + row;
-        if (vector)
-            *reinterpret_cast<uint2 *>(to_y) = make_uint2(narrow2<DT>(y[0], y[1]), narrow2<DT>(y[2], y[3]));
-        else
-            for (int e = 0; e < 4 && row + e < a.rows; ++e) to_y[e] = narrow1<DT>(y[e]);
+        const uint2 o = make_uint2(narrow2<DT>(y[0], y[1]), narrow2<DT>(y[2], y[3]));
+        if (vector) {
+            *reinterpret_cast<uint2 *>(to_y) = o;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (row + e < a.rows) to_y[e] = static_cast<uint16_t>((e < 2 ? o.x : o.y) >> (16 * (e & 1)));
+        }
     }
 }
 
@@ -528,7 +549,7 @@ static cudaError_t run_w8_tc(const W8Args &a, uint8_t *workspace, int n, cudaStr
     double best = static_cast<double>((tiles + shares.ctas - 1) / shares.ctas) * a.l.chunks * chunk;
     for (int c = sms; c >= 8; c = c * 3 / 4) {
         const double each = static_cast<double>(shares.all) / c;
-        const double cost = each * chunk + 3.0 + (each < a.l.chunks ? a.l.chunks / each : 1.0) * 0.3 + c * n * (4.0 * kWtRows * 4 / 6e6);
+        const double cost = each * chunk + 3.0 + (each < a.l.chunks ? a.l.chunks / each : 1.0) * 0.3 + c * n * (4.0 * kWtRows * 4 / 1e7);
         if (each >= 4 && cost < best) best = cost, shares.ctas = c;
     }
     shares.each = shares.all / shares.ctas;
