@@ -56,40 +56,43 @@ __global__ void __launch_bounds__(kWeThreads) w8_expand_kernel(W8Args a, uint8_t
     }
 }
 
-// Warps 0-7 codes, 8 products, 9 x, then those of the results, and up to 128 tokens
-// a last one for the packed codes' way in.  Results: eight warps, or four with 256
-// tokens, where more threads would leave the codes' warps too few registers (512
-// tokens through 10240 x 8192: eight 65 us, four 59).
+// Up to 192 tokens a tile the weights' bytes bound the kernel, or x's and theirs
+// alike: the packed codes come through shared memory, some steps ahead.  With more x
+// fills that, and the products leave time for two steps in the registers of the
+// warps that convert them (1024 tokens through 10240 x 8192: through shared memory
+// 111 us, registers 108; 129 through 20481 x 5123: 39 and 44).
 template <int N>
-constexpr int kWtResults = N >= 256 ? 4 : 8;
+constexpr bool kWtStaged = N <= 192;
+// Warps 0-7 codes, 8 products, 9 x, then those of the results (four where the codes'
+// warps need the registers), and a last one for the packed codes' way in.
 template <int N>
-constexpr int kWtThreads = 32 * (10 + kWtResults<N> + (N < 256));
+constexpr int kWtResults = kWtStaged<N> ? 8 : 4;
+template <int N>
+constexpr int kWtThreads = 32 * (10 + kWtResults<N> + kWtStaged<N>);
 constexpr int kWtRows = 128;
 constexpr uint32_t kWtColumns = 512;  // of tensor memory: codes, then accumulators
 constexpr int kWtMostCtas = 152;  // the workspace has two parts for each
 
+// N: tokens of a tile, at most.
 template <int N>
 struct WtSmem {
     static constexpr int kBlock = N * 128;
-    // chunks of a step, and buffers of codes in tensor memory, a step each: the next
-    // step's codes must be there when a step's products end, XX
+    // chunks of a step; buffers of codes in tensor memory, and of packed ones, a step
+    // each; accumulators
     static constexpr int kStep = 4, kA = N <= 64 ? 3 : 2;
+    static constexpr int kW = !kWtStaged<N> ? 1 : N > 64 ? 2 : N > 32 ? 3 : 4;
+    static constexpr int kD = N > 128 ? 1 : 2;
     static constexpr uint32_t kColD = kA * 32 * kStep;
-    // Up to 128 tokens the weights' bytes bound the kernel, and their way in is deep,
-    // through shared memory; with 256 tokens x fills that, and the products leave
-    // time for two steps in registers (64 tokens through 10240 x 8192: XX).
-    static constexpr bool kStaged = N < 256;
-    static constexpr int kW = kStaged ? (N >= 128 ? 2 : N >= 64 ? 3 : 4) : 1;  // steps of packed codes
+    static_assert(kColD + kD * N <= kWtColumns, "tensor memory");
     // x: chunks that are handed on together (a wait and a commit take the products'
     // warp some 150 cycles, four chunks' products of 64 tokens run for 512), and
     // buffers of them
-    static constexpr int kXc = N >= 256 ? 1 : N >= 128 ? 2 : 4;
-    static constexpr int kX = N >= 256 ? 6 : N >= 128 ? 4 : N >= 64 ? 3 : 4;
-    static constexpr int kD = N >= 256 ? 1 : 2;  // accumulators
+    static constexpr int kXc = N > 128 ? 1 : N > 64 ? 2 : 4;
+    static constexpr int kX = N > 128 ? 6 : N > 64 ? 4 : N > 32 ? 3 : 4;
     uint8_t x[kX * kXc * kBlock];
-    uint8_t codes[kStaged ? kW : 1][8][kStaged ? kStep * 1024 : 16];  // by warp: its row tile
-    uint8_t out[kWtResults<N>][16 * 80];  // by warp: 16 tokens of 32 rows
-    float x_scale[kWtResults<N>][N];      // by warp
+    uint8_t codes[kW][8][kWtStaged<N> ? kStep * 1024 : 16];  // by warp: its row tile
+    uint8_t out[kWtResults<N>][16 * 80];                     // by warp: 16 tokens of 32 rows
+    float x_scale[kWtResults<N>][N];                         // by warp
     uint64_t a_full[kA], a_done[kA], x_full[kX], x_done[kX], d_full[kD], d_done[kD], w_full[kW], w_done[kW];
     uint32_t tmem;
     int fail;
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
             if (lane == 0) mbar_arrive(&sm.a_full[b]);
         };
         bool ok = true;
-        if constexpr (S::kStaged) {
+        if constexpr (kWtStaged<N>) {
             for (unsigned p = 0; at.left > 0; ++p) {
                 const unsigned b = p % S::kA, ws = p % S::kW;
                 ok = tc_wait_warp(&sm.w_full[ws], (p / S::kW) & 1, fail, timeouts);
@@ -218,8 +221,7 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
                 at.advance(at.step());
             }
         } else {
-            // two steps on their way in registers
-            static_assert(S::kStaged || S::kA == 2, "a buffer each");
+            static_assert(S::kA == 2, "a buffer each for two steps");
             W8Walk<S::kStep> ahead = at;
             const int mine = 2 * quarter + (warp >> 2);
             uint4 w[2][S::kStep][2];
@@ -318,28 +320,26 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
         __syncwarp();
     } else if (warp == 10 + kWtResults<N>) {
         // ---- the packed codes' way in: a step of a row tile is one copy
-        if constexpr (S::kStaged) {
-            if (lane == 0) {
-                unsigned p = 0;
-                for (; at.left > 0; ++p) {
-                    const unsigned ws = p % S::kW;
-                    if (p >= S::kW && !tc_wait(&sm.w_done[ws], (p / S::kW - 1) & 1, fail, timeouts)) break;
-                    const int n = at.step();
-                    mbar_arrive_expect_tx(&sm.w_full[ws], 8 * n * 1024);
-                    for (int k = 0; k < 8; ++k) {
-                        const long long tile = min(at.row_tile * (kWtRows / 16) + k, a.l.row_tiles - 1);
-                        bulk_copy_g2s(sm.codes[ws][k], a.packed + (tile * a.l.chunks + at.chunk) * 1024, n * 1024, &sm.w_full[ws]);
-                    }
-                    at.advance(n);
+        if (lane == 0) {
+            unsigned p = 0;
+            for (; at.left > 0; ++p) {
+                const unsigned ws = p % S::kW;
+                if (p >= S::kW && !tc_wait(&sm.w_done[ws], (p / S::kW - 1) & 1, fail, timeouts)) break;
+                const int n = at.step();
+                mbar_arrive_expect_tx(&sm.w_full[ws], 8 * n * 1024);
+                for (int k = 0; k < 8; ++k) {
+                    const long long tile = min(at.row_tile * (kWtRows / 16) + k, a.l.row_tiles - 1);
+                    bulk_copy_g2s(sm.codes[ws][k], a.packed + (tile * a.l.chunks + at.chunk) * 1024, n * 1024, &sm.w_full[ws]);
                 }
-                for (unsigned k = p < S::kW ? 0 : p - S::kW; k < p; ++k) mbar_wait(&sm.w_full[k % S::kW], (k / S::kW) & 1);
+                at.advance(n);
             }
-            __syncwarp();
+            for (unsigned k = p < S::kW ? 0 : p - S::kW; k < p; ++k) mbar_wait(&sm.w_full[k % S::kW], (k / S::kW) & 1);
         }
+        __syncwarp();
     } else {
-        // ---- results: a thread per row, 16 tokens at a time, kStride apart
+        // ---- results: a thread per row, 16 tokens at a time
+        constexpr int kStride = 4 * kWtResults<N>;  // tokens between a warp's groups
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        constexpr int kStride = kWtResults<N> * 4;
         const int mine = warp - 10;
         const uint32_t stage = smem_addr(sm.out[mine]), x_scale = smem_addr(sm.x_scale[mine]);
         const uintptr_t odd = reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(a.y_stride * 2);
@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
                 __syncwarp();
                 const int each = wide == 16 ? 8 : 4;  // rows of a piece
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int piece = i * 32 + lane, m = wide == 16 ? piece >> 2 : piece >> 3, k = (wide == 16 ? piece & 3 : piece & 7) * each;
+                for (int q = 0; q < 4; ++q) {
+                    const int piece = q * 32 + lane, m = wide == 16 ? piece >> 2 : piece >> 3, k = (wide == 16 ? piece & 3 : piece & 7) * each;
                     if (m >= 16) break;
                     uint16_t *const to = a.y + (token0 + m0 + m) * a.y_stride + row0 + k;
                     const int rows = static_cast<int>(min(a.rows - row0 - k, static_cast<long long>(each)));
@@ -520,7 +520,7 @@ static size_t w8_x16_bytes(long long tokens, int chunks, int n) {
 
 // A buffer's size: of the next 32, 64, 128 or whole 256 tokens, so that it grows
 // with them.
-static int w8_most_tokens(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
+static int w8_most_tokens(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 192 ? 192 : 256; }
 
 size_t w8_workspace(long long tokens, int cols) {
     const int most = w8_most_tokens(tokens < 256 ? static_cast<int>(tokens) : 256);
@@ -570,6 +570,7 @@ static cudaError_t pick_tokens(int n, const W8Args &a, uint8_t *workspace, cudaS
         case 32: return run_w8_tc<DT, 32>(a, workspace, n, s);
         case 64: return run_w8_tc<DT, 64>(a, workspace, n, s);
         case 128: return run_w8_tc<DT, 128>(a, workspace, n, s);
+        case 192: return run_w8_tc<DT, 192>(a, workspace, n, s);
         default: return run_w8_tc<DT, 256>(a, workspace, n, s);
     }
 }
