@@ -5,7 +5,11 @@ R ranks each hold a share of the heads, a key/value cache of those heads in 8
 bits and a slice of the output projection in 4 bits.  A step plans its tokens'
 places once, and then every rank appends its keys and values, attends, and
 multiplies by its slice; the partial outputs are summed by ``qr_allreduce``.
-On one GPU the ranks are R sets of buffers, run in turn on one stream.
+``TPAttentionBlock`` begins where the last all-reduce ended: it adds the message
+to the residual, normalises into rows in 8 bits, and every rank makes its
+queries, keys and values from them with its 8-bit projection and turns them by
+their positions.  On one GPU the ranks are R sets of buffers, run in turn on one
+stream.
 
 A step reads its plan's counts back before it writes anything, so it waits once
 for the GPU and cannot be captured in a graph (the calls it makes can); requests
@@ -15,8 +19,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (KVCache, W4Weight, qr_allreduce, qr_kv_append, qr_kv_attention, qr_kv_attention_workspace, qr_kv_plan,
-               qr_w4_matvec)
+from . import (KVCache, KVPlan, Rope, W4Weight, W8Weight, qr_allreduce, qr_kv_append, qr_kv_attention,
+               qr_kv_attention_workspace, qr_kv_plan, qr_rms_norm_q8, qr_rope, qr_w4_matvec, qr_w8_matmul,
+               qr_w8_matmul_workspace)
 
 
 class TPAttentionLayer:
@@ -45,9 +50,13 @@ class TPAttentionLayer:
         Raises RuntimeError where the tokens do not fit the free blocks or the
         table, ValueError where ``new_lens`` are not the queries' tokens; the
         layer is then as it was, but for table entries past its requests' ends."""
+        plan, counts = self._plan(new_lens, q[0].shape[0])
+        return self._attend(plan, counts, zip(q, k, v), max_q)
+
+    def _plan(self, new_lens: torch.Tensor, tokens: int) -> tuple[KVPlan, torch.Tensor]:
+        """The step's plan and its counts, read back; raises as ``step`` does."""
         if self.counts is not None:
             self.release_taken()
-        tokens = q[0].shape[0]
         plan = qr_kv_plan(self.cached, new_lens, self.block_table, self.free_blocks, self.block_size, tokens)
         counts = plan.counts.cpu()
         _, new, short, beyond = counts.tolist()
@@ -55,15 +64,20 @@ class TPAttentionLayer:
             raise RuntimeError(f"the step needs {short} blocks and {beyond} table entries more than there are")
         if new != tokens:
             raise ValueError(f"new_lens bring {new} tokens, the queries are {tokens}")
-        if tokens > self.workspace_tokens:
-            self.workspace = qr_kv_attention_workspace(q[0], self.caches[0], new_lens.numel())
-            self.workspace_tokens = tokens
+        return plan, counts
+
+    def _attend(self, plan: KVPlan, counts: torch.Tensor, ranks, max_q: int) -> torch.Tensor:
+        """The rest of a step, from every rank's (queries, keys, values) in turn."""
         partial = []
-        for rank, cache in enumerate(self.caches):
-            qr_kv_append(cache, k[rank], v[rank], plan.slots)
-            out = qr_kv_attention(q[rank], cache, plan.q_offsets, plan.kv_lens, plan.block_table, max_q=max_q,
+        for cache, weight, (q, k, v) in zip(self.caches, self.weights, ranks):
+            tokens = q.shape[0]
+            if tokens > self.workspace_tokens:
+                self.workspace = qr_kv_attention_workspace(q, cache, plan.kv_lens.numel())
+                self.workspace_tokens = tokens
+            qr_kv_append(cache, k, v, plan.slots)
+            out = qr_kv_attention(q, cache, plan.q_offsets, plan.kv_lens, plan.block_table, max_q=max_q,
                                   workspace=self.workspace)
-            partial.append(qr_w4_matvec(out.view(tokens, -1), self.weights[rank]))
+            partial.append(qr_w4_matvec(out.view(tokens, -1), weight))
         y = qr_allreduce(self.bits, partial)
         self.cached = plan.kv_lens
         self.counts = counts
@@ -81,4 +95,51 @@ class TPAttentionLayer:
         self.counts = None
 
 
-__all__ = ["TPAttentionLayer"]
+class TPAttentionBlock:
+    """A ``TPAttentionLayer`` with what stands before it: the norm of the residual
+    stream, every rank's query, key and value projection and the positions.
+
+    ``norm_weight``: [hidden], the activations' type or fp32; ``qkv``: each
+    rank's ``W8Weight`` of [(q_heads + 2 * kv_heads) * head_dim, hidden], its
+    queries' heads, then its keys', then its values'."""
+
+    def __init__(self, norm_weight: torch.Tensor, qkv: list[W8Weight], rope: Rope, layer: TPAttentionLayer,
+                 eps: float = 1e-6):
+        kv_heads, dim = layer.caches[0].heads, layer.head_dim
+        rows, hidden = qkv[0].rows, norm_weight.shape[0]
+        if len(qkv) != len(layer.caches):
+            raise ValueError(f"{len(qkv)} projections for {len(layer.caches)} ranks")
+        if any(w.rows != rows or w.cols != hidden for w in qkv):
+            raise ValueError(f"every rank's projection must be [{rows}, {hidden}]")
+        self.q_heads = rows // dim - 2 * kv_heads
+        if rows % dim or self.q_heads < kv_heads or self.q_heads % kv_heads:
+            raise ValueError(f"a projection of {rows} rows holds no heads of {dim} for {kv_heads} key heads")
+        if any(w.cols != self.q_heads * dim for w in layer.weights):
+            raise ValueError(f"the layer's weights must have {self.q_heads * dim} columns")
+        self.norm_weight, self.qkv, self.rope, self.layer, self.eps = norm_weight, qkv, rope, layer, eps
+        self.workspace, self.workspace_tokens = None, 0
+
+    def step(self, x: torch.Tensor, residual: torch.Tensor, new_lens: torch.Tensor, max_q: int) -> torch.Tensor:
+        """The block's attention output [tokens, hidden], the next message, from
+        the last one, ``x`` [tokens, hidden], which is added to ``residual`` in
+        place.  ``new_lens``, ``max_q`` and what is raised (before ``residual``
+        or a cache is written) as ``TPAttentionLayer.step``."""
+        tokens = x.shape[0]
+        plan, counts = self.layer._plan(new_lens, tokens)
+        rows = qr_rms_norm_q8(x, self.norm_weight, self.eps, residual)
+        if tokens > self.workspace_tokens:
+            self.workspace, self.workspace_tokens = qr_w8_matmul_workspace(tokens, self.qkv[0]), tokens
+        return self.layer._attend(plan, counts, (self._heads(rows, w, plan, x.dtype) for w in self.qkv), max_q)
+
+    def _heads(self, rows, weight: W8Weight, plan: KVPlan, dtype):
+        """A rank's queries, keys and values, slices of its projection."""
+        y = qr_w8_matmul(rows, weight, dtype, workspace=self.workspace)
+        y = y.view(rows.tokens, -1, self.layer.head_dim)
+        q, rest = y[:, :self.q_heads], y[:, self.q_heads:]
+        kv_heads = rest.shape[1] // 2
+        k, v = rest[:, :kv_heads], rest[:, kv_heads:]
+        qr_rope(q, k, self.rope, plan=plan, out=(q, k))
+        return q, k, v
+
+
+__all__ = ["TPAttentionBlock", "TPAttentionLayer"]
