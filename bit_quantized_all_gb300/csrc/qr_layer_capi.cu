@@ -15,6 +15,8 @@ cudaError_t launch_norm(int dtype, int weight, const NormArgs &a, cudaStream_t s
     return dtype ? launch_norm_typed<1>(weight, a, s) : launch_norm_typed<0>(weight, a, s);
 }
 
+constexpr int kMostCols = 1 << 30;  // so that a loop over a row's values ends below 2^31
+
 cudaStream_t stream_of(qr_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Rows of `width` bytes, `stride` bytes apart.
@@ -45,7 +47,7 @@ qr_status_t norm(qr_dtype_t dtype, int64_t tokens, int cols, const void *x, int6
     if (!x || !weight || !y || (eight && !scales) || (residual_out && !residual)) return QR_ERR_INVALID_ARG;
     if (tokens < 1 || cols < 1 || !(eps > 0.0f) || eps - eps != 0.0f) return QR_ERR_INVALID_ARG;
     if (!dtype_ok(dtype)) return QR_ERR_UNSUPPORTED;
-    if (tokens > INT_MAX || cols > INT_MAX - 128) return QR_ERR_SIZE;
+    if (tokens > INT_MAX || cols > kMostCols) return QR_ERR_SIZE;
     if (!extent(tokens, 1, cols, x_row, 0) || !extent(tokens, 1, cols, y_row, 0) ||
         (residual && !extent(tokens, 1, cols, residual_row, 0)) ||
         (residual_out && !extent(tokens, 1, cols, residual_out_row, 0)))
@@ -76,7 +78,7 @@ QR_EXPORT qr_status_t qr_q8_quantize(qr_dtype_t dtype, int64_t tokens, int cols,
                                      int8_t *codes, int64_t codes_row_stride, float *scales, qr_stream_t stream) {
     if (!x || !codes || !scales || tokens < 1 || cols < 1) return QR_ERR_INVALID_ARG;
     if (!dtype_ok(dtype)) return QR_ERR_UNSUPPORTED;
-    if (tokens > INT_MAX || cols > INT_MAX - 128) return QR_ERR_SIZE;
+    if (tokens > INT_MAX || cols > kMostCols) return QR_ERR_SIZE;
     if (!extent(tokens, 1, cols, x_row_stride, 0) || !extent(tokens, 1, cols, codes_row_stride, 0)) return QR_ERR_SIZE;
     if (!aligned(x, 2) || !aligned(codes, 16) || !aligned(scales, 4) || (tokens > 1 && codes_row_stride % 16))
         return QR_ERR_MISALIGNED;
@@ -104,7 +106,7 @@ QR_EXPORT qr_status_t qr_rms_norm_q8(qr_dtype_t dtype, int64_t tokens, int cols,
 }
 
 QR_EXPORT size_t qr_w8_bytes(int rows, int cols) {
-    if (rows < 1 || cols < 1 || rows > INT_MAX - 128 || cols > INT_MAX - 128) return 0;
+    if (rows < 1 || cols < 1 || rows > kMostCols || cols > kMostCols) return 0;
     return w8_layout(rows, cols).bytes;
 }
 
@@ -132,7 +134,7 @@ QR_EXPORT qr_status_t qr_w8_quantize(qr_dtype_t dtype, int rows, int cols, const
 }
 
 QR_EXPORT size_t qr_w8_matmul_workspace_bytes(int64_t tokens, int cols) {
-    if (tokens < 1 || tokens > INT_MAX - 256 || cols < 1 || cols > INT_MAX - 128) return 0;
+    if (tokens < 1 || tokens > INT_MAX - 256 || cols < 1 || cols > kMostCols) return 0;
     return w8_workspace(tokens, cols);
 }
 

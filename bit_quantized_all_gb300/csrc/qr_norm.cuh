@@ -191,6 +191,10 @@ __global__ void __launch_bounds__(THREADS, WARP || (P == 2 && !EIGHT) ? 2 : 1) n
         uint4 kept[P];          // x itself where there is no weight
         float sum = 0.0f, most = 0.0f;
         if (!AHEAD) load(t);
+        // a warp's last lane reads what the next warp's first one may write, the
+        // residual in place; rows ahead are read before the barrier of the row before
+        if (kLanes < 32 && WARP) __syncwarp();
+        if (kLanes < 32 && !WARP && !AHEAD) __syncthreads();
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             if ((SHIFT || WARP) && !any(p)) break;

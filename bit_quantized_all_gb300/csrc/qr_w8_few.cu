@@ -57,10 +57,10 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) w8_few_kernel(W8Args a, int
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) w[d][r][h] = __ldcs(wp[r] + i * 64 + h * 32);
+            for (int h = 0; h < 2; ++h) w[d][r][h] = __ldcs(wp[r] + i * 64ll + h * 32);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            x[d][n] = n * 8 + g < tokens ? load16_codes(xp[n] + i * 64, cols - i * 64) : make_uint4(0, 0, 0, 0);
+            x[d][n] = n * 8 + g < tokens ? load16_codes(xp[n] + i * 64ll, cols - i * 64) : make_uint4(0, 0, 0, 0);
     };
 #pragma unroll
     for (int d = 0; d < kDepth; ++d)

@@ -48,6 +48,18 @@ def _lib():
     return _L
 
 
+def _rows_of(t, what: str, shape, dtype, device: torch.device) -> tuple[int, int]:
+    """(address, row stride) of a matrix of this shape and dtype on ``device``."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device.index:
+        stride, inner = t.stride()
+        if inner == 1 or shape[1] < 2:
+            return t.data_ptr(), stride
+    _matrix(t, what, shape[1])
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{what} must match x's shape and dtype")
+    raise ValueError(f"{what} must be on {device}")
+
+
 # ---------------------------------------------------------------------------
 # rows in 8 bits
 # ---------------------------------------------------------------------------
@@ -67,6 +79,7 @@ class Q8Rows:
         self.device = _same_device([codes, scales], "Q8Rows")
         self.codes, self.scales = codes, scales
         self.tokens, self.cols = codes.shape
+        self.pitch = codes.stride(0)  # between rows
 
     @classmethod
     def empty(cls, tokens: int, cols: int, device="cuda") -> "Q8Rows":
@@ -89,7 +102,7 @@ def _rows8_out(out, tokens: int, cols: int, device, what: str) -> Q8Rows:
         codes = torch.empty((tokens, cols + pad), dtype=torch.int8, device=device)
         out.codes = codes[:, :cols] if pad else codes
         out.scales = torch.empty(tokens, dtype=torch.float32, device=device)
-        out.device, out.tokens, out.cols = device, tokens, cols
+        out.device, out.tokens, out.cols, out.pitch = device, tokens, cols, cols + pad
         return out
     if not isinstance(out, Q8Rows):
         raise TypeError(f"{what}: out must be a Q8Rows")
@@ -102,18 +115,18 @@ def _rows8_out(out, tokens: int, cols: int, device, what: str) -> Q8Rows:
 
 def qr_q8_quantize(x: torch.Tensor, out: Q8Rows | None = None, stream=None) -> Q8Rows:
     """Rows of fp16/bf16 x [tokens, cols] in 8 bits."""
-    _matrix(x, "x")
     if stream is not None:
+        _matrix(x, "x")
         with _as_current(x.device, stream):
             return qr_q8_quantize(x, out)
+    _matrix(x, "x")
     dt = _dtype_code(x, "x")
     tokens, cols = x.shape
     dev = x.device
     out = _rows8_out(out, tokens, cols, dev, "qr_q8_quantize")
     if tokens and cols:
-        codes = out.codes
-        status = (_L or _lib()).qr_q8_quantize(dt, tokens, cols, x.data_ptr(), x.stride(0), codes.data_ptr(),
-                                               codes.stride(0), out.scales.data_ptr(), _current(dev))
+        status = (_L or _lib()).qr_q8_quantize(dt, tokens, cols, x.data_ptr(), x.stride(0), out.codes.data_ptr(),
+                                               out.pitch, out.scales.data_ptr(), _current(dev))
         if status:
             _check(status, "qr_q8_quantize")
     elif tokens:
@@ -125,59 +138,48 @@ def qr_q8_quantize(x: torch.Tensor, out: Q8Rows | None = None, stream=None) -> Q
 # norm
 # ---------------------------------------------------------------------------
 def _norm(what, x, weight, eps, residual, residual_out, out, eight):
+    _matrix(x, "x")
     dt = _dtype_code(x, "x")
     shape, dtype, dev = x.shape, x.dtype, x.device
     tokens, cols = shape
     wide = isinstance(weight, torch.Tensor) and weight.dtype is torch.float32
-    _int_tensor(weight, "weight", torch.float32 if wide else dtype, (cols,))
-    if weight.device != dev:
+    if not ((wide or isinstance(weight, torch.Tensor) and weight.dtype is dtype) and weight.shape == (cols,)
+            and weight.get_device() == dev.index and weight.is_contiguous()):
+        _int_tensor(weight, "weight", torch.float32 if wide else dtype, (cols,))
         _on(dev, what, weight)
     if not 0.0 < eps < math.inf:
         raise ValueError(f"eps must be finite and above 0, got {eps}")
     if residual is None:
         if residual_out is not None:
             raise ValueError(f"{what}: residual_out without residual")
-        res = (0, 0, 0, 0)
+        at = stride = out_at = out_stride = 0
     else:
-        _matrix(residual, "residual", cols)
-        if residual.dtype is not dtype or residual.shape != shape:
-            raise ValueError("residual must match x's shape and dtype")
-        if residual.device != dev:
-            _on(dev, what, residual)
-        at, stride = residual.data_ptr(), residual.stride(0)
+        at, stride = _rows_of(residual, "residual", shape, dtype, dev)
         if residual_out is None or residual_out is residual:
-            res = (at, stride, at, stride)
+            out_at, out_stride = at, stride
         else:
-            _matrix(residual_out, "residual_out", cols)
-            if residual_out.dtype is not dtype or residual_out.shape != shape:
-                raise ValueError("residual_out must match x's shape and dtype")
-            if residual_out.device != dev:
-                _on(dev, what, residual_out)
-            res = (at, stride, residual_out.data_ptr(), residual_out.stride(0))
+            out_at, out_stride = _rows_of(residual_out, "residual_out", shape, dtype, dev)
     if eight:
         out = _rows8_out(out, tokens, cols, dev, what)
-        y = out.codes
+        if tokens and cols:
+            status = (_L or _lib()).qr_rms_norm_q8(
+                dt, tokens, cols, x.data_ptr(), x.stride(0), at, stride, out_at, out_stride, weight.data_ptr(), wide, eps,
+                out.codes.data_ptr(), out.pitch, out.scales.data_ptr(), _current(dev))
+            if status:
+                _check(status, what)
+        elif tokens:
+            out.scales.zero_()
+        return out
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+        y, y_stride = out.data_ptr(), cols
     else:
-        if out is None:
-            out = torch.empty((tokens, cols), dtype=dtype, device=dev)
-        else:
-            _matrix(out, "out", cols)
-            if out.dtype is not dtype or out.shape != shape:
-                raise ValueError("out must match x's shape and dtype")
-            _on(dev, what, out)
-        y = out
+        y, y_stride = _rows_of(out, "out", shape, dtype, dev)
     if tokens and cols:
-        L = _L or _lib()
-        if eight:
-            status = L.qr_rms_norm_q8(dt, tokens, cols, x.data_ptr(), x.stride(0), *res, weight.data_ptr(), wide, eps,
-                                      y.data_ptr(), y.stride(0), out.scales.data_ptr(), _current(dev))
-        else:
-            status = L.qr_rms_norm(dt, tokens, cols, x.data_ptr(), x.stride(0), *res, weight.data_ptr(), wide, eps,
-                                   y.data_ptr(), y.stride(0), _current(dev))
+        status = (_L or _lib()).qr_rms_norm(dt, tokens, cols, x.data_ptr(), x.stride(0), at, stride, out_at, out_stride,
+                                            weight.data_ptr(), wide, eps, y, y_stride, _current(dev))
         if status:
             _check(status, what)
-    elif tokens and eight:
-        out.scales.zero_()
     return out
 
 
@@ -186,8 +188,8 @@ def qr_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     """h = x + residual (x without one), y = h / sqrt(mean(h^2) + eps) * weight
     for each row of fp16/bf16 x [tokens, cols].  ``residual_out`` (by default
     ``residual`` itself) gets h; ``weight`` is x's type or fp32."""
-    _matrix(x, "x")
     if stream is not None:
+        _matrix(x, "x")
         with _as_current(x.device, stream):
             return qr_rms_norm(x, weight, eps, residual, residual_out, out)
     return _norm("qr_rms_norm", x, weight, eps, residual, residual_out, out, False)
@@ -196,8 +198,8 @@ def qr_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
 def qr_rms_norm_q8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
                    residual_out: torch.Tensor | None = None, out: Q8Rows | None = None, stream=None) -> Q8Rows:
     """qr_rms_norm with its output as rows in 8 bits."""
-    _matrix(x, "x")
     if stream is not None:
+        _matrix(x, "x")
         with _as_current(x.device, stream):
             return qr_rms_norm_q8(x, weight, eps, residual, residual_out, out)
     return _norm("qr_rms_norm_q8", x, weight, eps, residual, residual_out, out, True)
@@ -304,9 +306,8 @@ def qr_w8_matmul(x: Q8Rows, weight: W8Weight, dtype: torch.dtype = torch.bfloat1
             _on(dev, "qr_w8_matmul", workspace)
         elif tokens > 16:
             workspace = torch.empty(qr_w8_matmul_workspace_bytes(tokens, cols), dtype=torch.uint8, device=dev)
-        codes = x.codes
         status = (_L or _lib()).qr_w8_matmul(
-            dt, tokens, codes.data_ptr(), codes.stride(0), x.scales.data_ptr(), rows, cols, weight.packed.data_ptr(),
+            dt, tokens, x.codes.data_ptr(), x.pitch, x.scales.data_ptr(), rows, cols, weight.packed.data_ptr(),
             y.data_ptr(), y.stride(0), 0 if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel(), _current(dev))
         if status:
@@ -371,6 +372,7 @@ class Rope:
         turns = [int(t) for t in np.rint(f / (2 * math.pi) * 2.0 ** 64)]
         self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
         self.layout, self.factor, self.rot_dim, self.device = layout, float(factor), 2 * f.size, self.turns.device
+        self.interleaved, self.address = layout == "interleaved", self.turns.data_ptr()
 
     @classmethod
     def make(cls, rot_dim: int, base: float = 10000.0, layout: str = "half", device="cuda", **scaling) -> "Rope":
@@ -379,15 +381,25 @@ class Rope:
         return cls(frequencies, layout, factor, device)
 
 
-def _heads(t: torch.Tensor, what: str) -> None:
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3 and t.stride(2) == 1:
-        return
+def _heads(t: torch.Tensor, what: str, shape=None, dtype=None, device=None) -> tuple[int, int, int]:
+    """(address, token stride, head stride) of [tokens, heads, head_dim], of this
+    shape and dtype on ``device`` where they are given."""
+    if isinstance(t, torch.Tensor) and t.dim() == 3:
+        token, head, inner = t.stride()
+        if (inner == 1 or t.shape[2] < 2) and t.is_cuda:
+            if shape is None:
+                return t.data_ptr(), token, head
+            if t.dtype is dtype and t.shape == shape and t.get_device() == device.index:
+                return t.data_ptr(), token, head
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{what} must be a tensor [tokens, heads, head_dim]")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor (there is no CPU path)")
     if t.shape[2] > 1 and t.stride(2) != 1:
         raise ValueError(f"{what}: the values of a head must be contiguous")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}")
+    raise ValueError(f"{what} must be on {device}")
 
 
 def qr_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope, positions: torch.Tensor | None = None,
@@ -396,20 +408,18 @@ def qr_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope, positions: torc
     turned by their positions: ``positions`` (int32 [tokens]), or those of a
     step's ``plan`` (tokens past its last one are left alone in ``out``).
     Returns (q, k), new or ``out``; ``out=(q, k)`` turns them in place."""
-    _heads(q, "q")
     if stream is not None:
+        _heads(q, "q")
         with _as_current(q.device, stream):
             return qr_rope(q, k, rope, positions, plan, out)
+    q_in = _heads(q, "q")
     dt = _dtype_code(q, "q")
     shape, dtype, dev = q.shape, q.dtype, q.device
     tokens, q_heads, dim = shape
+    k_in, k_heads = (0, 0, 0), 0
     if k is not None:
-        _heads(k, "k")
-        k_shape = k.shape
-        if k.dtype is not dtype or k_shape[0] != tokens or k_shape[2] != dim:
-            raise ValueError("k must have q's dtype, tokens and head_dim")
-        if k.device != dev:
-            _on(dev, "qr_rope", k)
+        k_heads = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+        k_in = _heads(k, "k", (tokens, k_heads, dim), dtype, dev)
     if rope.rot_dim > dim:
         raise ValueError(f"the table rotates {rope.rot_dim} values of a head, which has {dim}")
     if rope.device != dev:
@@ -418,40 +428,36 @@ def qr_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope, positions: torc
         raise ValueError("either positions or plan")
     if plan is None:
         _int_tensor(positions, "positions", torch.int32, (tokens,))
-        if positions.device != dev:
+        if positions.get_device() != dev.index:
             _on(dev, "qr_rope", positions)
-        where = (positions.data_ptr(), 0, 0, 0)
+        at, requests, offsets, lens = positions.data_ptr(), 0, 0, 0
+        new = torch.empty
     else:
         requests = plan.kv_lens.numel()
         _int_tensor(plan.kv_lens, "plan.kv_lens", torch.int32)
         _int_tensor(plan.q_offsets, "plan.q_offsets", torch.int32, (requests + 1,))
         _on(dev, "qr_rope", plan.kv_lens, plan.q_offsets)
-        where = (0, requests, plan.q_offsets.data_ptr(), plan.kv_lens.data_ptr())
+        at, offsets, lens = 0, plan.q_offsets.data_ptr(), plan.kv_lens.data_ptr()
+        new = torch.zeros  # (tokens that the plan leaves out: not what the memory held)
+    k_at, k_out = (0, 0, 0), None
     if out is None:
-        # (tokens that a plan leaves out: zeros rather than what the memory held)
-        new = torch.empty if plan is None else torch.zeros
         q_out = new(shape, dtype=dtype, device=dev)
-        k_out = None if k is None else new(k_shape, dtype=dtype, device=dev)
+        q_at = q_out.data_ptr(), q_heads * dim, dim
+        if k is not None:
+            k_out = new((tokens, k_heads, dim), dtype=dtype, device=dev)
+            k_at = k_out.data_ptr(), k_heads * dim, dim
     else:
         q_out, k_out = out
         if (k is None) != (k_out is None):
             raise ValueError("out must be (q, k), None where k is")
-        for t, x, what in ((q_out, q, "q"), (k_out, k, "k")):
-            if t is not None and t is not x:
-                _heads(t, f"out's {what}")
-                if t.dtype is not dtype or t.shape != x.shape:
-                    raise ValueError(f"out's {what} must match {what}'s shape and dtype")
-                _on(dev, "qr_rope", t)
+        q_at = q_in if q_out is q else _heads(q_out, "out's q", shape, dtype, dev)
+        if k is not None:
+            k_at = k_in if k_out is k else _heads(k_out, "out's k", (tokens, k_heads, dim), dtype, dev)
     if tokens and q_heads:
-        qs, qo = q.stride(), q_out.stride()
-        if k is None or not k_shape[1]:
-            keys = (0, 0, 0, 0, 0, 0, 0)
-        else:
-            ks, ko = k.stride(), k_out.stride()
-            keys = (k.data_ptr(), ks[0], ks[1], k_shape[1], k_out.data_ptr(), ko[0], ko[1])
-        status = (_L or _lib()).qr_rope(dt, tokens, dim, rope.rot_dim, rope.layout == "interleaved", rope.turns.data_ptr(),
-                                        rope.factor, *where, q.data_ptr(), qs[0], qs[1], q_heads, q_out.data_ptr(),
-                                        qo[0], qo[1], *keys, _current(dev))
+        if not k_heads:
+            k_in = k_at = (0, 0, 0)
+        status = (_L or _lib()).qr_rope(dt, tokens, dim, rope.rot_dim, rope.interleaved, rope.address, rope.factor, at,
+                                        requests, offsets, lens, *q_in, q_heads, *q_at, *k_in, k_heads, *k_at, _current(dev))
         if status:
             _check(status, "qr_rope")
     return q_out, k_out

@@ -764,7 +764,7 @@ qr_status_t qr_w4_matvec(qr_dtype_t dtype, int64_t tokens, const void *x, int64_
  * 16-byte aligned (pointer, and stride where there are several rows); of a
  * row only its `cols` bytes are read or written.  A row that holds a value
  * that is not finite has a scale that is not finite or NaN, unspecified
- * codes, and touches no other row.
+ * codes, and touches no other row.  cols (and rows of weights) up to 2^30.
  * ------------------------------------------------------------------------- */
 
 /* Rows of x (row stride >= cols) in 8 bits: codes [tokens][cols] at

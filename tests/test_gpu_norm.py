@@ -153,6 +153,22 @@ def test_in_place(cols):
     assert torch.equal(got.codes, q8.codes) and torch.equal(got.scales, q8.scales) and torch.equal(x2, fresh)
 
 
+@pytest.mark.parametrize("tokens", [3, 200, 2500])
+@pytest.mark.parametrize("cols", [33, 251, 1001, 5123, 17001])
+def test_residual_in_place_at_odd_sizes(cols, tokens):
+    """A warp's last lane has a piece of the next warp's, which that one overwrites."""
+    rng = np.random.default_rng(cols)
+    x, res, w = _x(rng, (tokens, cols), 1).cuda(), _x(rng, (tokens, cols), 1).cuda(), _x(rng, (cols,), 1).cuda()
+    fresh = torch.empty_like(res)
+    want = qr.qr_rms_norm_q8(x, w, EPS, res, fresh)
+    for _ in range(5):
+        res2, x2 = res.clone(), x.clone()
+        got = qr.qr_rms_norm_q8(x2, w, EPS, res2)
+        assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales) and torch.equal(res2, fresh)
+        got = qr.qr_rms_norm_q8(x2, w, EPS, res, residual_out=x2)
+        assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales) and torch.equal(x2, fresh)
+
+
 @pytest.mark.parametrize("cols", [64, 8192, 5123])
 def test_small_and_large_values(cols):
     rng = np.random.default_rng(cols)

@@ -39,7 +39,7 @@ def test_quantize_refusals():
         (dict(x=None), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(tokens=0), INVALID),
         (dict(cols=0), INVALID), (dict(codes=A), INVALID), (dict(scales=A + 700), INVALID), (dict(scales=B + 16), INVALID),
         (dict(dtype=2), UNSUPPORTED), (dict(xs=99), SIZE), (dict(cs=96), SIZE), (dict(tokens=1 << 31), SIZE),
-        (dict(xs=1 << 60), SIZE), (dict(x=A + 1), MISALIGNED), (dict(codes=B + 8), MISALIGNED), (dict(cs=120), MISALIGNED),
+        (dict(xs=1 << 60), SIZE), (dict(tokens=1, cols=(1 << 30) + 1), SIZE), (dict(x=A + 1), MISALIGNED), (dict(codes=B + 8), MISALIGNED), (dict(cs=120), MISALIGNED),
         (dict(scales=C + 2), MISALIGNED)])
 
 
