@@ -448,61 +448,70 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
 }
 
 // Adds the parts of the tiles that several CTAs share: block x is the tile in
-// which CTA x's share ends, y a group of 16 tokens of it.  What is not a part (the
-// scales) was there before the product began, and is read before its end.
-template <int DT>
-__global__ void __launch_bounds__(256, 6) w8_join_kernel(W8Args a, W8Shares shares, const float *parts, int pitch) {
+// which CTA x's share ends, y a group of tokens of it, kJoinEach for a warp, whose
+// lanes are a token's 128 rows.  What is not a part (the scales) was there before the product began, and
+// is read before its end.
+constexpr int kJoinThreads = 256;
+template <int DT, int kJoinEach>
+__global__ void __launch_bounds__(kJoinThreads, 4) w8_join_kernel(W8Args a, W8Shares shares, const float *parts, int pitch) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long end = shares.begin(blockIdx.x + 1), tile = shares.divide(end - 1, shares.chunks);
-    const long long from = tile * shares.chunks;
+    constexpr int kWarps = kJoinThreads / 32, kJoinTokens = kWarps * kJoinEach;
+    const int lane = threadIdx.x & 31, first = blockIdx.x;
+    const long long end = shares.begin(first + 1), tile = shares.divide(end - 1, shares.chunks);
+    const long long from = tile * shares.chunks, to = from + shares.chunks;
+    if (end == to || shares.begin(first) > from) {  // whole, or another block's to add
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
+    int last = first + 1;
+    while (shares.begin(last + 1) < to) ++last;
     const long long token_tile = shares.divide(tile, shares.row_ctas);
-    const long long row = (tile - token_tile * shares.row_ctas) * kWtRows + (threadIdx.x & 31) * 4;
-    const int col = blockIdx.y * 16 + (threadIdx.x >> 5);  // and the eighth from there
+    const long long row = (tile - token_tile * shares.row_ctas) * kWtRows + lane * 4;
+    const int col = blockIdx.y * kJoinTokens + (threadIdx.x >> 5);  // and every kWarps-th from there
     const long long token = token_tile * shares.n + col;
     const int have = static_cast<int>(min(a.tokens - token, static_cast<long long>(shares.n - col)));  // tokens from here on
-    // nothing where the tile is whole, or another block's to add
-    const bool mine = end != from + shares.chunks && shares.begin(blockIdx.x) <= from && have > 0 && row < a.rows;
     float4 scale = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float x_scale[2] = {0.0f, 0.0f};
-    if (mine) {
-        scale = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.packed + a.l.scales_at) + row);
-        x_scale[0] = a.x_scales[token];
-        if (have > 8) x_scale[1] = a.x_scales[token + 8];
-    }
+    if (row < a.rows) scale = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.packed + a.l.scales_at) + row);
+    float x_scale[kJoinEach];
+#pragma unroll
+    for (int k = 0; k < kJoinEach; ++k) x_scale[k] = kWarps * k < have ? a.x_scales[token + kWarps * k] : 0.0f;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!mine) return;
-    const float4 *const p = reinterpret_cast<const float4 *>(parts) + col * (kWtRows / 4) + (threadIdx.x & 31);
-    const long long next = static_cast<long long>(kWtRows / 4) * pitch;  // of a part; CTA c's are 2 c and 2 c + 1
-    const long long to = from + shares.chunks;
-    float4 sum[2];
+    if (have <= 0) return;
+    // CTA c's parts are 2 c and, of the tile that begins in its share, 2 c + 1
+    const float4 *const p = reinterpret_cast<const float4 *>(parts) + col * (kWtRows / 4) + lane;
+    const long long next = static_cast<long long>(kWtRows / 4) * pitch;
+    auto load = [&](float4 (&v)[kJoinEach], long long part) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) sum[k] = __ldcg(p + (2ll * blockIdx.x + 1) * next + k * 8 * (kWtRows / 4));
-    for (int c = blockIdx.x + 1; shares.begin(c) < to; c += 2) {
-        const bool two = shares.begin(c + 1) < to;
-        float4 v[2][2];
+        for (int k = 0; k < kJoinEach; ++k)
+            if (kWarps * k < have) v[k] = __ldcg(p + part * next + k * kWarps * (kWtRows / 4));
+    };
+    float4 sum[kJoinEach] = {}, v[kJoinEach] = {};
+    load(sum, 2ll * first + 1);
+#pragma unroll 2
+    for (int c = first + 1; c <= last; ++c) {
+        load(v, 2ll * c);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) v[0][k] = __ldcg(p + 2ll * c * next + k * 8 * (kWtRows / 4));
-#pragma unroll
-        for (int k = 0; k < 2; ++k) v[1][k] = two ? __ldcg(p + 2ll * (c + 1) * next + k * 8 * (kWtRows / 4)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) sum[k].x += v[i][k].x, sum[k].y += v[i][k].y, sum[k].z += v[i][k].z, sum[k].w += v[i][k].w;
+        for (int k = 0; k < kJoinEach; ++k) sum[k].x += v[k].x, sum[k].y += v[k].y, sum[k].z += v[k].z, sum[k].w += v[k].w;
     }
-    const bool vector = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0 && a.y_stride % 4 == 0 && row + 4 <= a.rows;
+    const bool vector = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0 && a.y_stride % 4 == 0 && a.rows % 4 == 0;
+    uint16_t *to_y = a.y + token * a.y_stride + row;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        if (8 * k >= have) break;
+    for (int k = 0; k < kJoinEach; ++k, to_y += kWarps * a.y_stride) {
+        if (kWarps * k >= have) break;
         const float s = x_scale[k];
-        const float y[4] = {sum[k].x * s * scale.x, sum[k].y * s * scale.y, sum[k].z * s * scale.z, sum[k].w * s * scale.w};
-        uint16_t *const to_y = a.y + (token + 8 * k) * a.y_stride + row;
-        const uint2 o = make_uint2(narrow2<DT>(y[0], y[1]), narrow2<DT>(y[2], y[3]));
+        const uint2 o = make_uint2(narrow2<DT>(sum[k].x * s * scale.x, sum[k].y * s * scale.y),
+                                   narrow2<DT>(sum[k].z * s * scale.z, sum[k].w * s * scale.w));
         if (vector) {
-            *reinterpret_cast<uint2 *>(to_y) = o;
-        } else {
+            if (row < a.rows) *reinterpret_cast<uint2 *>(to_y) = o;
+            continue;
+        }
+        // a store's lanes on consecutive rows: row 32 j + lane is the (lane % 4)-th of lane 8 j + lane / 4
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (row + e < a.rows) to_y[e] = static_cast<uint16_t>((e < 2 ? o.x : o.y) >> (16 * (e & 1)));
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = __shfl_sync(~0u, o.x, 8 * j + (lane >> 2)), hi = __shfl_sync(~0u, o.y, 8 * j + (lane >> 2));
+            const uint32_t w = lane & 2 ? hi : lo;
+            const int at = 32 * j + lane - 4 * lane;  // from this lane's rows
+            if (row + at < a.rows) to_y[at] = static_cast<uint16_t>(lane & 1 ? w >> 16 : w);
         }
     }
 }
@@ -561,7 +570,14 @@ static cudaError_t run_w8_tc(const W8Args &a, uint8_t *workspace, int n, cudaStr
     bool joined = false;
     for (int c = 1; c < shares.ctas && !joined; ++c) joined = shares.begin(c) % a.l.chunks != 0;
     if (!joined) return cudaSuccess;
-    return launch_chained(w8_join_kernel<DT>, dim3(shares.ctas - 1, (n + 15) / 16), 256, 0, s, a, shares, static_cast<const float *>(parts), N);  // (parts are N tokens apart)
+    // fewer tokens a warp where there are few (64 tokens: 16 in a block 23.0 us, 32
+    // 23.7; 1024 through 1280 x 8192: 32.6 and 30.6)
+    auto join = [&](auto kernel, int each) {
+        const unsigned groups = static_cast<unsigned>((n + 8 * each - 1) / (8 * each));
+        return launch_chained(kernel, dim3(shares.ctas - 1, groups), kJoinThreads, 0, s, a, shares,
+                              static_cast<const float *>(parts), N);  // (parts are N tokens apart)
+    };
+    return n <= 96 ? join(w8_join_kernel<DT, 2>, 2) : join(w8_join_kernel<DT, 4>, 4);
 }
 
 template <int DT>
