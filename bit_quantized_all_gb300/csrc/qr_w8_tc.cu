@@ -516,53 +516,28 @@ __global__ void __launch_bounds__(kJoinThreads, 4) w8_join_kernel(W8Args a, W8Sh
     }
 }
 
-// Tokens of a tile: 256 at most, in equal shares (129 tokens one tile of 144, 300
-// two of 160).
-static int w8_tile_tokens(long long tokens) {
-    const long long tiles = (tokens + 255) / 256;
-    return static_cast<int>(((tokens + tiles - 1) / tiles + 15) / 16 * 16);
-}
-
 static size_t w8_x16_bytes(long long tokens, int chunks, int n) {
     return static_cast<size_t>((tokens + n - 1) / n * n) * chunks * 128;
 }
 
-// A buffer's size: of the next 32, 64, 128 or whole 256 tokens, so that it grows
-// with them.
+// The kernel that takes tiles of n tokens.
 static int w8_most_tokens(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 192 ? 192 : 256; }
 
 size_t w8_workspace(long long tokens, int cols) {
-    const int most = w8_most_tokens(tokens < 256 ? static_cast<int>(tokens) : 256);
-    return w8_x16_bytes(tokens, cols / 64 + (cols % 64 != 0), most) + size_t(2) * kWtMostCtas * kWtRows * 4 * most;
+    // (tiles in equal shares of fewer tokens than 256 hold less than a tile more)
+    const int most = tokens <= 32 ? 32 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256;
+    return w8_x16_bytes(tokens > 256 ? tokens + 256 : tokens, cols / 64 + (cols % 64 != 0), most) + size_t(2) * kWtMostCtas * kWtRows * 4 * most;
 }
 
 template <int DT, int N>
-static cudaError_t run_w8_tc(const W8Args &a, uint8_t *workspace, int n, cudaStream_t s) {
+static cudaError_t run_w8_tc(const W8Args &a, const W8Shares &shares, uint8_t *workspace, cudaStream_t s) {
+    const int n = shares.n;
     auto kern = w8_tc_kernel<DT, N>;
     const int bytes = sizeof(WtSmem<N>) + 1024;
     cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void *>(kern), bytes);
     if (err != cudaSuccess) return err;
-    int sms = sm_count(&err);
-    if (sms <= 0) return err;
-    if (sms > kWtMostCtas) sms = kWtMostCtas;
     unsigned *timeouts = wait_timeout_counter(&err);
     if (!timeouts) return err;
-    const long long tiles = (a.l.row_tiles + 7) / 8 * ((a.tokens + n - 1) / n);
-    W8Shares shares = {tiles * a.l.chunks, 0, 0, a.l.chunks, (a.l.row_tiles + 7) / 8, 1, n};
-    // Whole tiles, or even shares and a kernel that joins the parts of the tiles that
-    // they divide: what either takes in microseconds.  A chunk is bound by its
-    // products or its hand-overs; joining takes a launch, the parts' way to L2 and
-    // back, and some time for each part of a tile.
-    const double chunk = (n > 160 ? 2 * n : 320) / 1900.0;
-    shares.ctas = static_cast<int>(tiles < sms ? tiles : sms);
-    double best = static_cast<double>((tiles + shares.ctas - 1) / shares.ctas) * a.l.chunks * chunk;
-    for (int c = sms; c >= 8; c = c * 3 / 4) {
-        const double each = static_cast<double>(shares.all) / c;
-        const double cost = each * chunk + 3.0 + (each < a.l.chunks ? a.l.chunks / each : 1.0) * 0.3 + c * n * (4.0 * kWtRows * 4 / 1e7);
-        if (each >= 4 && cost < best) best = cost, shares.ctas = c;
-    }
-    shares.each = shares.all / shares.ctas;
-    shares.rest = static_cast<int>(shares.all % shares.ctas);
     float *const parts = reinterpret_cast<float *>(workspace + w8_x16_bytes(a.tokens, a.l.chunks, n));
     err = launch_chained(kern, shares.ctas, kWtThreads<N>, bytes, s, a, shares, static_cast<const uint8_t *>(workspace), parts,
                          timeouts);
@@ -581,24 +556,62 @@ static cudaError_t run_w8_tc(const W8Args &a, uint8_t *workspace, int n, cudaStr
 }
 
 template <int DT>
-static cudaError_t pick_tokens(int n, const W8Args &a, uint8_t *workspace, cudaStream_t s) {
-    switch (w8_most_tokens(n)) {
-        case 32: return run_w8_tc<DT, 32>(a, workspace, n, s);
-        case 64: return run_w8_tc<DT, 64>(a, workspace, n, s);
-        case 128: return run_w8_tc<DT, 128>(a, workspace, n, s);
-        case 192: return run_w8_tc<DT, 192>(a, workspace, n, s);
-        default: return run_w8_tc<DT, 256>(a, workspace, n, s);
+static cudaError_t pick_tokens(const W8Args &a, const W8Shares &p, uint8_t *workspace, cudaStream_t s) {
+    switch (w8_most_tokens(p.n)) {
+        case 32: return run_w8_tc<DT, 32>(a, p, workspace, s);
+        case 64: return run_w8_tc<DT, 64>(a, p, workspace, s);
+        case 128: return run_w8_tc<DT, 128>(a, p, workspace, s);
+        case 192: return run_w8_tc<DT, 192>(a, p, workspace, s);
+        default: return run_w8_tc<DT, 256>(a, p, workspace, s);
     }
 }
 
+// The tiles' tokens, equal shares of up to 128, 192 or 256, and the division of their
+// chunks: whole tiles, or even shares, whose divided tiles' parts are joined; by what
+// each takes, in microseconds.  A chunk is bound by its products or its hand-overs,
+// and weights that do not stay in L2 between tiles by HBM;
+// a tile's results are stored beside the next one's products where there are two
+// accumulators; joining takes a launch, the parts' way to L2 and back, and some time
+// for each part of a tile.
+static W8Shares w8_shares(const W8Args &a, int sms) {
+    W8Shares best = {};
+    double least = 0.0;
+    for (int most = 128; most <= 256; most += 64) {
+        const long long token_tiles = (a.tokens + most - 1) / most;
+        const int n = static_cast<int>(((a.tokens + token_tiles - 1) / token_tiles + 15) / 16 * 16);
+        W8Shares p = {0, 0, 0, a.l.chunks, (a.l.row_tiles + 7) / 8, 1, n};
+        const long long tiles = token_tiles * p.row_ctas;
+        p.all = tiles * p.chunks;
+        const double chunk = n > 192 ? n * 0.0011 : n > 128 ? 0.3 : a.l.scales_at > (32 << 20) ? 0.22 : 0.19;
+        const double results = n * (n > 192 ? 0.013 : 0.007);
+        const double tile = n > 128 ? p.chunks * chunk + results : p.chunks * chunk > results ? p.chunks * chunk : results;
+        p.ctas = static_cast<int>(tiles < sms ? tiles : sms);
+        double cost = static_cast<double>((tiles + p.ctas - 1) / p.ctas) * tile + results;
+        for (int c = sms; c >= 8; c = c * 3 / 4) {
+            const double each = static_cast<double>(p.all) / c;
+            const double split = each / p.chunks * tile + results + 3.0 + (each < p.chunks ? p.chunks / each : 1.0) * 0.3 +
+                                 c * n * (4.0 * kWtRows * 4 / 1e7);
+            if (each >= 4 && split < cost) cost = split, p.ctas = c;
+        }
+        if (least == 0.0 || cost < least) least = cost, best = p;
+        if (a.tokens <= most) break;
+    }
+    best.each = best.all / best.ctas;
+    best.rest = static_cast<int>(best.all % best.ctas);
+    return best;
+}
+
 cudaError_t launch_w8_tc(int dtype, const W8Args &a, void *workspace, cudaStream_t s) {
-    const int n = w8_tile_tokens(a.tokens);
+    cudaError_t err = cudaSuccess;
+    const int sms = sm_count(&err);
+    if (sms <= 0) return err;
+    const W8Shares p = w8_shares(a, sms < kWtMostCtas ? sms : kWtMostCtas);
     uint8_t *const to = static_cast<uint8_t *>(workspace);
     const int sweep = (a.l.chunks + kWeThreads / 16 - 1) / (kWeThreads / 16);
     const dim3 grid(static_cast<unsigned>((a.tokens + 7) / 8), static_cast<unsigned>(sweep < 65535 ? sweep : 65535));
-    const cudaError_t err = launch_chained(w8_expand_kernel, grid, kWeThreads, 0, s, a, to, n);
+    err = launch_chained(w8_expand_kernel, grid, kWeThreads, 0, s, a, to, p.n);
     if (err != cudaSuccess) return err;
-    return dtype ? pick_tokens<1>(n, a, to, s) : pick_tokens<0>(n, a, to, s);
+    return dtype ? pick_tokens<1>(a, p, to, s) : pick_tokens<0>(a, p, to, s);
 }
 
 }  // namespace qrk

@@ -46,7 +46,7 @@ def _check_equal(x, sx, w, sw, dtype, y=None, weight=None):
 
 
 @pytest.mark.parametrize("dtype", [0, 1])
-@pytest.mark.parametrize("tokens", [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 255, 256, 257, 300, 520])
+@pytest.mark.parametrize("tokens", [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 255, 256, 257, 300, 410, 520, 769, 1100])
 def test_tokens(dtype, tokens):
     rng = np.random.default_rng(tokens)
     rows, cols = 272, 960
