@@ -3,6 +3,8 @@
 Each translation unit under csrc/ compiles in parallel; the objects link into
 ``libqr.so`` next to this file with the CUDA runtime linked statically and
 every symbol hidden except the ``qr_*`` entry points of include/qr.h.
+csrc/qr_fast.cpp becomes the extension module ``_qr_fast.so`` beside it, the
+compiled form of the calls in layer.py.
 """
 from __future__ import annotations
 
@@ -12,11 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libqr.so")
+FAST_PATH = os.path.join(HERE, "_qr_fast.so")  # csrc/qr_fast.cpp, an extension module
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["qr_capi.cu", "qr_grid.cu", "qr_encode.cu", "qr_decode.cu", "qr_reduce.cu", "qr_allreduce.cu",
@@ -53,10 +57,28 @@ def _deps() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(FAST_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(FAST_PATH))
     return any(os.path.getmtime(f) > t for f in _deps())
+
+
+def _build_fast() -> None:
+    """The extension module, against the running interpreter's and torch's headers."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    includes = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    tmp = FAST_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in includes),
+           os.path.join(CSRC, "qr_fast.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"g++ failed on qr_fast.cpp:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
+    os.replace(tmp, FAST_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -90,8 +112,10 @@ def _build_locked(verbose: bool, ptxas_info: bool) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
         return obj, p.stdout + p.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        fast = ex.submit(_build_fast)
         results = list(ex.map(compile_one, SOURCES))
+        fast.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log.strip():

@@ -7,6 +7,11 @@ the next layer.
 rows by 8-bit weights with a scale for each output channel; ``qr_rope`` turns
 queries and keys by their positions.  ``include/qr.h`` has the arithmetic,
 layouts and contracts; checks, streams and errors are as in ``serving.py``.
+
+Each call first offers its arguments to the compiled module ``_qr_fast``
+(``csrc/qr_fast.cpp``), which does the common form of it, with outputs of its
+own, in a third of the interpreter's time, and declines everything else: what
+the functions here then check, serve or refuse.
 """
 from __future__ import annotations
 
@@ -20,6 +25,7 @@ from . import _check, _cuda_contig, _dtype_code, _same_device, lib
 from .serving import KVPlan, _as_current, _current, _int_tensor, _matrix, _on
 
 _L = None  # the library, these calls' signatures set
+_F = None  # the compiled module, bound to the library
 
 
 def _lib():
@@ -46,6 +52,18 @@ def _lib():
             fn.argtypes = args
         _L = L
     return _L
+
+
+def _fast():
+    global _F
+    if _F is None:
+        L = _lib()
+        from . import _qr_fast
+        _qr_fast.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+                        for name in ("qr_q8_quantize", "qr_rms_norm", "qr_rms_norm_q8", "qr_rope", "qr_w8_matmul",
+                                     "qr_w8_matmul_workspace_bytes")))
+        _F = _qr_fast
+    return _F
 
 
 def _rows_of(t, what: str, shape, dtype, device: torch.device) -> tuple[int, int]:
@@ -76,10 +94,13 @@ class Q8Rows:
         if codes.data_ptr() % 16 or (codes.shape[0] > 1 and codes.stride(0) % 16):
             raise ValueError("codes: every row must begin on a 16-byte boundary")
         _int_tensor(scales, "scales", torch.float32, (codes.shape[0],))
-        self.device = _same_device([codes, scales], "Q8Rows")
+        _same_device([codes, scales], "Q8Rows")
         self.codes, self.scales = codes, scales
-        self.tokens, self.cols = codes.shape
         self.pitch = codes.stride(0)  # between rows
+
+    tokens = property(lambda self: self.codes.shape[0])
+    cols = property(lambda self: self.codes.shape[1])
+    device = property(lambda self: self.codes.device)
 
     @classmethod
     def empty(cls, tokens: int, cols: int, device="cuda") -> "Q8Rows":
@@ -94,16 +115,18 @@ class Q8Rows:
         return self.codes.float() * self.scales[:, None]
 
 
+def _made(got, what: str) -> Q8Rows:
+    """A Q8Rows of (codes, scales, pitch), without its checks; or the error of a status."""
+    if type(got) is int:
+        _check(got, what)
+    out = Q8Rows.__new__(Q8Rows)
+    out.codes, out.scales, out.pitch = got
+    return out
+
+
 def _rows8_out(out, tokens: int, cols: int, device, what: str) -> Q8Rows:
     if out is None:
-        # (as Q8Rows.empty without its checks: some 5 us a call)
-        out = Q8Rows.__new__(Q8Rows)
-        pad = -cols % 16
-        codes = torch.empty((tokens, cols + pad), dtype=torch.int8, device=device)
-        out.codes = codes[:, :cols] if pad else codes
-        out.scales = torch.empty(tokens, dtype=torch.float32, device=device)
-        out.device, out.tokens, out.cols, out.pitch = device, tokens, cols, cols + pad
-        return out
+        return Q8Rows.empty(tokens, cols, device)
     if not isinstance(out, Q8Rows):
         raise TypeError(f"{what}: out must be a Q8Rows")
     if out.tokens != tokens or out.cols != cols:
@@ -115,6 +138,10 @@ def _rows8_out(out, tokens: int, cols: int, device, what: str) -> Q8Rows:
 
 def qr_q8_quantize(x: torch.Tensor, out: Q8Rows | None = None, stream=None) -> Q8Rows:
     """Rows of fp16/bf16 x [tokens, cols] in 8 bits."""
+    if out is None and stream is None:
+        got = (_F or _fast()).quantize(x)
+        if got is not None:
+            return _made(got, "qr_q8_quantize")
     if stream is not None:
         _matrix(x, "x")
         with _as_current(x.device, stream):
@@ -188,6 +215,12 @@ def qr_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     """h = x + residual (x without one), y = h / sqrt(mean(h^2) + eps) * weight
     for each row of fp16/bf16 x [tokens, cols].  ``residual_out`` (by default
     ``residual`` itself) gets h; ``weight`` is x's type or fp32."""
+    if out is None and stream is None:
+        got = (_F or _fast()).norm(x, weight, eps, residual, residual_out, False)
+        if got is not None:
+            if type(got) is int:
+                _check(got, "qr_rms_norm")
+            return got
     if stream is not None:
         _matrix(x, "x")
         with _as_current(x.device, stream):
@@ -198,6 +231,10 @@ def qr_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
 def qr_rms_norm_q8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
                    residual_out: torch.Tensor | None = None, out: Q8Rows | None = None, stream=None) -> Q8Rows:
     """qr_rms_norm with its output as rows in 8 bits."""
+    if out is None and stream is None:
+        got = (_F or _fast()).norm(x, weight, eps, residual, residual_out, True)
+        if got is not None:
+            return _made(got, "qr_rms_norm_q8")
     if stream is not None:
         _matrix(x, "x")
         with _as_current(x.device, stream):
@@ -278,6 +315,13 @@ def qr_w8_matmul(x: Q8Rows, weight: W8Weight, dtype: torch.dtype = torch.bfloat1
     """y = x @ w.T for rows in 8 bits and 8-bit weights, in ``dtype`` (fp16 or
     bf16; y's where that is given).  More than 16 tokens use ``workspace``
     (uint8, qr_w8_matmul_workspace); without one it is allocated."""
+    if y is None and stream is None and isinstance(x, Q8Rows) and isinstance(weight, W8Weight) and dtype in _OUT_CODES:
+        got = (_F or _fast()).matmul(x.codes, x.scales, weight.packed, weight.rows, weight.cols,
+                                     dtype is torch.bfloat16, workspace)
+        if got is not None:
+            if type(got) is int:
+                _check(got, "qr_w8_matmul")
+            return got
     if stream is not None:
         with _as_current(weight.packed.device, stream):
             return qr_w8_matmul(x, weight, dtype, y, workspace)
@@ -408,6 +452,14 @@ def qr_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope, positions: torc
     turned by their positions: ``positions`` (int32 [tokens]), or those of a
     step's ``plan`` (tokens past its last one are left alone in ``out``).
     Returns (q, k), new or ``out``; ``out=(q, k)`` turns them in place."""
+    in_place = out is not None and out[0] is q and out[1] is k
+    if stream is None and (out is None or in_place) and (positions is None) != (plan is None):
+        got = (_F or _fast()).rope(q, k, rope.turns, rope.rot_dim, rope.interleaved, rope.factor, positions,
+                                   None if plan is None else plan.q_offsets, None if plan is None else plan.kv_lens, in_place)
+        if got is not None:
+            if type(got) is int:
+                _check(got, "qr_rope")
+            return got
     if stream is not None:
         _heads(q, "q")
         with _as_current(q.device, stream):
