@@ -7,6 +7,10 @@
 // cosines, once for all heads, in shared memory; then a thread takes a unit of 2 VP
 // values, VP rotated pairs in two loads of VP values (or as many that are only
 // copied), of one head at a time.
+//
+// What bounds it: HBM (32768 tokens of 48 heads of 128, slices of a projection, 141 us,
+// 5.7 TB/s of reads and writes, 0.84 of the copy rate); for few tokens the launch,
+// position, sine and store one after the other (16 tokens 2.1 us).
 #include "qr_device.cuh"
 #include "qr_launch.h"
 #include "qr_serving.h"
