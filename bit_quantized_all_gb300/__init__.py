@@ -51,7 +51,8 @@ EXPORTS = ("qr_tile_values", "qr_tile_bytes", "qr_wire_bytes", "qr_encode", "qr_
            "qr_fp4_twoshot_peer_workspace_bytes", "qr_fp4_twoshot_peer_send", "qr_fp4_twoshot_peer_reduce",
            "qr_fp4_twoshot_peer_decode", "qr_kv_plan", "qr_kv_append", "qr_kv_attention_workspace_bytes",
            "qr_kv_attention", "qr_w4_bytes", "qr_w4_pack", "qr_w4_quantize", "qr_w4_matvec_workspace_bytes",
-           "qr_w4_matvec")
+           "qr_w4_matvec", "qr_q8_quantize", "qr_rms_norm", "qr_rms_norm_q8", "qr_w8_bytes", "qr_w8_pack",
+           "qr_w8_quantize", "qr_w8_matmul_workspace_bytes", "qr_w8_matmul", "qr_rope")
 TWOSHOT_STATIC_WORKSPACE_BYTES = 32 << 20  # QR_TWOSHOT_STATIC_WORKSPACE_BYTES
 FC_BITS = (4, 8)
 FC_PAIRS = ((4, 4), (4, 8), (8, 8))  # (reduce-scatter, all-gather) widths; (4, 8) is the mixed "INT6"
