@@ -93,8 +93,8 @@ struct WtSmem {
     // x: chunks that are handed on together (a wait and a commit take the products'
     // warp some 150 cycles, four chunks' products of 64 tokens run for 512), and
     // buffers of them
-    static constexpr int kXc = N > 128 ? 1 : N > 64 ? 2 : 4;
-    static constexpr int kX = N > 128 ? 6 : N > 64 ? 4 : N > 32 ? 3 : 4;
+    static constexpr int kXc = N > 192 ? 1 : N > 64 ? 2 : 4;
+    static constexpr int kX = N > 192 ? 6 : N > 128 ? 3 : N > 64 ? 4 : N > 32 ? 3 : 4;
     uint8_t x[kX * kXc * kBlock];
     uint8_t codes[kW][8][kWtStaged<N> ? kStep * 1024 : 16];  // by warp: its row tile
     uint8_t out[kWtResults<N>][16 * 80];                     // by warp: 16 tokens of 32 rows
