@@ -142,7 +142,7 @@ __device__ __forceinline__ void row_reduce(float &sum, float &most, float2 *s, i
 // that eight of them are a piece's last and the next lane's first; a warp's last
 // lane has the piece that the next warp's first has too, and stores none.
 template <int DT, int W, bool EIGHT, bool SHIFT, bool WARP, int P, int THREADS, bool AHEAD>
-__global__ void __launch_bounds__(THREADS, WARP || (P == 2 && !EIGHT) ? 2 : 1) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(THREADS, WARP || (P == 2 && !EIGHT) || THREADS == 320 ? 2 : 1) norm_kernel(NormArgs a) {
     chain_entry();
     constexpr int kLanes = SHIFT && EIGHT ? 31 : 32;
     __shared__ float2 s_part[64];
@@ -339,7 +339,9 @@ static cudaError_t run_norm(const NormArgs &a, cudaStream_t s) {
     if (threads(1) <= 1024 && a.tokens <= 2 * sms)
         return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 1, 1024, false>, threads(1), 1);
     if constexpr (W == 0) {
-        if (threads(4) > 512) return launch(norm_kernel<DT, 0, EIGHT, SHIFT, false, 8, 512, true>, threads(8), 1);
+        if (threads(4) > 512)
+            return threads(8) <= 320 ? launch(norm_kernel<DT, 0, EIGHT, SHIFT, false, 8, 320, true>, threads(8), 1)
+                                     : launch(norm_kernel<DT, 0, EIGHT, SHIFT, false, 8, 512, true>, threads(8), 1);
     }
     if constexpr (SHIFT) {
         if (threads(2) <= 512) return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 2, 512, true>, threads(2), 1);

@@ -4,6 +4,7 @@
 #include "qr_kv_device.cuh"
 #include "qr_launch.h"
 #include "qr_serving.h"
+#include "qr_w8.cuh"
 
 namespace qrk {
 
@@ -19,17 +20,19 @@ __global__ void __launch_bounds__(kW8Threads) w8_pack_kernel(int rows, int cols,
         if (i < pieces) {
             const long long tile = i >> 6, row = tile / l.chunks * 16 + (i >> 2 & 15);
             const int col = static_cast<int>(tile % l.chunks) * 64 + static_cast<int>(i & 3) * 16;
-            uint32_t w[4];
-            for (int k = 0; k < 4; ++k) {
-                w[k] = 0;
-                for (int b = 0; b < 4; ++b) {
-                    const int c = col + 4 * k + b;
-                    const uint32_t u = row < rows && c < cols ? static_cast<uint8_t>(codes[row * stride + c]) : 0u;
-                    w[k] |= u << (8 * b);
+            const int8_t *const src = codes + row * stride + col;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (row < rows) {
+                if ((reinterpret_cast<uintptr_t>(src) & 15) == 0 || cols - col < 16) {
+                    w = load16_codes(src, cols - col);
+                } else {  // by the bytes that the address allows no more than
+                    uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int b = 0; b < 16; ++b) u[b >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(src[b])) << (8 * (b & 3));
+                    w = make_uint4(u[0], u[1], u[2], u[3]);
                 }
-                w[k] ^= kFlip;
             }
-            reinterpret_cast<uint4 *>(packed)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4 *>(packed)[i] = make_uint4(w.x ^ kFlip, w.y ^ kFlip, w.z ^ kFlip, w.w ^ kFlip);
         } else {
             const long long row = i - pieces;
             reinterpret_cast<float *>(packed + l.scales_at)[row] = row < rows ? scales[row] : 0.0f;
