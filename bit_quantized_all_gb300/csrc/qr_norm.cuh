@@ -8,8 +8,8 @@
 // scale; both reductions share one barrier.
 //
 // What bounds it: HBM (32768 x 8192 in 8 bits with the residual 272 us, 6.9 TB/s, a
-// plain copy's rate; 8192 x 20480 without a norm 88 us, 5.7 TB/s: one CTA an SM, 64
-// KB of the next row on its way); for few rows the launch and two round trips (16 x
+// plain copy's rate; 8192 x 20480 without a norm 74 us, 6.8 TB/s, with one CTA an SM
+// rather than two 88); for few rows the launch and two round trips (16 x
 // 8192 2.6 us); for a few thousand rows that do not begin on 16-byte boundaries the
 // issue of a row's instructions (2049 x 5123 in 16 bits 14 us, 2049 x 5120 10).
 #pragma once

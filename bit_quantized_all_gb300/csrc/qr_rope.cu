@@ -8,9 +8,9 @@
 // values, VP rotated pairs in two loads of VP values (or as many that are only
 // copied), of one head at a time.
 //
-// What bounds it: HBM (32768 tokens of 48 heads of 128, slices of a projection, 141 us,
-// 5.7 TB/s of reads and writes, 0.84 of the copy rate); for few tokens the launch,
-// position, sine and store one after the other (16 tokens 2.1 us).
+// What bounds it: HBM (32768 tokens of 48 heads of 128, slices of a projection, 143 us,
+// 5.6 TB/s of reads and writes, 0.83 of the copy rate); for few tokens the launch,
+// position, sine and store one after the other (16 tokens 1.8 us).
 #include "qr_device.cuh"
 #include "qr_launch.h"
 #include "qr_serving.h"
@@ -85,7 +85,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, RopeShap
     }
 
     const int tasks = tokens * s.heads * s.units;
-    constexpr int kEach = VP == 8 ? 4 : 2;  // units under way
+    // units under way (four: 32768 x 48 heads 141 us for 143, 16 tokens 2.1 for 1.8,
+    // 4097 of 10 heads 10.4 for 9.7; a round of them ahead: 154 us)
+    constexpr int kEach = 2;
     struct Unit {
         const uint16_t *in;
         uint16_t *out;

@@ -8,18 +8,20 @@
 // tokens is one bulk copy.  Then y^T = W x^T in tiles of 128 weight rows by N
 // tokens: eight warps, a row tile of 16 each, turn packed codes into fp16 and store
 // them as the A operand in tensor memory, one warp brings x, one issues the
-// products, and four scale and store a finished tile while the next one runs.
+// products, and four or eight scale and store a finished tile while the next one runs.
 //
 // The chunks of all tiles, one tile after the other, are divided evenly among
-// the CTAs, one an SM.  A tile that one CTA has whole is stored by it; the parts
-// of the others go to the workspace as fp32 sums, and a last kernel adds them in
-// order, so that the result has the same bits every time.
+// the CTAs, one an SM, or whole tiles are where that is quicker.  A tile that one
+// CTA has whole is stored by it; the parts of the others go to the workspace as fp32
+// sums, and a last kernel adds them in order, so that the result has the same bits
+// every time.
 //
 // What bounds it: with 256 tokens a tile the products (4096 tokens through 10240 x
 // 8192: 405 to 425 us as the clock goes under the power limit, 1.62 to 1.70 PFLOP/s;
 // 1024 tokens 106 us, the tensor pipe busy 82%); with fewer the weights' bytes, in
 // the steady state, and around it the first kernel, the first loads' way and the
-// join, some 7 us (64 tokens 23 us, 3.7 TB/s; 129 through 20481 x 5123 38 us).
+// join, some 7 us (64 tokens 23 us, 3.7 TB/s; 129 through 20481 x 5123 37.6 us: the
+// two rings in shared memory hold too little of either operand for HBM's latency).
 //
 // A lane's 16 codes of a tile's row are consecutive columns; as fragments of the
 // store to tensor memory they stand at the columns 16 j + 4 t + 0..3, so x is
