@@ -51,7 +51,7 @@ class TPAttentionLayer:
         table, ValueError where ``new_lens`` are not the queries' tokens; the
         layer is then as it was, but for table entries past its requests' ends."""
         plan, counts = self._plan(new_lens, q[0].shape[0])
-        return self._attend(plan, counts, zip(q, k, v), max_q)
+        return self._attend(plan, counts, ((q[r], k[r], v[r]) for r in range(len(self.caches))), max_q)
 
     def _plan(self, new_lens: torch.Tensor, tokens: int) -> tuple[KVPlan, torch.Tensor]:
         """The step's plan and its counts, read back; raises as ``step`` does."""

@@ -99,3 +99,12 @@ def test_refusals():
                 dict(qkv=[qr.qr_w8_quantize(w[:-DIM]) for w in dense]), dict(qkv=[qr.qr_w8_quantize(w[:-1]) for w in dense])):
         with pytest.raises(ValueError):
             TPAttentionBlock(**{"norm_weight": norm, "qkv": qkv, "rope": rope, "layer": _layer(out), **bad})
+
+
+def test_a_step_without_every_rank_is_refused():
+    _, out = _weights(np.random.default_rng(4))
+    layer = _layer(out)
+    q = [torch.zeros(2, HEADS, DIM, dtype=torch.bfloat16, device="cuda")]
+    k = [torch.zeros(2, KV, DIM, dtype=torch.bfloat16, device="cuda")]
+    with pytest.raises(IndexError):
+        layer.step(q, k, k, torch.tensor([1, 1, 0], dtype=torch.int32, device="cuda"), 1)
