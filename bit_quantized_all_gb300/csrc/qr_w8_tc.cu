@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kWeThreads) w8_expand_kernel(W8Args a, uint8_t
 }
 
 // Up to 192 tokens a tile the weights' bytes bound the kernel, or x's and theirs
-// alike: the packed codes come through shared memory, some steps ahead.  With more x
+// alike: the packed codes come through shared memory, some steps ahead.  With more, x
 // fills that, and the products leave time for two steps in the registers of the
 // warps that convert them (1024 tokens through 10240 x 8192: through shared memory
 // 111 us, registers 108; 129 through 20481 x 5123: 39 and 44).
@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(kWtThreads<N>, 1)
 
 // Adds the parts of the tiles that several CTAs share: block x is the tile in
 // which CTA x's share ends, y a group of tokens of it, kJoinEach for a warp, whose
-// lanes are a token's 128 rows.  What is not a part (the scales) was there before the product began, and
-// is read before its end.
+// lanes are a token's 128 rows.  What is not a part (the scales) was there before
+// the product began, and is read before its end.
 constexpr int kJoinThreads = 256;
 template <int DT, int kJoinEach>
 __global__ void __launch_bounds__(kJoinThreads, 4) w8_join_kernel(W8Args a, W8Shares shares, const float *parts, int pitch) {
@@ -577,9 +577,8 @@ static cudaError_t pick_tokens(const W8Args &a, const W8Shares &p, uint8_t *work
 // The tiles' tokens, equal shares of up to 128, 192 or 256, and the division of their
 // chunks: whole tiles, or even shares, whose divided tiles' parts are joined; by what
 // each takes, in microseconds.  A chunk is bound by its products or its hand-overs,
-// and weights that do not stay in L2 between tiles by HBM;
-// a tile's results are stored beside the next one's products where there are two
-// accumulators; joining takes a launch, the parts' way to L2 and back, and some time
+// and weights that do not stay in L2 between tiles by HBM; a tile's results are
+// stored beside the next one's products where there are two accumulators; joining takes a launch, the parts' way to L2 and back, and some time
 // for each part of a tile.
 static W8Shares w8_shares(const W8Args &a, int sms) {
     W8Shares best = {};
