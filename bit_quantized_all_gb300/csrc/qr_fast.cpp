@@ -17,6 +17,7 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -163,6 +164,7 @@ PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
             return none();
     }
     const bool in_place = args[9] == Py_True;
+    const qr_stream_t stream = stream_on(device);
     at::Tensor q_out, k_out;
     if (in_place) {
         q_out = *q;
@@ -172,7 +174,9 @@ PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const auto options = at::TensorOptions().dtype(q->scalar_type()).device(device);
         const int64_t k_at = (q->numel() + 7) / 8 * 8, n = k ? k_at + k->numel() : q->numel();
         // (tokens that a plan leaves out: not what the memory held)
-        const at::Tensor all = pos ? at::empty({n}, options) : at::zeros({n}, options);
+        const at::Tensor all = at::empty({n}, options);
+        if (!pos && cudaMemsetAsync(all.data_ptr(), 0, static_cast<size_t>(n) * 2, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return PyLong_FromLong(QR_ERR_CUDA);
         auto part = [&](const at::Tensor &x, int64_t from) {
             return inside(all, q->scalar_type(), from, x.sizes(), {x.size(1) * dim, dim, 1});
         };
@@ -186,7 +190,7 @@ PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
         lens ? static_cast<int>(lens->size(0)) : 0, data(offsets), data(lens), q->data_ptr(), q->stride(0), q->stride(1),
         static_cast<int>(q->size(1)), q_out.data_ptr(), q_out.stride(0), q_out.stride(1), k ? k->data_ptr() : nullptr,
         k ? k->stride(0) : 0, k ? k->stride(1) : 0, k ? static_cast<int>(k->size(1)) : 0, k ? k_out.data_ptr() : nullptr,
-        k ? k_out.stride(0) : 0, k ? k_out.stride(1) : 0, stream_on(device));
+        k ? k_out.stride(0) : 0, k ? k_out.stride(1) : 0, stream);
     if (status) return PyLong_FromLong(status);
     if (in_place) return Py_BuildValue("(OO)", args[0], args[1]);
     if (!k) return Py_BuildValue("(NO)", THPVariable_Wrap(q_out), Py_None);

@@ -94,3 +94,29 @@ def test_declines():
         qr.qr_w8_matmul(qr.Q8Rows.empty(40, 64), weight, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(TypeError):
         F.bind(1, 2)
+
+
+def test_a_plan_that_leaves_tokens_out_captured():
+    """Tokens past the plan's last one are zeros in new outputs, in a replay too."""
+    q = torch.randn((6, 2, 64), device="cuda").half()
+    rope = qr.Rope.make(64)
+    plan = qr.KVPlan(None, torch.tensor([0, 3, 4], dtype=torch.int32, device="cuda"),
+                     torch.tensor([3, 9], dtype=torch.int32, device="cuda"), None, None)
+    want = qr.qr_rope(q[:4], q[:4, :1], rope, torch.tensor([0, 1, 2, 8], dtype=torch.int32, device="cuda"))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [qr.qr_rope(q, q[:, :1], rope, plan=plan)]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            got.append(qr.qr_rope(q, q[:, :1], rope, plan=plan))
+    for t in got[1]:
+        t.fill_(7.0)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for a in got:
+        for t, w in zip(a, want):
+            assert torch.equal(t[:4], w) and not t[4:].any()
