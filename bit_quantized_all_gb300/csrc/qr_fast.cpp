@@ -2,7 +2,7 @@
 // their checks, their outputs and the C ABI, as an extension module.
 //
 // A call of a few rows takes the GPU two to five microseconds and the interpreter
-// fifteen: checks of each tensor, the allocation of the outputs, the conversion of
+// eleven to twenty: checks of each tensor, the allocation of the outputs, the conversion of
 // twenty arguments.  Here the same checks are a few loads.  A function takes what
 // the Python function of that name would accept without a stream or an output of the
 // caller's, returns its outputs (or the C ABI's status, as an int, where that is not

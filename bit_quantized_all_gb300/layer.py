@@ -10,8 +10,8 @@ layouts and contracts; checks, streams and errors are as in ``serving.py``.
 
 Each call first offers its arguments to the compiled module ``_qr_fast``
 (``csrc/qr_fast.cpp``), which does the common form of it, with outputs of its
-own, in a third of the interpreter's time, and declines everything else: what
-the functions here then check, serve or refuse.
+own (which share an allocation), in a third of the interpreter's time or less, and
+declines everything else: what the functions here then check, serve or refuse.
 """
 from __future__ import annotations
 
