@@ -2,12 +2,12 @@
 // their checks, their outputs and the C ABI, as an extension module.
 //
 // A call of a few rows takes the GPU two to five microseconds and the interpreter
-// eleven to twenty: checks of each tensor, the allocation of the outputs, the conversion of
-// twenty arguments.  Here the same checks are a few loads.  A function takes what
-// the Python function of that name would accept without a stream or an output of the
-// caller's, returns its outputs (or the C ABI's status, as an int, where that is not
-// QR_OK), and None for anything else, which the Python function then handles or
-// refuses: no error is raised here.
+// eleven to twenty: checks of each tensor, the allocation of the outputs, the
+// conversion of twenty arguments.  Here the same checks are a few loads.  A function
+// takes what the Python function of that name would accept without a stream or an
+// output of the caller's, returns its outputs (or the C ABI's status, as an int,
+// where that is not QR_OK), and None for anything else, which the Python function
+// then handles or refuses: no error is raised here.
 #include <Python.h>
 
 #include <cmath>
@@ -15,7 +15,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
