@@ -1,9 +1,10 @@
 // qr_grid.cu -- launch-shape choice shared by every launcher: how many CTAs
 // a grid-stride kernel gets (from the SM count and the kernel's occupancy,
-// cached per device and kernel), and the per-context state every launcher
+// cached per device, kernel and threads), and the per-context state every launcher
 // relies on (kernel attributes, symbol addresses), cached per CUDA context.
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <utility>
 
 #include <cuda.h>
@@ -98,11 +99,12 @@ int grid_for(const void *kernel, int threads, long long tiles, int ctas, int wav
     int dev = 0;
     if ((*err = cudaGetDevice(&dev)) != cudaSuccess) return 0;
     static std::mutex mu;
-    static std::map<std::pair<int, const void *>, int> resident;  // (device, kernel) -> CTAs per wave
+    // (device, kernel, threads per CTA, which some kernels take by the width of a row) -> CTAs per wave
+    static std::map<std::tuple<int, const void *, int>, int> resident;
     int wave = 0;
     {
         std::lock_guard<std::mutex> lock(mu);
-        auto it = resident.find({dev, kernel});
+        auto it = resident.find({dev, kernel, threads});
         if (it != resident.end()) wave = it->second;
     }
     if (wave == 0) {
@@ -112,7 +114,7 @@ int grid_for(const void *kernel, int threads, long long tiles, int ctas, int wav
             return 0;
         wave = sms * (per_sm > 0 ? per_sm : 1);
         std::lock_guard<std::mutex> lock(mu);
-        resident[{dev, kernel}] = wave;
+        resident[{dev, kernel, threads}] = wave;
     }
     const long long want = static_cast<long long>(wave) * (waves > 0 ? waves : 1);
     return static_cast<int>(tiles < want ? tiles : want);
