@@ -415,8 +415,11 @@ class Rope:
         # turns a position times 2^64: below 2^63 in magnitude, exact but for the division's rounding
         turns = [int(t) for t in np.rint(f / (2 * math.pi) * 2.0 ** 64)]
         self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
-        self.layout, self.factor, self.rot_dim, self.device = layout, float(factor), 2 * f.size, self.turns.device
-        self.interleaved, self.address = layout == "interleaved", self.turns.data_ptr()
+        self.layout, self.factor, self.rot_dim, self.interleaved = layout, float(factor), 2 * f.size, layout == "interleaved"
+
+    # (of the tensor: a copy of the table has another one)
+    address = property(lambda self: self.turns.data_ptr())
+    device = property(lambda self: self.turns.device)
 
     @classmethod
     def make(cls, rot_dim: int, base: float = 10000.0, layout: str = "half", device="cuda", **scaling) -> "Rope":
