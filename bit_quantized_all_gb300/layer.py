@@ -66,6 +66,14 @@ def _fast():
     return _F
 
 
+_MOST = 2 ** 31 - 1  # of a size that the C ABI takes as an int: ctypes would pass a larger one's low bits
+
+
+def _sizes(what: str, *sizes: int) -> None:
+    if max(sizes) > _MOST:
+        raise ValueError(f"{what}: a size of {max(sizes)} is beyond {_MOST}")
+
+
 def _rows_of(t, what: str, shape, dtype, device: torch.device) -> tuple[int, int]:
     """(address, row stride) of a matrix of this shape and dtype on ``device``."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device.index:
@@ -149,6 +157,7 @@ def qr_q8_quantize(x: torch.Tensor, out: Q8Rows | None = None, stream=None) -> Q
     _matrix(x, "x")
     dt = _dtype_code(x, "x")
     tokens, cols = x.shape
+    _sizes("qr_q8_quantize", cols)
     dev = x.device
     out = _rows8_out(out, tokens, cols, dev, "qr_q8_quantize")
     if tokens and cols:
@@ -169,6 +178,7 @@ def _norm(what, x, weight, eps, residual, residual_out, out, eight):
     dt = _dtype_code(x, "x")
     shape, dtype, dev = x.shape, x.dtype, x.device
     tokens, cols = shape
+    _sizes(what, cols)
     wide = isinstance(weight, torch.Tensor) and weight.dtype is torch.float32
     if not ((wide or isinstance(weight, torch.Tensor) and weight.dtype is dtype) and weight.shape == (cols,)
             and weight.get_device() == dev.index and weight.is_contiguous()):
@@ -259,7 +269,7 @@ class W8Weight:
 
 
 def qr_w8_bytes(rows: int, cols: int) -> int:
-    return int(_lib().qr_w8_bytes(rows, cols))
+    return int(_lib().qr_w8_bytes(rows, cols)) if max(rows, cols) <= _MOST else 0
 
 
 def _new_w8(rows: int, cols: int, device) -> W8Weight:
@@ -297,7 +307,7 @@ def qr_w8_quantize(w: torch.Tensor, stream=None) -> W8Weight:
 
 
 def qr_w8_matmul_workspace_bytes(tokens: int, cols: int) -> int:
-    return int(_lib().qr_w8_matmul_workspace_bytes(tokens, cols))
+    return int(_lib().qr_w8_matmul_workspace_bytes(tokens, cols)) if max(tokens, cols) <= _MOST else 0
 
 
 def qr_w8_matmul_workspace(tokens: int, weight: W8Weight) -> torch.Tensor:
@@ -471,10 +481,12 @@ def qr_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope, positions: torc
     dt = _dtype_code(q, "q")
     shape, dtype, dev = q.shape, q.dtype, q.device
     tokens, q_heads, dim = shape
+    _sizes("qr_rope", q_heads, dim)
     k_in, k_heads = (0, 0, 0), 0
     if k is not None:
         k_heads = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
         k_in = _heads(k, "k", (tokens, k_heads, dim), dtype, dev)
+        _sizes("qr_rope", k_heads)
     if rope.rot_dim > dim:
         raise ValueError(f"the table rotates {rope.rot_dim} values of a head, which has {dim}")
     if rope.device != dev:
@@ -489,6 +501,7 @@ def qr_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope, positions: torc
         new = torch.empty
     else:
         requests = plan.kv_lens.numel()
+        _sizes("qr_rope", requests)
         _int_tensor(plan.kv_lens, "plan.kv_lens", torch.int32)
         _int_tensor(plan.q_offsets, "plan.q_offsets", torch.int32, (requests + 1,))
         _on(dev, "qr_rope", plan.kv_lens, plan.q_offsets)
