@@ -99,7 +99,7 @@ class Q8Rows:
         _matrix(codes, "codes")
         if codes.dtype != torch.int8:
             raise TypeError(f"codes must be torch.int8, got {codes.dtype}")
-        if codes.data_ptr() % 16 or (codes.shape[0] > 1 and codes.stride(0) % 16):
+        if codes.numel() and (codes.data_ptr() % 16 or (codes.shape[0] > 1 and codes.stride(0) % 16)):
             raise ValueError("codes: every row must begin on a 16-byte boundary")
         _int_tensor(scales, "scales", torch.float32, (codes.shape[0],))
         _same_device([codes, scales], "Q8Rows")
