@@ -521,6 +521,8 @@ def qr_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope, positions: torc
         q_at = q_in if q_out is q else _heads(q_out, "out's q", shape, dtype, dev)
         if k is not None:
             k_at = k_in if k_out is k else _heads(k_out, "out's k", (tokens, k_heads, dim), dtype, dev)
+    if not q_heads:  # (the keys alone)
+        q_in, q_heads, q_at, k_heads = k_in, k_heads, k_at, 0
     if tokens and q_heads:
         if not k_heads:
             k_in = k_at = (0, 0, 0)
