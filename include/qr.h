@@ -828,8 +828,9 @@ qr_status_t qr_w8_matmul(qr_dtype_t dtype, int64_t tokens, const int8_t *x, int6
  *   (a c - b s, b c + a s),  c = factor * cos(angle),  s = factor * sin(angle),
  *   angle = 2 pi * position * turns[j] / 2^64,
  * in fp32, rounded once; turns[j] (device) is the pair's frequency in turns a
- * position times 2^64, so that the product, which wraps at whole turns, keeps
- * every bit at any position.  Values from rot_dim on are copied.  head_dim
+ * position times 2^64, so that the product, which wraps at whole turns, is exact
+ * at any position; the angle, up to half a turn either way, is that product with
+ * at most two roundings to fp32.  Values from rot_dim on are copied.  head_dim
  * and rot_dim even, 2 <= rot_dim <= head_dim <= 1024.
  * Positions are positions[token] (device int32, any sign) or, where that is
  * NULL, those of a step's plan: token t of request r (q_offsets[r] <= t <
