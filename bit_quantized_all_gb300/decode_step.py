@@ -20,8 +20,8 @@ from __future__ import annotations
 import torch
 
 from . import (KVCache, KVPlan, Rope, W4Weight, W8Weight, qr_allreduce, qr_kv_append, qr_kv_attention,
-               qr_kv_attention_workspace, qr_kv_plan, qr_rms_norm_q8, qr_rope, qr_w4_matvec, qr_w8_matmul,
-               qr_w8_matmul_workspace)
+               qr_kv_attention_workspace, qr_kv_attention_workspace_bytes, qr_kv_plan, qr_rms_norm_q8, qr_rope,
+               qr_w4_matvec, qr_w8_matmul, qr_w8_matmul_workspace)
 
 
 class TPAttentionLayer:
@@ -116,6 +116,16 @@ class TPAttentionBlock:
             raise ValueError(f"a projection of {rows} rows holds no heads of {dim} for {kv_heads} key heads")
         if any(w.cols != self.q_heads * dim for w in layer.weights):
             raise ValueError(f"the layer's weights must have {self.q_heads * dim} columns")
+        if any(w.rows != layer.weights[0].rows for w in layer.weights):
+            raise ValueError("the layer's weights must have the same rows")
+        # what a step would refuse only after it has written the residual
+        if qr_kv_attention_workspace_bytes(1, 1, self.q_heads, kv_heads, dim) == 0:
+            raise ValueError(f"no attention of {self.q_heads} heads of {dim} over {kv_heads} key heads")
+        if rope.rot_dim > dim:
+            raise ValueError(f"the table rotates {rope.rot_dim} values of a head, which has {dim}")
+        dev = layer.caches[0].device
+        if any(d != dev for d in (norm_weight.device, rope.device, *(w.packed.device for w in (*qkv, *layer.weights)))):
+            raise ValueError(f"every tensor must be on {dev}")
         self.norm_weight, self.qkv, self.rope, self.layer, self.eps = norm_weight, qkv, rope, layer, eps
         self.workspace, self.workspace_tokens = None, 0
 
@@ -124,6 +134,8 @@ class TPAttentionBlock:
         the last one, ``x`` [tokens, hidden], which is added to ``residual`` in
         place.  ``new_lens``, ``max_q`` and what is raised (before ``residual``
         or a cache is written) as ``TPAttentionLayer.step``."""
+        if max_q < 1:
+            raise ValueError(f"max_q must be at least 1, got {max_q}")
         tokens = x.shape[0]
         plan, counts = self.layer._plan(new_lens, tokens)
         rows = qr_rms_norm_q8(x, self.norm_weight, self.eps, residual)
