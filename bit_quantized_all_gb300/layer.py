@@ -12,11 +12,13 @@ Each call first offers its arguments to the compiled module ``_qr_fast``
 (``csrc/qr_fast.cpp``), which does the common form of it, with outputs of its
 own (which share an allocation), in a third of the interpreter's time or less, and
 declines everything else: what the functions here then check, serve or refuse.
+Where that module is missing, they do it all, after a warning.
 """
 from __future__ import annotations
 
 import ctypes
 import math
+import warnings
 
 import numpy as np
 import torch
@@ -54,11 +56,27 @@ def _lib():
     return _L
 
 
+class _Interpreted:
+    """Stands for the compiled module where there is none: it declines every call."""
+
+    @staticmethod
+    def _declines(*args):
+        return None
+
+    quantize = norm = rope = matmul = _declines
+
+
 def _fast():
     global _F
     if _F is None:
         L = _lib()
-        from . import _qr_fast
+        try:
+            from . import _qr_fast
+        except ImportError as e:
+            warnings.warn(f"the calls of layer.py run without the compiled module _qr_fast, their host time some three "
+                          f"times as long ({e})", RuntimeWarning, stacklevel=3)
+            _F = _Interpreted()
+            return _F
         _qr_fast.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value
                         for name in ("qr_q8_quantize", "qr_rms_norm", "qr_rms_norm_q8", "qr_rope", "qr_w8_matmul",
                                      "qr_w8_matmul_workspace_bytes")))
