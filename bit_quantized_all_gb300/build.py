@@ -4,7 +4,8 @@ Each translation unit under csrc/ compiles in parallel; the objects link into
 ``libqr.so`` next to this file with the CUDA runtime linked statically and
 every symbol hidden except the ``qr_*`` entry points of include/qr.h.
 csrc/qr_fast.cpp becomes the extension module ``_qr_fast.so`` beside it, the
-compiled form of the calls in layer.py.
+compiled form of the calls in layer.py, where the interpreter's and torch's headers
+are there; without them the library is built all the same, after a warning.
 """
 from __future__ import annotations
 
@@ -15,12 +16,14 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libqr.so")
 FAST_PATH = os.path.join(HERE, "_qr_fast.so")  # csrc/qr_fast.cpp, an extension module
+FAST_FAILED = os.path.join(OBJ_DIR, "qr_fast.failed")  # why it could not be built
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["qr_capi.cu", "qr_grid.cu", "qr_encode.cu", "qr_decode.cu", "qr_reduce.cu", "qr_allreduce.cu",
@@ -50,17 +53,45 @@ def _nvcc() -> str:
 
 
 def _deps() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")]
     files.append(os.path.join(INCLUDE, "qr.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(FAST_PATH):
+def _older(made: str, sources: list[str]) -> bool:
+    if not os.path.exists(made):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(FAST_PATH))
-    return any(os.path.getmtime(f) > t for f in _deps())
+    t = os.path.getmtime(made)
+    return any(os.path.getmtime(f) > t for f in sources)
+
+
+def _stale() -> bool:
+    return _older(LIB_PATH, _deps())
+
+
+def _fast_stale() -> bool:
+    """Whether the extension module is to be built: not where it is up to date, nor
+    where it could not be built from these sources (which build(force=True) tries again)."""
+    sources = [os.path.join(CSRC, "qr_fast.cpp"), os.path.join(INCLUDE, "qr.h"), os.path.abspath(__file__)]
+    return _older(FAST_PATH, sources) and _older(FAST_FAILED, sources)
+
+
+def _try_fast() -> None:
+    """The extension module where it can be built; the calls in layer.py run without
+    it too, so what is missing for it (the interpreter's headers, say) stops nothing else."""
+    try:
+        _build_fast()
+    except (RuntimeError, OSError) as e:
+        if os.path.exists(FAST_PATH):  # of other sources
+            os.remove(FAST_PATH)
+        with open(FAST_FAILED, "w") as f:
+            f.write(f"{e}\n")
+        warnings.warn(f"{os.path.basename(FAST_PATH)} could not be built: the calls of layer.py run without it ({e})",
+                      RuntimeWarning, stacklevel=2)
+    else:
+        if os.path.exists(FAST_FAILED):
+            os.remove(FAST_FAILED)
 
 
 def _build_fast() -> None:
@@ -87,20 +118,24 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     workers) take turns on a lock file, and each re-checks whether the
     library is still stale once it holds the lock, so the objects are never
     written by two compilers at once."""
-    if not force and not ptxas_info and not _stale():
+    if not force and not ptxas_info and not _stale() and not _fast_stale():
         return LIB_PATH
     os.makedirs(OBJ_DIR, exist_ok=True)
     with open(os.path.join(OBJ_DIR, ".lock"), "w") as lock:
         fcntl.flock(lock, fcntl.LOCK_EX)
         try:
-            if not force and not ptxas_info and not _stale():
-                return LIB_PATH
-            return _build_locked(verbose, ptxas_info)
+            with cf.ThreadPoolExecutor(max_workers=1) as ex:
+                fast = ex.submit(_try_fast) if force or _fast_stale() else None
+                if force or ptxas_info or _stale():
+                    _build_locked(verbose, ptxas_info)
+                if fast is not None:
+                    fast.result()
+            return LIB_PATH
         finally:
             fcntl.flock(lock, fcntl.LOCK_UN)
 
 
-def _build_locked(verbose: bool, ptxas_info: bool) -> str:
+def _build_locked(verbose: bool, ptxas_info: bool) -> None:
     nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
@@ -112,10 +147,8 @@ def _build_locked(verbose: bool, ptxas_info: bool) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
         return obj, p.stdout + p.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        fast = ex.submit(_build_fast)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        fast.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log.strip():
@@ -126,7 +159,6 @@ def _build_locked(verbose: bool, ptxas_info: bool) -> str:
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":
