@@ -3,7 +3,7 @@
 Each translation unit under csrc/ compiles in parallel; the objects link into
 ``libqr.so`` next to this file with the CUDA runtime linked statically and
 every symbol hidden except the ``qr_*`` entry points of include/qr.h.
-csrc/qr_fast.cpp becomes the extension module ``_qr_fast.so`` beside it, the
+csrc/qr_fast.cpp becomes the extension module ``_qr_fast`` beside it, the
 compiled form of the calls in layer.py, where the interpreter's and torch's headers
 are there; without them the library is built all the same, after a warning.
 """
@@ -18,12 +18,16 @@ import sys
 import sysconfig
 import warnings
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libqr.so")
-FAST_PATH = os.path.join(HERE, "_qr_fast.so")  # csrc/qr_fast.cpp, an extension module
-FAST_FAILED = os.path.join(OBJ_DIR, "qr_fast.failed")  # why it could not be built
+# csrc/qr_fast.cpp, an extension module; it uses inline parts of torch's classes, so that
+# one built for another torch or interpreter, which this name is not, must not be loaded
+FAST_PATH = os.path.join(HERE, f"_qr_fast-torch{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
+FAST_FAILED = os.path.join(OBJ_DIR, os.path.basename(FAST_PATH) + ".failed")  # why it could not be built
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["qr_capi.cu", "qr_grid.cu", "qr_encode.cu", "qr_decode.cu", "qr_reduce.cu", "qr_allreduce.cu",
@@ -96,7 +100,6 @@ def _try_fast() -> None:
 
 def _build_fast() -> None:
     """The extension module, against the running interpreter's and torch's headers."""
-    import torch
     root = os.path.dirname(torch.__file__)
     includes = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
                 os.path.join(root, "include", "torch", "csrc", "api", "include"),

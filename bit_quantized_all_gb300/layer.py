@@ -17,6 +17,7 @@ Where that module is missing, they do it all, after a warning.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import warnings
 
@@ -24,6 +25,7 @@ import numpy as np
 import torch
 
 from . import _check, _cuda_contig, _dtype_code, _same_device, lib
+from .build import FAST_PATH
 from .serving import KVPlan, _as_current, _current, _int_tensor, _matrix, _on
 
 _L = None  # the library, these calls' signatures set
@@ -71,7 +73,9 @@ def _fast():
     if _F is None:
         L = _lib()
         try:
-            from . import _qr_fast
+            spec = importlib.util.spec_from_file_location(__package__ + "._qr_fast", FAST_PATH)
+            _qr_fast = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(_qr_fast)
         except ImportError as e:
             warnings.warn(f"the calls of layer.py run without the compiled module _qr_fast, their host time some three "
                           f"times as long ({e})", RuntimeWarning, stacklevel=3)
