@@ -200,6 +200,15 @@ QR_EXPORT qr_status_t qr_rope(qr_dtype_t dtype, int64_t tokens, int head_dim, in
     auto rows = [&](const Operand &o) {
         return Rows{o.p, tokens, o.token * 2, ((o.heads - 1) * (o.heads > 1 ? o.head : 0) + head_dim) * 2};
     };
+    // ... or the heads of one lie between those of the other (queries and keys of
+    // a projection whose heads alternate)
+    auto heads_apart = [&](const Operand &a, const Operand &b) {
+        const int64_t s = a.head * 2, width = head_dim * 2ll;
+        if (a.heads < 2 || b.heads < 2 || a.head != b.head || (tokens > 1 && (a.token % a.head || b.token % a.head))) return false;
+        const int64_t d = ((int64_t(reinterpret_cast<uintptr_t>(b.p)) - int64_t(reinterpret_cast<uintptr_t>(a.p))) % s + s) % s;
+        return d >= width && s - d >= width;
+    };
+    auto clear = [&](const Operand &a, const Operand &b) { return apart(rows(a), rows(b)) || heads_apart(a, b); };
     auto identical = [&](const Operand &a, const Operand &b) {
         return a.p == b.p && (tokens == 1 || a.token == b.token) && (a.heads == 1 || a.head == b.head);
     };
@@ -208,11 +217,11 @@ QR_EXPORT qr_status_t qr_rope(qr_dtype_t dtype, int64_t tokens, int head_dim, in
                             flat(positions ? nullptr : kv_lens, size_t(requests) * 4)};
     for (int i = 0; i < both; ++i) {
         for (int j = 0; j < both; ++j)
-            if (!apart(rows(out[i]), rows(in[j])) && !(i == j && identical(out[i], in[j]))) return QR_ERR_INVALID_ARG;
+            if (!clear(out[i], in[j]) && !(i == j && identical(out[i], in[j]))) return QR_ERR_INVALID_ARG;
         for (const Rows &t : tables)
             if (!apart(rows(out[i]), t)) return QR_ERR_INVALID_ARG;
     }
-    if (both == 2 && !apart(rows(out[0]), rows(out[1]))) return QR_ERR_INVALID_ARG;
+    if (both == 2 && !clear(out[0], out[1])) return QR_ERR_INVALID_ARG;
     RopeArgs a = {};
     for (int i = 0; i < both; ++i) {
         a.in[i] = static_cast<const uint16_t *>(in[i].p);
