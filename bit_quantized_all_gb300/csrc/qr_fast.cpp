@@ -10,11 +10,13 @@
 // then handles or refuses: no error is raised here.
 #include <Python.h>
 
+#include <array>
 #include <cmath>
-#include <string>
 
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <c10/core/Allocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
@@ -54,8 +56,12 @@ bool list_of(const at::Tensor &t, at::ScalarType type, int64_t n, const at::Devi
 }
 bool heads(const at::Tensor &t) { return t.dim() == 3 && (t.size(2) < 2 || t.stride(2) == 1); }
 
-at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const at::Device &device) {
-    return at::empty(sizes, at::TensorOptions().dtype(type).device(device));
+// A new tensor on the current stream; without the dispatcher, which takes longer than
+// the allocator.
+at::Tensor empty(at::IntArrayRef sizes, at::IntArrayRef strides, at::ScalarType type, const at::Device &device) {
+    const c10::cuda::CUDAGuard on(device);
+    return at::detail::empty_strided_generic(sizes, strides, c10::GetAllocator(at::kCUDA),
+                                             c10::DispatchKeySet(c10::DispatchKey::CUDA), type);
 }
 qr_stream_t stream_on(const at::Device &d) {
     return reinterpret_cast<qr_stream_t>(c10::cuda::getCurrentCUDAStream(d.index()).stream());
@@ -63,23 +69,21 @@ qr_stream_t stream_on(const at::Device &d) {
 
 // A tensor in `of`'s memory, `offset` of its values from the start (a view takes
 // the dispatcher a microsecond).
-at::Tensor inside(const at::Tensor &of, at::ScalarType type, int64_t offset, at::IntArrayRef sizes, at::IntArrayRef strides) {
-    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(of.storage()), of.key_set(), c10::scalarTypeToTypeMeta(type));
+at::Tensor inside(const at::Tensor &of, int64_t offset, at::IntArrayRef sizes, at::IntArrayRef strides) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(of.storage()), of.key_set(), of.dtype());
     t.unsafeGetTensorImpl()->set_storage_offset(offset);
     t.unsafeGetTensorImpl()->set_sizes_and_strides(sizes, strides);
     return t;
 }
 
-// (codes, scales, pitch): what a Q8Rows holds, the scales behind the codes in one
-// allocation (two take 0.8 us more).
+// (codes, scales, pitch): what a Q8Rows holds.
 struct Rows8 {
     at::Tensor codes, scales;
     int64_t pitch;
 
     Rows8(int64_t tokens, int64_t cols, const at::Device &d) : pitch((cols + 15) / 16 * 16) {
-        const at::Tensor all = empty({tokens * (pitch + 4)}, at::kChar, d);
-        codes = inside(all, at::kChar, 0, {tokens, cols}, {pitch, 1});
-        scales = inside(all, at::kFloat, tokens * pitch / 4, {tokens}, {1});
+        codes = empty({tokens, cols}, {pitch, 1}, at::kChar, d);
+        scales = empty({tokens}, {1}, at::kFloat, d);
     }
     int8_t *at_codes() const { return static_cast<int8_t *>(codes.data_ptr()); }
     float *at_scales() const { return static_cast<float *>(scales.data_ptr()); }
@@ -130,7 +134,7 @@ PyObject *norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
                                        stream_on(device));
         return status ? PyLong_FromLong(status) : y.wrap();
     }
-    const at::Tensor y = empty(x->sizes(), x->scalar_type(), device);
+    const at::Tensor y = empty(x->sizes(), {x->size(1), 1}, x->scalar_type(), device);
     const int status = rms_norm(dt, x->size(0), cols, x->data_ptr(), x->stride(0), at_r, r_row, at_ro, ro_row, w->data_ptr(),
                                 wide, static_cast<float>(eps), y.data_ptr(), cols, stream_on(device));
     return status ? PyLong_FromLong(status) : THPVariable_Wrap(y);
@@ -169,18 +173,21 @@ PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
         q_out = *q;
         if (k) k_out = *k;
     } else {
-        // one allocation, k's from a 16-byte boundary on
-        const auto options = at::TensorOptions().dtype(q->scalar_type()).device(device);
-        const int64_t k_at = (q->numel() + 7) / 8 * 8, n = k ? k_at + k->numel() : q->numel();
-        // (tokens that a plan leaves out: not what the memory held)
-        const at::Tensor all = at::empty({n}, options);
-        if (!pos && cudaMemsetAsync(all.data_ptr(), 0, static_cast<size_t>(n) * 2, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-            return PyLong_FromLong(QR_ERR_CUDA);
-        auto part = [&](const at::Tensor &x, int64_t from) {
-            return inside(all, q->scalar_type(), from, x.sizes(), {x.size(1) * dim, dim, 1});
-        };
-        q_out = part(*q, 0);
-        if (k) k_out = part(*k, k_at);
+        auto strides = [&](const at::Tensor &x) { return std::array<int64_t, 3>{x.size(1) * dim, dim, 1}; };
+        if (pos) {
+            q_out = empty(q->sizes(), strides(*q), q->scalar_type(), device);
+            if (k) k_out = empty(k->sizes(), strides(*k), k->scalar_type(), device);
+        } else {
+            // tokens that a plan leaves out: not what the memory held.  One memset of one
+            // allocation, k's part from a 16-byte boundary on (in a graph two memsets take
+            // 4.5 us more)
+            const int64_t k_at = (q->numel() + 7) / 8 * 8, n = k ? k_at + k->numel() : q->numel();
+            const at::Tensor all = empty({n}, {1}, q->scalar_type(), device);
+            if (cudaMemsetAsync(all.data_ptr(), 0, static_cast<size_t>(n) * 2, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+                return PyLong_FromLong(QR_ERR_CUDA);
+            q_out = inside(all, 0, q->sizes(), strides(*q));
+            if (k) k_out = inside(all, k_at, k->sizes(), strides(*k));
+        }
     }
     auto data = [](const at::Tensor *t) { return t ? static_cast<const int32_t *>(t->data_ptr()) : nullptr; };
     const int status = rope_call(
@@ -212,11 +219,11 @@ PyObject *matmul(PyObject *, PyObject *const *args, Py_ssize_t n) {
         ws = on_gpu(args[6]);
         if (!ws || ws->scalar_type() != at::kByte || !ws->is_contiguous() || ws->device() != device) return none();
     } else if (tokens > 16) {
-        own = empty({static_cast<int64_t>(w8_workspace_bytes(tokens, static_cast<int>(cols)))}, at::kByte, device);
+        own = empty({static_cast<int64_t>(w8_workspace_bytes(tokens, static_cast<int>(cols)))}, {1}, at::kByte, device);
         ws = &own;
     }
     const at::ScalarType type = args[5] == Py_True ? at::kBFloat16 : at::kHalf;
-    const at::Tensor y = empty({tokens, rows}, type, device);
+    const at::Tensor y = empty({tokens, rows}, {rows, 1}, type, device);
     const int status = w8_matmul(type_of(type), tokens, static_cast<const int8_t *>(codes->data_ptr()), codes->stride(0),
                                  static_cast<const float *>(scales->data_ptr()), static_cast<int>(rows), static_cast<int>(cols),
                                  packed->data_ptr(), y.data_ptr(), rows, ws ? ws->data_ptr() : nullptr,

@@ -10,8 +10,8 @@ layouts and contracts; checks, streams and errors are as in ``serving.py``.
 
 Each call first offers its arguments to the compiled module ``_qr_fast``
 (``csrc/qr_fast.cpp``), which does the common form of it, with outputs of its
-own (which share an allocation), in a third of the interpreter's time or less, and
-declines everything else: what the functions here then check, serve or refuse.
+own, in a third of the interpreter's time or less, and declines everything else:
+what the functions here then check, serve or refuse.
 Where that module is missing, they do it all, after a warning.
 """
 from __future__ import annotations
@@ -486,7 +486,9 @@ def qr_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope, positions: torc
     """Queries and keys (fp16/bf16 [tokens, heads, head_dim]; k may be None)
     turned by their positions: ``positions`` (int32 [tokens]), or those of a
     step's ``plan`` (tokens past its last one are left alone in ``out``).
-    Returns (q, k), new or ``out``; ``out=(q, k)`` turns them in place."""
+    Returns (q, k), new or ``out``; ``out=(q, k)`` turns them in place.  New
+    outputs of a plan, in which the tokens left out are zeros, may share an
+    allocation."""
     in_place = out is not None and out[0] is q and out[1] is k
     if stream is None and (out is None or in_place) and (positions is None) != (plan is None):
         got = (_F or _fast()).rope(q, k, rope.turns, rope.rot_dim, rope.interleaved, rope.factor, positions,
