@@ -347,7 +347,8 @@ static cudaError_t run_norm(const NormArgs &a, cudaStream_t s) {
         if (threads(2) <= 512) return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 2, 512, true>, threads(2), 1);
     }
     if (threads(4) <= 512) return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 4, 512, true>, threads(4), 1);
-    return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 4, 1024, false>, threads(4), 1);
+    if constexpr (!SHIFT) return launch(norm_kernel<DT, W, EIGHT, false, false, 4, 1024, false>, threads(4), 1);
+    return cudaErrorInvalidValue;  // (pick_norm sends none)
 }
 
 template <int DT, int W, bool EIGHT>
@@ -362,7 +363,11 @@ static cudaError_t pick_norm(const NormArgs &a, cudaStream_t s) {
                       (EIGHT || alike(a.y, a.y_row));
     const bool whole = a.cols % 8 == 0 && at(a.x) == 0 && (a.tokens == 1 || a.x_row % 8 == 0) && at(a.weight) == 0;
     if (like && whole && a.cols <= 32768) return run_norm<DT, W, EIGHT, false>(a, s);
-    if (like && a.cols <= 31 * 1024 - 8) return run_norm<DT, W, EIGHT, true>(a, s);
+    // Shifted rows as far as 512 threads hold them with the next row on its way.  Without
+    // that, 1024 threads lost to the kernel that reads rows twice at every size (in 8 bits
+    // with the residual 8192 x 20481 598 us, read twice 356; 16 x 16401 9.8 and 6.5).
+    constexpr int kShifted = W == 0 ? 31 * 1024 : (EIGHT ? 31 : 32) * 512;
+    if (like && a.cols <= kShifted - 8) return run_norm<DT, W, EIGHT, true>(a, s);
     cudaError_t err = cudaSuccess;
     const int grid = grid_for(reinterpret_cast<const void *>(norm_long_kernel<DT, W, EIGHT>), kNormLongThreads, a.tokens, 0, 1, &err);
     return grid <= 0 ? err : launch_chained(norm_long_kernel<DT, W, EIGHT>, grid, kNormLongThreads, 0, s, a);
