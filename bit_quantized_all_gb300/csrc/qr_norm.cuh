@@ -7,11 +7,12 @@
 // factor of the whole row, so that they come from h w, and rs goes into the
 // scale; both reductions share one barrier.
 //
-// What bounds it: HBM (32768 x 8192 in 8 bits with the residual 272 us, 6.9 TB/s, a
-// plain copy's rate; 8192 x 20480 without a norm 74 us, 6.8 TB/s, with one CTA an SM
-// rather than two 88); for few rows the launch and two round trips (16 x
-// 8192 2.6 us); for a few thousand rows that do not begin on 16-byte boundaries the
-// issue of a row's instructions (2049 x 5123 in 16 bits 14 us, 2049 x 5120 10).
+// What bounds it: HBM (32768 x 8192 in 8 bits with the residual 272 to 276 us, 6.8 to
+// 6.9 TB/s, a plain copy's rate; 8192 x 20480 without a norm 74 us, 6.8 TB/s); for few
+// rows the launch and two round trips (16 x 8192 2.4 us); for a few thousand rows that do
+// not begin on 16-byte boundaries a CTA's rows one after the other, load, barrier and
+// store, with more instructions a piece (2049 x 5123 in 16 bits 14 us, 2049 x 5120 10; 55%
+// of the issue slots and 22 warps an SM in use).
 #pragma once
 
 #include "qr_device.cuh"
@@ -335,17 +336,37 @@ static cudaError_t run_norm(const NormArgs &a, cudaStream_t s) {
         if (SHIFT && rows == 1 && grid < units) grid &= ~7;  // (a CTA's rows lie alike)
         return grid <= 0 ? err : launch_chained(kern, grid, n, 0, s, a);
     };
+    // Times in us of bf16 rows: in 8 bits with the residual / norm in 16 bits / 8 bits
+    // without a norm.
+    //
+    // A warp a row from eight rows an SM on (2432 x 1024: 3.2 / 2.7 / 2.4, a CTA a row 4.3 /
+    // 3.8 / 2.8; 1300 x 1024 alike; 608 x 1024: 2.4 / 2.0 / 1.7 and 2.1 / 2.0 / 1.6).
     if (threads(4) <= 32 && a.tokens > 8 * sms) return launch(norm_kernel<DT, W, EIGHT, SHIFT, true, 4, 256, true>, 256, 8);
-    if (threads(1) <= 1024 && a.tokens <= 2 * sms)
+    // Few rows: one piece a thread, the fewest loads in turn, where two CTAs an SM hold
+    // 640 threads each (16 x 5120: 2.0 / 1.8 / 1.5, four pieces a thread 2.1 / 2.0 / 1.6; 304 x
+    // 5120: 3.2 / 2.8 / 1.9 and 3.3 / 2.6 / 1.9; past that 16 x 8192: 2.5 / 2.2 / 1.7 and 2.3 / 2.1 /
+    // 1.7; 304 x 5632: 3.4 / 2.9 / 2.0 and 2.8 / 2.4 / 1.9), and wherever shifts make a piece
+    // dear (16 x 7001: 3.5 / 2.7 / 2.0 and 5.8 / 3.4 / 2.1).  From two rows an SM on the other
+    // form has the next row on its way (456 x 5120: 4.2 / 3.6 / 2.7 and 3.1 / 2.7 / 2.3).
+    if (threads(1) <= (SHIFT ? 1024 : 640) && a.tokens <= 2 * sms)
         return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 1, 1024, false>, threads(1), 1);
+    // Without a weight a row needs fewer registers: eight pieces a thread keep long rows
+    // ahead (8192 x 24576: 98, four pieces of 1024 threads 127).  Up to 320 threads two such
+    // CTAs fit an SM, with 96 registers a thread (8192 x 20480: 75, one CTA an SM 89).  (Up to
+    // 384 with 80 registers: 8192 x 22528 81 for 94, 24576 92 for 98, not built.)
     if constexpr (W == 0) {
         if (threads(4) > 512)
             return threads(8) <= 320 ? launch(norm_kernel<DT, 0, EIGHT, SHIFT, false, 8, 320, true>, threads(8), 1)
                                      : launch(norm_kernel<DT, 0, EIGHT, SHIFT, false, 8, 512, true>, threads(8), 1);
     }
+    // Shifted rows: two pieces a thread (2049 x 5123: 22.5 / 11.8 / -, four pieces 30.8 / 12.5;
+    // aligned rows alike or slower: 32768 x 8192 310 / 177 / - and 276 / 180).
     if constexpr (SHIFT) {
         if (threads(2) <= 512) return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 2, 512, true>, threads(2), 1);
     }
+    // Four pieces of up to 512 threads, the next row ahead (32768 x 8192: 276 / 180, 1024
+    // threads without it 311 / 183); longer rows: 1024 threads (8192 x 20480: 212 / 168, read
+    // twice 360 / 196).
     if (threads(4) <= 512) return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 4, 512, true>, threads(4), 1);
     if constexpr (!SHIFT) return launch(norm_kernel<DT, W, EIGHT, false, false, 4, 1024, false>, threads(4), 1);
     return cudaErrorInvalidValue;  // (pick_norm sends none)
