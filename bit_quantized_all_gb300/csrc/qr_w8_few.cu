@@ -1,5 +1,5 @@
 // qr_w8_few.cu -- y = x W^T for up to 16 rows of x and weights in 8 bits
-// (qr_w8_matmul); qr_w8.cu describes the packed order.
+// (qr_w8_matmul); W8Layout in qr_serving.h describes the packed order.
 //
 // y^T = W x^T on m16n8k16 with fp16 operands: 16 weight rows as M, 8 tokens as
 // N, both sides' codes as exact fp16 integers.  Which of an instruction's

@@ -1,5 +1,5 @@
 // qr_w8_tc.cu -- y = x W^T for 17 and more rows of x and weights in 8 bits, on
-// tcgen05 (qr_w8_matmul; qr_w8.cu describes the packed order).
+// tcgen05 (qr_w8_matmul; W8Layout in qr_serving.h describes the packed order).
 //
 // The fast integer products of this GPU are those of 16-bit floats: codes are
 // exact fp16 numbers, their products exact in fp32.  A first kernel writes x's
@@ -17,8 +17,8 @@
 // every time.
 //
 // What bounds it: with 256 tokens a tile the products (4096 tokens through 10240 x
-// 8192: 405 to 425 us as the clock goes under the power limit, 1.62 to 1.70 PFLOP/s;
-// 1024 tokens 106 us, the tensor pipe busy 82%); with fewer the weights' bytes, in
+// 8192: 405 to 436 us as the clock goes under the power limit, 1.58 to 1.70 PFLOP/s;
+// 1024 tokens 106 to 108 us, the tensor pipe busy 82%); with fewer the weights' bytes, in
 // the steady state, and around it the first kernel, the first loads' way and the
 // join, some 7 us (64 tokens 23 us, 3.7 TB/s; 129 through 20481 x 5123 37.6 us: the
 // two rings in shared memory hold too little of either operand for HBM's latency).
@@ -575,11 +575,12 @@ static cudaError_t pick_tokens(const W8Args &a, const W8Shares &p, uint8_t *work
 }
 
 // The tiles' tokens, equal shares of up to 128, 192 or 256, and the division of their
-// chunks: whole tiles, or even shares, whose divided tiles' parts are joined; by what
-// each takes, in microseconds.  A chunk is bound by its products or its hand-overs,
-// and weights that do not stay in L2 between tiles by HBM; a tile's results are
-// stored beside the next one's products where there are two accumulators; joining takes a launch, the parts' way to L2 and back, and some time
-// for each part of a tile.
+// chunks: a CTA for each tile where there are no more tiles than SMs, or even shares,
+// whose divided tiles' parts are joined; by what each takes, in microseconds.  A chunk is
+// bound by its products or its hand-overs, and weights that do not stay in L2 between
+// tiles by HBM; a tile's results are stored beside the next one's products where there
+// are two accumulators; joining takes a launch, the parts' way to L2 and back, and some
+// time for each part of a tile.
 static W8Shares w8_shares(const W8Args &a, int sms) {
     W8Shares best = {};
     double least = 0.0;

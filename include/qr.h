@@ -813,7 +813,9 @@ qr_status_t qr_w8_quantize(qr_dtype_t dtype, int rows, int cols, const void *w,
 /* y[t][n] = (sum_k x[t][k] w[n][k]) * x_scale[t] * w_scale[n], rounded once to
  * `dtype`: x rows in 8 bits (any codes -128..127) and 8-bit weights.  The
  * products are integers summed in fp32: no sum is rounded as long as
- * sum_k |x w| stays below 2^24.  Above 16 tokens the workspace
+ * sum_k |x w| stays below 2^24.  The scales are multiplied in fp32 from left to
+ * right: where sum * x_scale is beyond fp32 the result is infinite, whatever
+ * w_scale.  Above 16 tokens the workspace
  * (qr_w8_matmul_workspace_bytes, 16-byte aligned) is written and read; up to
  * 16 it may be NULL.  y: any row stride >= rows, 2-byte aligned. */
 size_t qr_w8_matmul_workspace_bytes(int64_t tokens, int cols); /* 0 if unsupported */
