@@ -134,7 +134,7 @@ class TPAttentionBlock:
         the last one, ``x`` [tokens, hidden], which is added to ``residual`` in
         place.  ``new_lens``, ``max_q`` and what is raised (before ``residual``
         or a cache is written) as ``TPAttentionLayer.step``."""
-        if max_q < 1:
+        if max_q is not None and max_q < 1:
             raise ValueError(f"max_q must be at least 1, got {max_q}")
         tokens = x.shape[0]
         plan, counts = self.layer._plan(new_lens, tokens)

@@ -16,14 +16,17 @@ def lib():
     qr.lib()
 
 
-def _refused(**bad):
-    dim = bad.pop("dim", 64)
-    hidden = bad.pop("hidden", (HIDDEN, HIDDEN))
+def _parts(dim=64, hidden=(HIDDEN, HIDDEN)):
     half = dict(dtype=torch.float16, device="cuda")
     out = [qr.qr_w4_quantize(torch.ones((n, HEADS * dim), **half)) for n in hidden]
     layer = TPAttentionLayer(out, KV, dim, requests=2, max_len=64, blocks=16)
     qkv = [qr.qr_w8_quantize(torch.ones(((HEADS + 2 * KV) * dim, HIDDEN), **half)) for _ in out]
-    ok = dict(norm_weight=torch.ones(HIDDEN, device="cuda"), qkv=qkv, rope=qr.Rope.make(8), layer=layer)
+    return dict(norm_weight=torch.ones(HIDDEN, device="cuda"), qkv=qkv, rope=qr.Rope.make(8), layer=layer)
+
+
+def _refused(**bad):
+    ok = _parts(**{name: bad.pop(name) for name in ("dim", "hidden") if name in bad})
+    layer = ok["layer"]
     x, residual = (torch.randn((4, HIDDEN), device="cuda").half() for _ in range(2))
     kept, max_q = residual.clone(), bad.pop("max_q", 2)
     with pytest.raises(ValueError):
@@ -53,3 +56,11 @@ def test_unlike_outputs():
 @pytest.mark.parametrize("max_q", [0, -1])
 def test_no_queries(max_q):
     _refused(max_q=max_q)
+
+
+def test_no_bound_on_the_queries():
+    """max_q None: all of the step's tokens, as qr_kv_attention takes it."""
+    x, residual = (torch.randn((4, HIDDEN), device="cuda").half() for _ in range(2))
+    new = torch.tensor([1, 3], dtype=torch.int32, device="cuda")
+    a, b = (TPAttentionBlock(**_parts()).step(x, residual.clone(), new, max_q) for max_q in (None, 4))
+    assert torch.equal(a, b)
