@@ -342,12 +342,12 @@ static cudaError_t run_norm(const NormArgs &a, cudaStream_t s) {
     // A warp a row from eight rows an SM on (2432 x 1024: 3.2 / 2.7 / 2.4, a CTA a row 4.3 /
     // 3.8 / 2.8; 1300 x 1024 alike; 608 x 1024: 2.4 / 2.0 / 1.7 and 2.1 / 2.0 / 1.6).
     if (threads(4) <= 32 && a.tokens > 8 * sms) return launch(norm_kernel<DT, W, EIGHT, SHIFT, true, 4, 256, true>, 256, 8);
-    // Few rows: one piece a thread, the fewest loads in turn, where two CTAs an SM hold
-    // 640 threads each (16 x 5120: 2.0 / 1.8 / 1.5, four pieces a thread 2.1 / 2.0 / 1.6; 304 x
-    // 5120: 3.2 / 2.8 / 1.9 and 3.3 / 2.6 / 1.9; past that 16 x 8192: 2.5 / 2.2 / 1.7 and 2.3 / 2.1 /
-    // 1.7; 304 x 5632: 3.4 / 2.9 / 2.0 and 2.8 / 2.4 / 1.9), and wherever shifts make a piece
-    // dear (16 x 7001: 3.5 / 2.7 / 2.0 and 5.8 / 3.4 / 2.1).  From two rows an SM on the other
-    // form has the next row on its way (456 x 5120: 4.2 / 3.6 / 2.7 and 3.1 / 2.7 / 2.3).
+    // Few rows: one piece a thread, the fewest loads in turn, up to 640 threads (16 x 5120:
+    // 2.0 / 1.8 / 1.5, four pieces a thread 2.1 / 2.0 / 1.6; 304 x 5120: 3.2 / 2.8 / 1.9 and 3.3 /
+    // 2.6 / 1.9; past that 16 x 8192: 2.5 / 2.2 / 1.7 and 2.3 / 2.1 / 1.7; 304 x 5632: 3.4 / 2.9 /
+    // 2.0 and 2.8 / 2.4 / 1.9), and wherever shifts make a piece dear (16 x 7001: 3.5 / 2.7 /
+    // 2.0 and 5.8 / 3.4 / 2.1).  From two rows an SM on the other form has the next row on its
+    // way (456 x 5120: 4.2 / 3.6 / 2.7 and 3.1 / 2.7 / 2.3).
     if (threads(1) <= (SHIFT ? 1024 : 640) && a.tokens <= 2 * sms)
         return launch(norm_kernel<DT, W, EIGHT, SHIFT, false, 1, 1024, false>, threads(1), 1);
     // Without a weight a row needs fewer registers: eight pieces a thread keep long rows
